@@ -13,6 +13,16 @@ device memory and the current stream; nothing is computed in Python.
                                                     # (= expert_gateup + expert_down)
     out, rw_sk = buf.combine(plan, y, rw_nvs)       # moonep_combine
 
+Around it, what a training step needs next (framework-side steps on the pages):
+`Buffer.route` / `route_bwd` (the router's choice, its weights and their
+gradient), `Buffer.combine_bwd` (the gradient of the weighted combine) and
+`orthogonalize` (the Muon optimiser's direction of the weight gradients):
+
+    topk, rw = buf.route(logits)                    # moonep_route
+    dy, drw = buf.combine_bwd(plan, dout, y, rw_nvs)  # moonep_combine_bwd
+    dlogits = buf.route_bwd(logits, topk, drw)      # moonep_route_bwd
+    direction = orthogonalize(grad_home)            # moonep_orthogonalize
+
 `SymmetricBuffer` is the README's [E+B,H,H'] weight (or fp32 gradient) buffer
 of one projection on virtual memory (moonep_symbuf_*): per-rank views whose
 rows [0,E) map every rank's home chunk, with the *_views methods addressing
@@ -27,7 +37,8 @@ import torch
 from . import _abi
 from ._abi import MoonepError, lib  # noqa: F401
 
-__all__ = ["Buffer", "Plan", "SymmetricBuffer", "MoonepError", "lib", "vmm_granularity"]
+__all__ = ["Buffer", "Plan", "SymmetricBuffer", "MoonepError", "lib", "vmm_granularity",
+           "orthogonalize", "orthogonalize_workspace"]
 
 
 def _stream():
@@ -48,6 +59,37 @@ def _dev_ptr(t, dtype, shape, name, nullable=False):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+_FLOATS = {torch.float32: _abi.F32, torch.bfloat16: _abi.BF16}
+
+
+def _float_type(t, name):
+    if t.dtype not in _FLOATS:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return _FLOATS[t.dtype]
+
+
+def _score(score):
+    if score not in _abi.SCORES:
+        raise ValueError(f"score: expected one of {sorted(_abi.SCORES)}, got {score!r}")
+    return _abi.SCORES[score]
+
+
+def _same_device(device, **tensors):
+    """The calls below launch on `device`: every tensor has to be there."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: expected device {device}, got {t.device}")
+
+
+def _apart(name, out, **inputs):
+    """`out` must not share memory with any of `inputs`."""
+    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+    o = span(out)
+    for n, t in inputs.items():
+        if t is not None and o[0] < span(t)[1] and span(t)[0] < o[1]:
+            raise ValueError(f"{name} must not overlap {n}")
 
 
 class Plan:
@@ -190,6 +232,84 @@ class Buffer:
         _abi.check(lib().moonep_combine(self._h, ctypes.byref(plan.struct), *args, _stream()),
                    "moonep_combine")
         return out, rw_sk
+
+    def combine_bwd(self, plan, dout, y_nvs, rw_nvs, dy_nvs=None, drw=None, need_drw=True):
+        """Gradient of the weighted combine: (dy_nvs, drw) from dout [R,S,W],
+        the forward's y_nvs [R,NvS,W] and rw_nvs [R,NvS].  dy_nvs may be y_nvs
+        (in place).  need_drw=False: the route weights need no gradient, drw is
+        None and y_nvs may be None."""
+        R, S, K, NvS = self.R, self.S, self.K, self.NvS
+        W = dout.shape[-1]
+        if drw is not None and not need_drw:
+            raise ValueError("drw given, but need_drw is False")
+        dev = dout.device
+        if dy_nvs is None:
+            dy_nvs = torch.empty((R, NvS, W), dtype=torch.bfloat16, device=dev)
+        if drw is None and need_drw:
+            drw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+        args = (_dev_ptr(dout, torch.bfloat16, (R, S, W), "dout"), int(W),
+                _dev_ptr(y_nvs, torch.bfloat16, (R, NvS, W), "y_nvs", not need_drw),
+                _dev_ptr(rw_nvs, torch.float32, (R, NvS), "rw_nvs"),
+                _dev_ptr(dy_nvs, torch.bfloat16, (R, NvS, W), "dy_nvs"),
+                _dev_ptr(drw, torch.float32, (R, S, K), "drw", True))
+        _same_device(dev, y_nvs=y_nvs, rw_nvs=rw_nvs, dy_nvs=dy_nvs, drw=drw,
+                     plan=plan.dest)
+        inplace = y_nvs is not None and dy_nvs.data_ptr() == y_nvs.data_ptr()
+        _apart("dy_nvs", dy_nvs, dout=dout, y_nvs=None if inplace else y_nvs, rw_nvs=rw_nvs)
+        if drw is not None:
+            _apart("drw", drw, dout=dout, y_nvs=y_nvs, rw_nvs=rw_nvs, dy_nvs=dy_nvs)
+        with torch.cuda.device(dev):
+            _abi.check(lib().moonep_combine_bwd(self._h, ctypes.byref(plan.struct), *args,
+                                                _stream()), "moonep_combine_bwd")
+        return dy_nvs, drw
+
+    def route(self, logits, bias=None, score="softmax", normalize=True, scale=1.0, topk=None,
+              rw=None):
+        """The router's choice: (topk [R,S,K] int32, rw [R,S,K] fp32) from logits
+        [R,S,E] (float32 or bfloat16).  score: "softmax" or "sigmoid"; bias [E]
+        fp32 (selection only): the choice goes by score + bias instead of the
+        logit; normalize: the K weights are divided by their sum; scale
+        multiplies them.  A logit of -inf closes its expert."""
+        R, S, K, E = self.R, self.S, self.K, self.E
+        dev = logits.device
+        if topk is None:
+            topk = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+        if rw is None:
+            rw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+        dt = _float_type(logits, "logits")
+        args = (_dev_ptr(logits, logits.dtype, (R, S, E), "logits"), dt,
+                _dev_ptr(bias, torch.float32, (E,), "bias", True), _score(score),
+                int(bool(normalize)), float(scale),
+                _dev_ptr(topk, torch.int32, (R, S, K), "topk"),
+                _dev_ptr(rw, torch.float32, (R, S, K), "rw"))
+        _same_device(dev, bias=bias, topk=topk, rw=rw)
+        _apart("topk", topk, logits=logits, bias=bias, rw=rw)
+        _apart("rw", rw, logits=logits, bias=bias)
+        with torch.cuda.device(dev):
+            _abi.check(lib().moonep_route(self._h, *args, _stream()), "moonep_route")
+        return topk, rw
+
+    def route_bwd(self, logits, topk, drw, score="softmax", normalize=True, scale=1.0,
+                  dlogits=None):
+        """Gradient of route's weights: dlogits [R,S,E] in the logits' type from
+        drw [R,S,K] fp32, for the topk and the form of the forward call (the
+        selection bias takes no part).  dlogits may be logits (in place)."""
+        R, S, K, E = self.R, self.S, self.K, self.E
+        dev = logits.device
+        if dlogits is None:
+            dlogits = torch.empty_like(logits)
+        dt = _float_type(logits, "logits")
+        args = (_dev_ptr(logits, logits.dtype, (R, S, E), "logits"), dt, _score(score),
+                int(bool(normalize)), float(scale),
+                _dev_ptr(topk, torch.int32, (R, S, K), "topk"),
+                _dev_ptr(drw, torch.float32, (R, S, K), "drw"),
+                _dev_ptr(dlogits, logits.dtype, (R, S, E), "dlogits"))
+        _same_device(dev, topk=topk, drw=drw, dlogits=dlogits)
+        inplace = dlogits.data_ptr() == logits.data_ptr()
+        _apart("dlogits", dlogits, topk=topk, drw=drw, logits=None if inplace else logits)
+        with torch.cuda.device(dev):
+            _abi.check(lib().moonep_route_bwd(self._h, *args, _stream()), "moonep_route_bwd")
+        return dlogits
 
     def _weights(self, ts, pool, used=(0, 1, 2)):
         R, E, B, H, Hp = self.R, self.E, self.B, self.H, self.Hp
@@ -349,6 +469,48 @@ def vmm_granularity():
     g = ctypes.c_int64()
     _abi.check(lib().moonep_vmm_granularity(ctypes.byref(g)), "moonep_vmm_granularity")
     return int(g.value)
+
+
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize_workspace(n, rows, cols, device="cuda"):
+    """Workspace tensor of `orthogonalize` for n matrices of rows x cols."""
+    nbytes = int(lib().moonep_orthogonalize_ws(n, rows, cols))
+    if nbytes < 0:
+        raise MoonepError(_abi.MOONEP_ERR_CONFIG, "moonep_orthogonalize_ws")
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
+    """Newton-Schulz directions of weight gradients (moonep_orthogonalize): g
+    [n,rows,cols] or [rows,cols], float32 (such as grad_home [E,H,Hp]) or
+    bfloat16, each matrix on its own, to bfloat16 of the same shape.  coeffs:
+    one (a, b, c) for every step, or a sequence of `steps` of them.  ws: a
+    workspace of orthogonalize_workspace(n, rows, cols); without one it is
+    allocated per call."""
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g: expected [n,rows,cols] or [rows,cols], got {tuple(g.shape)}")
+    n, rows, cols = (1, *g.shape) if g.dim() == 2 else g.shape
+    dt = _float_type(g, "g")
+    flat = [tuple(c) for c in coeffs] if hasattr(coeffs[0], "__len__") else [tuple(coeffs)] * steps
+    if len(flat) != steps or any(len(c) != 3 for c in flat):
+        raise ValueError("coeffs: expected (a, b, c) or one (a, b, c) per step")
+    dev = g.device
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+    if ws is None:
+        ws = orthogonalize_workspace(n, rows, cols, device=dev)
+    args = (_dev_ptr(g, g.dtype, g.shape, "g"), dt, int(n), int(rows), int(cols),
+            (ctypes.c_float * (3 * steps))(*[v for c in flat for v in c]), int(steps), float(eps),
+            _dev_ptr(out, torch.bfloat16, g.shape, "out"),
+            _dev_ptr(ws, torch.uint8, (ws.numel(),), "ws"), int(ws.numel()))
+    _same_device(dev, out=out, ws=ws)
+    _apart("out", out, g=g, ws=ws)
+    _apart("ws", ws, g=g)
+    with torch.cuda.device(dev):
+        _abi.check(lib().moonep_orthogonalize(*args, _stream()), "moonep_orthogonalize")
+    return out
 
 
 class SymmetricBuffer:

@@ -72,6 +72,12 @@ def lib():
                                       ctypes.POINTER(MoonepPlan), vp]),
         "moonep_dispatch": (i32, [vp, ctypes.POINTER(MoonepPlan), vp, i32, vp, vp, vp, vp]),
         "moonep_combine": (i32, [vp, ctypes.POINTER(MoonepPlan), vp, i32, vp, vp, vp, vp]),
+        "moonep_combine_bwd": (i32, [vp, ctypes.POINTER(MoonepPlan), vp, i32, vp, vp, vp, vp, vp]),
+        "moonep_route": (i32, [vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp]),
+        "moonep_route_bwd": (i32, [vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp]),
+        "moonep_orthogonalize_ws": (i64, [i32, i32, i32]),
+        "moonep_orthogonalize": (i32, [vp, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_float), i32,
+                                       ctypes.c_float, vp, vp, i64, vp]),
         "moonep_copy_rows": (i32, [vp, ctypes.POINTER(MoonepPlan), vp, i32, vp, vp]),
         "moonep_prefetch_weight": (i32, [vp, ctypes.POINTER(MoonepPlan), P3, P3, vp]),
         "moonep_expert_ffn": (i32, [vp, ctypes.POINTER(MoonepPlan), i32, vp, P3, P3, vp, vp, vp]),
@@ -123,7 +129,10 @@ def plan_len(cfg: MoonepConfig, which: int) -> int:
     return int(lib().moonep_plan_len(ctypes.byref(cfg), which))
 
 
-GRID_DISPATCH, GRID_COMBINE, GRID_COPY, GRID_PREFETCH, GRID_REDUCE_GRAD = range(5)
+(GRID_DISPATCH, GRID_COMBINE, GRID_COPY, GRID_PREFETCH, GRID_REDUCE_GRAD,
+ GRID_COMBINE_BWD) = range(6)
+F32, BF16 = range(2)
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 def launch_grid(cfg: MoonepConfig, which: int, W: int = 0, device_cus: int = 256) -> int:

@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoonep.so")
 SOURCES = ["api.hip", "plan.hip", "plan_noalloc.hip", "move.hip", "gemm.hip", "gemm_bwd.hip",
-           "symbuf.hip"]
+           "route.hip", "ortho.hip", "symbuf.hip"]
 ARCH = "gfx950"
 
 

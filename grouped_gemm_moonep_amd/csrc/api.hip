@@ -145,7 +145,7 @@ const char* moonep_status_string(moonep_status_t s) {
     case MOONEP_ERR_HIP: return "HIP runtime error";
     case MOONEP_ERR_NOMEM: return "device allocation failed";
     case MOONEP_ERR_SCRATCH:
-      return "configuration needs more planning scratch than the allocation-free entry point holds";
+      return "configuration needs more scratch than the library or the given workspace holds";
     default: return "unknown status";
   }
 }
@@ -177,11 +177,12 @@ int64_t moonep_launch_grid(const moonep_config_t* cfg, int32_t which, int32_t W,
   if (!dims_from_config(cfg, &c.d) || device_cus < 1) return -1;
   c.num_cu_device = device_cus;
   const bool rows = which == MOONEP_GRID_DISPATCH || which == MOONEP_GRID_COMBINE ||
-                    which == MOONEP_GRID_COPY;
+                    which == MOONEP_GRID_COPY || which == MOONEP_GRID_COMBINE_BWD;
   if (rows && (W <= 0 || W % 8)) return -1;
   switch (which) {
     case MOONEP_GRID_DISPATCH: return dispatch_grid(c, W).blocks;
     case MOONEP_GRID_COMBINE: return combine_grid(c, W);
+    case MOONEP_GRID_COMBINE_BWD: return combine_bwd_grid(c, W).blocks;
     case MOONEP_GRID_COPY: return copy_grid(c);
     case MOONEP_GRID_PREFETCH: return prefetch_grid(c);
     case MOONEP_GRID_REDUCE_GRAD: return reduce_grad_grid(c);
@@ -268,6 +269,75 @@ moonep_status_t moonep_combine(moonep_handle_t h, const moonep_plan_t* plan,
   if (rw_sk && !rw_nvs) return MOONEP_ERR_ARG;
   if ((rw_nvs && !aligned(rw_nvs, 4)) || (rw_sk && !aligned(rw_sk, 4))) return MOONEP_ERR_ARG;
   return hip_status(launch_combine(h->c, *plan, y_nvs, W, rw_nvs, out, rw_sk, stream));
+}
+
+moonep_status_t moonep_combine_bwd(moonep_handle_t h, const moonep_plan_t* plan,
+                                   const uint16_t* dout, int32_t W, const uint16_t* y_nvs,
+                                   const float* rw_nvs, uint16_t* dy_nvs, float* drw,
+                                   hipStream_t stream) {
+  if (!h || !plan_ok(plan) || !dout || !rw_nvs || !dy_nvs) return MOONEP_ERR_ARG;
+  if (W <= 0 || W % 8 || !aligned(dout, 16) || !aligned(dy_nvs, 16) || !aligned(rw_nvs, 4))
+    return MOONEP_ERR_ARG;
+  if (drw && (!y_nvs || !aligned(y_nvs, 16) || !aligned(drw, 4))) return MOONEP_ERR_ARG;
+  if ((const void*)dout == (const void*)dy_nvs) return MOONEP_ERR_ARG;
+  return hip_status(launch_combine_bwd(h->c, *plan, dout, W, y_nvs, rw_nvs, dy_nvs, drw, stream));
+}
+
+static size_t type_bytes(int32_t dtype) { return dtype == MOONEP_F32 ? 4 : 2; }
+
+static bool route_form_ok(int32_t dtype, int32_t score) {
+  return (dtype == MOONEP_F32 || dtype == MOONEP_BF16) &&
+         (score == MOONEP_SCORE_SOFTMAX || score == MOONEP_SCORE_SIGMOID);
+}
+
+moonep_status_t moonep_route(moonep_handle_t h, const void* logits, int32_t dtype,
+                             const float* bias, int32_t score, int32_t normalize, float scale,
+                             int32_t* topk, float* rw, hipStream_t stream) {
+  if (!h || !logits || !topk || !rw || !route_form_ok(dtype, score)) return MOONEP_ERR_ARG;
+  if (!aligned(logits, type_bytes(dtype)) || !aligned(topk, 4) || !aligned(rw, 4) ||
+      (bias && !aligned(bias, 4)))
+    return MOONEP_ERR_ARG;
+  const RouteForm f = {dtype, score, normalize != 0, scale};
+  return hip_status(launch_route(h->c, logits, bias, f, topk, rw, stream));
+}
+
+moonep_status_t moonep_route_bwd(moonep_handle_t h, const void* logits, int32_t dtype,
+                                 int32_t score, int32_t normalize, float scale,
+                                 const int32_t* topk, const float* drw, void* dlogits,
+                                 hipStream_t stream) {
+  if (!h || !logits || !topk || !drw || !dlogits || !route_form_ok(dtype, score))
+    return MOONEP_ERR_ARG;
+  if (!aligned(logits, type_bytes(dtype)) || !aligned(dlogits, type_bytes(dtype)) ||
+      !aligned(topk, 4) || !aligned(drw, 4))
+    return MOONEP_ERR_ARG;
+  const RouteForm f = {dtype, score, normalize != 0, scale};
+  return hip_status(launch_route_bwd(h->c, logits, f, topk, drw, dlogits, stream));
+}
+
+int64_t moonep_orthogonalize_ws(int32_t n, int32_t rows, int32_t cols) {
+  return ortho_shape_ok(n, rows, cols) ? ortho_ws_bytes(n, rows, cols) : -1;
+}
+
+moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
+                                     int32_t cols, const float* coeffs, int32_t steps, float eps,
+                                     uint16_t* out, void* ws, int64_t ws_bytes,
+                                     hipStream_t stream) {
+  if (!ortho_shape_ok(n, rows, cols)) return MOONEP_ERR_CONFIG;
+  if ((dtype != MOONEP_F32 && dtype != MOONEP_BF16) || !coeffs || !(eps > 0.0f) ||
+      steps < 1 || steps > MOONEP_ORTHO_MAX_STEPS)
+    return MOONEP_ERR_ARG;
+  double gain = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    if (!(coeffs[3 * i] > 0.0f)) return MOONEP_ERR_ARG;
+    gain *= coeffs[3 * i];
+    if (!(gain <= MOONEP_ORTHO_MAX_GAIN)) return MOONEP_ERR_ARG;
+  }
+  if (n == 0) return MOONEP_OK;
+  if (!g || !out || !ws || !aligned(g, type_bytes(dtype)) || !aligned(out, 2) || !aligned(ws, 256))
+    return MOONEP_ERR_ARG;
+  if (ws_bytes < ortho_ws_bytes(n, rows, cols)) return MOONEP_ERR_SCRATCH;
+  return hip_status(launch_orthogonalize(g, dtype, n, rows, cols, coeffs, steps, eps, out, ws,
+                                         stream));
 }
 
 moonep_status_t moonep_copy_rows(moonep_handle_t h, const moonep_plan_t* plan,

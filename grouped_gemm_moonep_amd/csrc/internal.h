@@ -86,6 +86,13 @@ struct DispatchGrid {
   int64_t blocks;     // the whole grid
 };
 DispatchGrid dispatch_grid(const Ctx& c, int W);
+// Workgroups of the combine gradient: `lanes` lanes per (token, k) item, item_blocks workgroups
+// of items (item_grid of them launched, rounded up per XCD), then the padding workgroups.
+struct CombineBwdGrid {
+  int xcd_local, lanes, npad_used, pad_parts;
+  int64_t item_blocks, item_grid, blocks;
+};
+CombineBwdGrid combine_bwd_grid(const Ctx& c, int W);
 int64_t combine_grid(const Ctx& c, int W);
 int64_t copy_grid(const Ctx& c);
 int64_t prefetch_grid(const Ctx& c);
@@ -97,6 +104,9 @@ hipError_t launch_dispatch(const Ctx& c, const moonep_plan_t& p,
 hipError_t launch_combine(const Ctx& c, const moonep_plan_t& p,
                           const uint16_t* y, int W, const float* rw_nvs,
                           uint16_t* out, float* rw_sk, hipStream_t s);
+hipError_t launch_combine_bwd(const Ctx& c, const moonep_plan_t& p, const uint16_t* dout, int W,
+                              const uint16_t* y, const float* rw_nvs, uint16_t* dy, float* drw,
+                              hipStream_t s);
 hipError_t launch_copy_rows(const Ctx& c, const moonep_plan_t& p,
                             const uint16_t* src, int W, uint16_t* dst,
                             hipStream_t s);
@@ -114,6 +124,23 @@ hipError_t launch_ffn_bwd(const Ctx& c, const moonep_plan_t& p, int rank,
                           const uint16_t* x, const uint16_t* dy, const WeightRef& w,
                           uint16_t* dz, uint16_t* dg, uint16_t* du, uint16_t* dx,
                           hipStream_t s);
+// Router (route.hip).  dtype: MOONEP_F32 or MOONEP_BF16.
+struct RouteForm {
+  int32_t dtype, score, normalize;
+  float scale;
+};
+hipError_t launch_route(const Ctx& c, const void* logits, const float* bias, const RouteForm& f,
+                        int32_t* topk, float* rw, hipStream_t s);
+hipError_t launch_route_bwd(const Ctx& c, const void* logits, const RouteForm& f,
+                            const int32_t* topk, const float* drw, void* dlogits, hipStream_t s);
+
+// Newton-Schulz orthogonalisation (ortho.hip).
+bool ortho_shape_ok(int32_t n, int32_t rows, int32_t cols);
+int64_t ortho_ws_bytes(int32_t n, int32_t rows, int32_t cols);
+hipError_t launch_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
+                                int32_t cols, const float* coeffs, int32_t steps, float eps,
+                                uint16_t* out, void* ws, hipStream_t s);
+
 hipError_t launch_wgrad(const Ctx& c, const moonep_plan_t& p, int rank,
                         const uint16_t* a, const uint16_t* b, float* gh,
                         float* rb, hipStream_t s);

@@ -223,6 +223,103 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
   }
 }
 
+// Gradient of the weighted combine out[t] = sum_k w_k y[slot_k]:
+//   dy[slot_k] = bf16(w_k dout[t]),   dw_k = <dout[t], y[slot_k]> in fp32.
+// HBM-bound (every slot row read and written once, every dout row read once).
+// One item per (token, k): G lanes (a power of two that covers a narrow row,
+// else the whole wave) read the slot's row of y and the token's row of dout in
+// chunks of V vectors per lane, add their products and write the scaled dout.
+// The sum's order is fixed (a lane's vectors in ascending order, then a
+// butterfly over the lanes), so the result does not depend on the launch.
+// A chunk is read before it is written, so dy may be y itself.
+struct CombineBwdArgs {
+  const u32x4* dout;     // [R*S][W/8]
+  const u32x4* y;        // [R*NvS][W/8] (unused without drw)
+  const float* rw_nvs;   // [R*NvS]
+  float* drw;            // [R*S][K] or null
+  const int32_t* dest;   // [R*S][K]
+  DispatchArgs pad;      // dy (as x_nvs) and the padding items
+  int64_t items;         // R*S*K
+  int64_t item_blocks;   // workgroups that the items fill
+  int nv, K;
+};
+
+template <int G, int V, bool kDot>
+__device__ __forceinline__ void combine_bwd_items(const CombineBwdArgs& a, int64_t blk, int wv,
+                                                  int lane) {
+  constexpr int kPerWave = 64 / G;
+  const int64_t it = (blk * kWaves + wv) * kPerWave + lane / G;
+  if (it >= a.items) return;                             // whole groups of G lanes at once
+  const int gl = lane % G;
+  int slot = a.dest[it], tok = (int)(it / a.K);
+  if (G == 64) {
+    slot = uniform(slot);
+    tok = uniform(tok);
+  }
+  const float w = a.rw_nvs[slot];
+  const u32x4* d = a.dout + (int64_t)tok * a.nv;
+  const u32x4* y = a.y + (int64_t)slot * a.nv;
+  u32x4* dy = a.pad.x_nvs + (int64_t)slot * a.nv;
+  float sum = 0.0f;
+  for (int c0 = 0; c0 < a.nv; c0 += G * V) {
+    u32x4 dv[V], yv[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int v = c0 + u * G + gl;
+      if (v < a.nv) {
+        if (kDot) yv[u] = __builtin_nontemporal_load(y + v);
+        dv[u] = d[v];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int v = c0 + u * G + gl;
+      if (v < a.nv) {
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = bf16_lo(dv[u][j]), hi = bf16_hi(dv[u][j]);
+          if (kDot) {
+            sum = __fmaf_rn(lo, bf16_lo(yv[u][j]), sum);
+            sum = __fmaf_rn(hi, bf16_hi(yv[u][j]), sum);
+          }
+          o[j] = pack_bf16x2(__fmul_rn(w, lo), __fmul_rn(w, hi));
+        }
+        __builtin_nontemporal_store(o, dy + v);
+      }
+    }
+  }
+  if (kDot) {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) sum = __fadd_rn(sum, __shfl_xor(sum, o, 64));
+    if (gl == 0) a.drw[it] = sum;
+  }
+}
+
+// Without a CU budget every workgroup has one piece of work: K consecutive
+// item workgroups hold the items of 4 (or 256/G) tokens, and they run on one
+// XCD, whose L2 then serves all but the first read of a token's dout row; the
+// padding workgroups follow.  With a budget the workgroups loop.
+template <int G, int V, bool kDot>
+__global__ __launch_bounds__(kThreads) void combine_bwd_kernel(CombineBwdArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int wv = threadIdx.x >> 6;
+  if (a.pad.xcd_local) {
+    const int64_t b = blockIdx.x;
+    if (b >= a.pad.item_blocks) {
+      dispatch_pad(a.pad, (int)(b - a.pad.item_blocks), wv, lane);
+      return;
+    }
+    const int64_t r = b / kXcdsMove;
+    const int64_t blk = (r / a.K * kXcdsMove + b % kXcdsMove) * a.K + r % a.K;
+    combine_bwd_items<G, V, kDot>(a, blk, wv, lane);
+    return;
+  }
+  for (int pb = blockIdx.x; pb < a.pad.npad_used; pb += gridDim.x) dispatch_pad(a.pad, pb, wv, lane);
+  for (int64_t b = blockIdx.x; b < a.item_blocks; b += gridDim.x)
+    combine_bwd_items<G, V, kDot>(a, b, wv, lane);
+}
+
 // prefetch: workgroup = (projection, 16 KiB column chunk of a weight row); it
 // copies that chunk of every used slot in turn, so at any moment the
 // workgroups sweep the rows of one slot together (a moving window, which
@@ -391,6 +488,31 @@ DispatchGrid dispatch_grid(const Ctx& c, int W) {
   return g;
 }
 
+// lanes per item of the combine gradient: the smallest power of two from 8 that covers the row
+static int combine_bwd_lanes(int nv) { return nv <= 8 ? 8 : nv <= 16 ? 16 : nv <= 32 ? 32 : 64; }
+
+CombineBwdGrid combine_bwd_grid(const Ctx& c, int W) {
+  const Dims& d = c.d;
+  const DispatchGrid dg = dispatch_grid(c, W);
+  CombineBwdGrid g;
+  g.pad_parts = dg.pad_parts;
+  g.npad_used = dg.npad_used;
+  g.lanes = combine_bwd_lanes(W / 8);
+  const int64_t per_block = kThreads / g.lanes;
+  g.item_blocks = ((int64_t)d.R * d.S * d.K + per_block - 1) / per_block;
+  if (d.num_cus > 0) {
+    g.xcd_local = 0;
+    g.item_grid = 0;
+    g.blocks = capped_grid(c, g.item_blocks + g.npad_used);
+  } else {
+    const int64_t round = (int64_t)kXcdsMove * d.K;      // whole rounds of K workgroups per XCD
+    g.xcd_local = 1;
+    g.item_grid = (g.item_blocks + round - 1) / round * round;
+    g.blocks = g.item_grid + g.npad_used;
+  }
+  return g;
+}
+
 int64_t combine_grid(const Ctx& c, int W) {
   const int nchunks = (W / 8 + 64 * kCombVecs - 1) / (64 * kCombVecs);
   return capped_grid(c, ((int64_t)c.d.R * c.d.S * nchunks + kWaves - 1) / kWaves);
@@ -442,6 +564,41 @@ hipError_t launch_combine(const Ctx& c, const moonep_plan_t& p, const uint16_t* 
     combine_kernel<true><<<blocks, kThreads, 0, s>>>(a);
   else
     combine_kernel<false><<<blocks, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int G, int V>
+static void run_combine_bwd(const CombineBwdArgs& a, unsigned blocks, hipStream_t s) {
+  if (a.drw)
+    combine_bwd_kernel<G, V, true><<<blocks, kThreads, 0, s>>>(a);
+  else
+    combine_bwd_kernel<G, V, false><<<blocks, kThreads, 0, s>>>(a);
+}
+
+hipError_t launch_combine_bwd(const Ctx& c, const moonep_plan_t& p, const uint16_t* dout, int W,
+                              const uint16_t* y, const float* rw_nvs, uint16_t* dy, float* drw,
+                              hipStream_t s) {
+  const Dims& d = c.d;
+  const CombineBwdGrid g = combine_bwd_grid(c, W);
+  CombineBwdArgs a;
+  a.dout = (const u32x4*)dout; a.y = (const u32x4*)y; a.rw_nvs = rw_nvs; a.drw = drw;
+  a.dest = p.dest; a.K = d.K; a.nv = W / 8;
+  a.items = (int64_t)d.R * d.S * d.K;
+  a.item_blocks = g.item_blocks;
+  DispatchArgs& q = a.pad;
+  q.x = nullptr; q.rw = nullptr; q.x_nvs = (u32x4*)dy; q.rw_nvs = nullptr;
+  q.dest = p.dest; q.cu = p.cu_seqlens; q.segn = p.seg_tokens; q.act = p.aux + d.aux.act;
+  q.ntok = d.R * d.S; q.K = d.K; q.nv = W / 8; q.EB = d.E + d.B; q.L2 = 2 * d.L;
+  q.tp = d.tp; q.NvS = (int)d.NvS;
+  q.pad_parts = g.pad_parts; q.npad_used = g.npad_used;
+  q.xcd_local = g.xcd_local; q.item_blocks = (int)g.item_grid;
+  const unsigned blocks = (unsigned)g.blocks;
+  switch (g.lanes) {
+    case 8: run_combine_bwd<8, 1>(a, blocks, s); break;
+    case 16: run_combine_bwd<16, 1>(a, blocks, s); break;
+    case 32: run_combine_bwd<32, 1>(a, blocks, s); break;
+    default: run_combine_bwd<64, 8>(a, blocks, s); break;
+  }
   return hipGetLastError();
 }
 

@@ -50,7 +50,8 @@ enum {
   MOONEP_ERR_HIP = 4,     /* a HIP runtime call or kernel launch failed    */
   MOONEP_ERR_NOMEM = 5,   /* scratch allocation in moonep_create failed    */
   MOONEP_ERR_SCRATCH = 6  /* moonep_plan_noalloc: the configuration needs
-                             more planning scratch than the library holds  */
+                             more planning scratch than the library holds;
+                             moonep_orthogonalize: workspace too small      */
 };
 
 /* Problem sizes, in the README's notation ("Usage > Integration"):
@@ -125,14 +126,14 @@ int64_t moonep_plan_len(const moonep_config_t* cfg, int32_t which);
  * (README "API guide", Buffer(..., num_sms, ...): the CU budget caps the
  * grids of the data-movement kernels; planning and GEMM grids are not
  * capped).  which: MOONEP_GRID_*.  W: row width in elements for dispatch,
- * combine and copy (a positive multiple of 8; ignored otherwise).
+ * combine, its gradient and copy (a positive multiple of 8; ignored otherwise).
  * device_cus: the device's compute units (reduce_grad launches at most 8
  * workgroups per CU).  Host only: no GPU call is made.  With cfg->num_cus > 0
  * every result is at most num_cus * 8.  Returns -1 for an invalid config,
  * which, W or device_cus. */
 enum {
   MOONEP_GRID_DISPATCH = 0, MOONEP_GRID_COMBINE, MOONEP_GRID_COPY,
-  MOONEP_GRID_PREFETCH, MOONEP_GRID_REDUCE_GRAD
+  MOONEP_GRID_PREFETCH, MOONEP_GRID_REDUCE_GRAD, MOONEP_GRID_COMBINE_BWD
 };
 int64_t moonep_launch_grid(const moonep_config_t* cfg, int32_t which, int32_t W,
                            int32_t device_cus);
@@ -142,6 +143,44 @@ int64_t moonep_launch_grid(const moonep_config_t* cfg, int32_t which, int32_t W,
 moonep_status_t moonep_create(const moonep_config_t* cfg, moonep_handle_t* out);
 /* Free the scratch (the README's buffer.destroy()).  NULL is a no-op. */
 moonep_status_t moonep_destroy(moonep_handle_t h);
+
+/* Element types of the entry points that take more than one. */
+enum { MOONEP_F32 = 0, MOONEP_BF16 = 1 };
+/* Scores of the router. */
+enum { MOONEP_SCORE_SOFTMAX = 0, MOONEP_SCORE_SIGMOID = 1 };
+
+/* Router (the framework-side step that makes the README's topk_experts_sk and
+ * route_weights_sk, "API guide > dispatch fwd"): from logits [R,S,E] (dtype:
+ * MOONEP_F32 or MOONEP_BF16) the K experts of every token and their weights.
+ *   score_e = softmax(l)_e or sigma(l_e), by `score`;
+ *   the choice goes by l_e, or by score_e + bias_e if bias [E] fp32 is given
+ *   (a selection bias: it takes no part in the weights);
+ *   topk [R,S,K]: the K largest in descending order, equal ones by ascending
+ *   id (scores with a bias are compared as if computed exactly);
+ *   rw [R,S,K] fp32 = scale * score_k, divided by the sum of the K chosen
+ *   scores if `normalize` is nonzero.
+ * A logit of -inf closes its expert: it comes after every open one, with a
+ * weight of 0; a token without an open expert has weights of 0.  NaN logits
+ * come first and show in the weights.  The ids of a token are always distinct
+ * and in range, as moonep_plan needs them.  The handle's R, S, K and E count;
+ * no scratch is used, and outputs must not overlap the inputs. */
+moonep_status_t moonep_route(moonep_handle_t h, const void* logits, int32_t dtype,
+                             const float* bias, int32_t score, int32_t normalize, float scale,
+                             int32_t* topk, float* rw, hipStream_t stream);
+
+/* Gradient of the route weights with respect to the logits, for the topk that
+ * moonep_route gave (the choice itself and the bias have no gradient): drw
+ * [R,S,K] fp32 -> dlogits [R,S,E] in the logits' type, every element written.
+ *   g = scale * drw, q = the chosen scores, t = their sum,
+ *   dq_k = (g_k - sum_j g_j q_j / t) / t if normalized, else g_k;
+ *   softmax: dl_e = score_e (dq_e [e chosen] - sum_j dq_j q_j);
+ *   sigmoid: dl_e = dq_e sigma(l_e) sigma(-l_e) for the chosen, else 0.
+ * A closed expert and a token without an open one get 0.  An id outside
+ * [0,E) is left out; a repeated id is not allowed.  dlogits may be logits. */
+moonep_status_t moonep_route_bwd(moonep_handle_t h, const void* logits, int32_t dtype,
+                                 int32_t score, int32_t normalize, float scale,
+                                 const int32_t* topk, const float* drw, void* dlogits,
+                                 hipStream_t stream);
 
 /* Plan (README "API guide > dispatch fwd", planning part).
  * topk [R,S,K] int32 expert ids, k in the router's order.
@@ -199,6 +238,23 @@ moonep_status_t moonep_combine(moonep_handle_t h, const moonep_plan_t* plan,
                                const uint16_t* y_nvs, int32_t W,
                                const float* rw_nvs, uint16_t* out,
                                float* rw_sk, hipStream_t stream);
+
+/* Gradient of the weighted combine (the framework-side step before the FFN
+ * backward when the route weights are applied by combine; with an unweighted
+ * combine it is the README's "combine bwd", a re-dispatch).  For dout
+ * [R,S,W] bf16, the gradient of combine's output, W % 8 == 0, the forward's
+ * y_nvs [R,NvS,W] and rw_nvs [R,NvS] fp32:
+ *   dy_nvs[slot_k] = bf16_rne(rw_nvs[slot_k] * dout[r,s,:])  [R,NvS,W],
+ *   drw[r,s,k] = sum_w dout[r,s,w] * y_nvs[slot_k,w]          [R,S,K] fp32,
+ * the sum in fp32 in an order that depends on W alone.  Padding slots inside a
+ * segment get zeros; slots past a rank's last segment are not written.  drw
+ * may be NULL (y_nvs is not read then and may be NULL too).  dy_nvs may be
+ * y_nvs (in place); no other aliasing.  dy_nvs is moonep_expert_ffn_bwd's
+ * dy_nvs, drw is moonep_route_bwd's. */
+moonep_status_t moonep_combine_bwd(moonep_handle_t h, const moonep_plan_t* plan,
+                                   const uint16_t* dout, int32_t W, const uint16_t* y_nvs,
+                                   const float* rw_nvs, uint16_t* dy_nvs, float* drw,
+                                   hipStream_t stream);
 
 /* Copy of the used slots (README "API guide > zero_copy"): with zero_copy
  * off, dispatch hands back a new tensor copied out of the communication
@@ -306,6 +362,35 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
                                    float* const grad_home[3],
                                    float* const reduce_buf[3],
                                    hipStream_t stream);
+
+/* Orthogonalised directions of n weight gradients (the framework-side step
+ * after reduce_grad, as the Muon optimiser takes it): for every matrix G of g
+ * [n,rows,cols] (dtype: MOONEP_F32, such as rows of grad_home [E,H,Hp], or
+ * MOONEP_BF16),
+ *   X = G / (|G| + eps), |G| the Frobenius norm, then for every step i
+ *   X = a_i X + (b_i A + c_i A A) X, A = X X^T,
+ * and out [n,rows,cols] = bf16_rne(X).  coeffs: HOST array [steps][3] of
+ * (a, b, c), read before the call returns.  The products are taken on values
+ * held to 22 bits and summed in fp32; the rounding left in X is a few parts
+ * in 10^4 of its norm at most, below that of its bf16 values.  The a_i scale
+ * that rounding up, so their product may be at most
+ * MOONEP_ORTHO_MAX_GAIN, each a_i > 0, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS,
+ * eps > 0.  Coefficients have to keep X's singular values below 1.9, as those
+ * of any converging iteration do.  A zero matrix gives zeros; infinities and
+ * NaN stay within their own matrix.
+ * ws: device workspace of at least moonep_orthogonalize_ws bytes, 256-byte
+ * aligned; its contents need not be kept between calls, and calls that overlap
+ * need one each (MOONEP_ERR_SCRATCH if it is too small).  g, out and ws must
+ * not overlap.  The current device is used; no handle is needed. */
+#define MOONEP_ORTHO_MAX_STEPS 16
+#define MOONEP_ORTHO_MAX_GAIN 2048
+/* Workspace bytes for these sizes (host only): n >= 0, rows, cols >= 1,
+ * rows * cols < 2^29; -1 otherwise. */
+int64_t moonep_orthogonalize_ws(int32_t n, int32_t rows, int32_t cols);
+moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
+                                     int32_t cols, const float* coeffs, int32_t steps, float eps,
+                                     uint16_t* out, void* ws, int64_t ws_bytes,
+                                     hipStream_t stream);
 
 /* ---- Symmetric [E+B,H,Hp] buffers on virtual memory ----
  *
