@@ -9,9 +9,9 @@
 // iterate on m x m matrices (m the shorter side, n the longer) and touch the
 // long side twice:
 //   A = X_0 X_0^T                                (first product, K = n)
-//   S = A A,  B = (b A + c S) / a                per step
-//   T = A + B A,  P = P + B P                    (P = I + B in the first)
-//   A = a^2 (T + B T)
+//   R = I + (b A + c A A) / a                    per step
+//   T = R A,  P = R P                            (P = R in the first)
+//   A = a^2 R T
 //   out = (prod a) P X_0                         (last product)
 // All m x m matrices are symmetric, so only the tiles on and above the
 // diagonal are computed and every element above it is written twice: to the bit, for an
@@ -48,20 +48,50 @@ constexpr int kParts = 256;                   // partial sums of a matrix's norm
 constexpr int kK = 32;                        // values of K per step (a 64-element block)
 
 // ------------------------------------------------------------- K loop
-// One step = 32 values of K = two 16-deep halves, hi in fragment columns kk =
-// 0, 1 and lo in kk = 2, 3: per half three groups of 16 MFMAs, h.a h.b, h.a l.b
-// and l.a h.b.  The operand bytes of a step are those of 64 values in 16 bits
-// and its MFMAs 1.5 times theirs, so the loads and LDS reads hide more easily
-// than in the expert GEMMs.  The groups run B-fragment by B-fragment: in the third
-// one h.b[j] is free after its four MFMAs and takes the next half's, so two
-// fragment sets (64 registers) suffice.
-template <int MI>
-struct Frag3 {
-  bf16x8 a[MI], b[4];
+// A workgroup's tile is 64 MI x 64 NJ: four waves in a 2 x 2 grid, each MI x NJ
+// blocks of 32 x 32.  One step = 32 values of K = two 16-deep halves, hi in
+// fragment columns kk = 0, 1 and lo in kk = 2, 3: per half three groups of MI
+// NJ MFMAs, h.a h.b, h.a l.b and l.a h.b.  The operand bytes of a step are
+// those of 64 values in 16 bits and its MFMAs 1.5 times theirs, so the loads
+// and LDS reads hide more easily than in the expert GEMMs.  The groups run
+// B-fragment by B-fragment: in the third one h.b[j] is free after its MI MFMAs
+// and takes the next half's, so two fragment sets suffice.
+//
+// The ring: kSlots = 5 slots shared by A and B as in gemm_core.h (A one step
+// ahead, B two), or, kDeep, 5 slots for each (both four steps ahead), which a
+// launch of few workgroups needs: its operands were just written by other XCDs,
+// a load takes as long as several steps, and no second workgroup fills the gap
+// (five steps on five 509 x 1283 matrices: 310 us without, 290 us with).
+template <int MI, int NJ, bool kDeep>
+struct Tile3 {
+  static constexpr int kRows = 64 * MI, kCols = 64 * NJ;
+  static constexpr int kNA = 2 * MI, kNB = 2 * NJ;                      // loads per wave and step
+  static constexpr int kSlot = 128 * (kRows > kCols ? kRows : kCols);   // bytes of a ring slot
+  static constexpr int kLds = (kDeep ? 2 : 1) * kSlots * kSlot;
+  static constexpr int kWaveLds = kLds / 4;                             // a wave's share of the ring
+  static constexpr int kAheadA = kDeep ? kSlots - 1 : 1, kAheadB = kDeep ? kSlots - 1 : 2;
+  // loads that may be outstanding when the next step's tiles have to be there
+  static constexpr int kLater = kDeep ? (kSlots - 2) * (kNA + kNB) : kNB;
+  // a workgroup takes a CU (160 KiB of LDS), or two share one
+  static constexpr int kWavesPerSimd = kLds > 81920 ? 1 : 2;
+  lds_t* base;
+  template <int J>
+  __device__ __forceinline__ lds_t* a() const {
+    return base + (kDeep ? J % kSlots : (2 * J + 1) % kSlots) * kSlot;
+  }
+  template <int J>
+  __device__ __forceinline__ lds_t* b() const {
+    return base + (kDeep ? kSlots + J % kSlots : (2 * J) % kSlots) * kSlot;
+  }
 };
 
-template <int MI>
-__device__ __forceinline__ void mma3(f32x16 acc[MI][4], const bf16x8& a, const bf16x8& b, int i,
+template <int MI, int NJ>
+struct Frag3 {
+  bf16x8 a[MI], b[NJ];
+};
+
+template <int MI, int NJ>
+__device__ __forceinline__ void mma3(f32x16 acc[MI][NJ], const bf16x8& a, const bf16x8& b, int i,
                                      int j) {
   acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b),
                                                      __builtin_bit_cast(f16x8, a), acc[i][j], 0, 0,
@@ -73,98 +103,156 @@ __device__ __forceinline__ bf16x8 read3(const lds_t* tile, int row0, int kk) {
   return RowTile::frag(tile, row0 + (lane & 31), kk, lane >> 5);
 }
 
-// Half HALF of step j (J = j mod 5): three groups of 4 MI MFMAs.  The loads of
-// A(j+1), then of B(j+2), go out between the step's first MFMAs; when the
-// first B fragment of the last group is free comes the wait for step j + 1's
-// tiles and the barrier, then the reads of step j + 1's first fragments (all
-// but h.b[3], which that step reads first).
-template <int J, int HALF, int MI>
-__device__ __forceinline__ void khalf3(const RowTileT<2 * MI>& la, const RowTile& lb,
-                                       const Ring& ring, uint32_t koa, uint32_t kob, Frag3<MI>& h,
-                                       Frag3<MI>& l, f32x16 acc[MI][4], int arow0,
-                                       const int nrow[4]) {
-  constexpr int J1 = (J + 1) % kSlots, J2 = (J + 2) % kSlots;
-  constexpr int GRP = 4 * MI, N = 3 * GRP, BAR = 21 * MI - 1, B0 = 6 * MI, BS = (BAR - B0) / 8;
-  static_assert(B0 >= 3 * 2 * MI && B0 + 7 * BS <= BAR, "loads must precede the barrier");
-  const lds_t* A = ring.a<J>();
-  const lds_t* Bt = ring.b<J>();
-  const lds_t* nA = HALF ? ring.a<J1>() : A;             // the next half's hi fragments
-  const lds_t* nB = HALF ? ring.b<J1>() : Bt;
+// at most N LDS-DMA loads of this wave outstanding
+template <int N>
+__device__ __forceinline__ void wait_dma() {
+  static_assert(N == 4 || N == 8 || N == 24, "outstanding loads");
+  if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+  else if constexpr (N == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
+}
+
+// Half HALF of step j (J = j mod 5).  The loads of the A and B tiles some
+// steps ahead go out between the step's first MFMAs, into slots that step j -
+// 1 read; before the first fragment of step j + 1 is read comes the wait for
+// that step's tiles and the barrier.  h.b[NJ-1] of a half is read at its own start.
+template <int J, int HALF, int MI, int NJ, bool kDeep>
+__device__ __forceinline__ void khalf3(const RowTileT<2 * MI>& la, const RowTileT<2 * NJ>& lb,
+                                       const Tile3<MI, NJ, kDeep>& ring, uint32_t koa,
+                                       uint32_t kob, Frag3<MI, NJ>& h, Frag3<MI, NJ>& l,
+                                       f32x16 acc[MI][NJ], int arow0, int bcol0) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  constexpr int J1 = J + 1, JA = J + TL::kAheadA, JB = J + TL::kAheadB;
+  constexpr int GRP = MI * NJ, N = 3 * GRP, NA = TL::kNA, NB = TL::kNB;
+  constexpr int F = 2 * GRP + MI;                        // h.b[0] is free from here, h.a MI before
+  constexpr int HA = NJ == 4 ? F + 1 : 2 * GRP;          // reads of the next h.a
+  constexpr int BAR = N + (HA < F ? HA : F) - 1;
+  constexpr int B0 = 3 * NA, BS = (BAR - B0) / NB;
+  static_assert(BS >= 1 && B0 + (NB - 1) * BS <= BAR, "loads must precede the barrier");
+  const lds_t* A = ring.template a<J>();
+  const lds_t* Bt = ring.template b<J>();
+  const lds_t* nA = HALF ? ring.template a<J1>() : A;    // the next half's hi fragments
+  const lds_t* nB = HALF ? ring.template b<J1>() : Bt;
   constexpr int nkk = HALF ? 0 : 1;
 #pragma unroll
   for (int o = 0; o < N; ++o) {
-    const int p = N * HALF + o, mi = o % MI, mj = o / MI % 4;
-    if (o < GRP) mma3<MI>(acc, h.a[mi], h.b[mj], mi, mj);
-    else if (o < 2 * GRP) mma3<MI>(acc, h.a[mi], l.b[mj], mi, mj);
-    else mma3<MI>(acc, l.a[mi], h.b[mj], mi, mj);
-    if (o == 0) h.b[3] = read3(Bt, nrow[3], HALF);
-    if (o >= 1 && o < 5) l.b[o - 1] = read3(Bt, nrow[o - 1], 2 + HALF);
-    if (o >= 5 && o < 5 + MI) l.a[o - 5] = read3(A, arow0 + 32 * (o - 5), 2 + HALF);
-    if (p % 3 == 1 && p / 3 < 2 * MI) la.issue1(ring.a<J1>(), p / 3, koa);
-    if (p >= B0 && (p - B0) % BS == 0 && (p - B0) / BS < 8)
-      lb.issue1(ring.b<J2>(), (p - B0) / BS, kob);
+    const int p = N * HALF + o, mi = o % MI, mj = o / MI % NJ;
+    if (o < GRP) mma3<MI, NJ>(acc, h.a[mi], h.b[mj], mi, mj);
+    else if (o < 2 * GRP) mma3<MI, NJ>(acc, h.a[mi], l.b[mj], mi, mj);
+    else mma3<MI, NJ>(acc, l.a[mi], h.b[mj], mi, mj);
+    if (o == 0) h.b[NJ - 1] = read3(Bt, bcol0 + 32 * (NJ - 1), HALF);
+    if (o >= 1 && o < 1 + NJ) l.b[o - 1] = read3(Bt, bcol0 + 32 * (o - 1), 2 + HALF);
+    if (o >= 1 + NJ && o < 1 + NJ + MI)
+      l.a[o - 1 - NJ] = read3(A, arow0 + 32 * (o - 1 - NJ), 2 + HALF);
+    if (p % 3 == 1 && p / 3 < NA) la.issue1(ring.template a<JA>(), p / 3, koa);
+    if (p >= B0 && (p - B0) % BS == 0 && (p - B0) / BS < NB)
+      lb.issue1(ring.template b<JB>(), (p - B0) / BS, kob);
     if (p == BAR) {
       MOONEP_PIN();
-      wait_loads<kLoadsPerStep>();
+      wait_dma<TL::kLater>();
       barrier_reads_done();
     }
-    constexpr int F = 9 * MI;                            // h.b[0] and h.a are free
-    if (o == F) h.b[0] = read3(nB, nrow[0], nkk);
-    if (o > F && o <= F + MI) h.a[o - F - 1] = read3(nA, arow0 + 32 * (o - F - 1), nkk);
-    if (o == F + MI + 1) h.b[1] = read3(nB, nrow[1], nkk);
-    if (o == F + 2 * MI) h.b[2] = read3(nB, nrow[2], nkk);
+    if (o >= HA && o < HA + MI) h.a[o - HA] = read3(nA, arow0 + 32 * (o - HA), nkk);
+    if (o == F) h.b[0] = read3(nB, bcol0, nkk);
+    if constexpr (NJ == 4) {
+      if (o == F + MI + 1) h.b[1] = read3(nB, bcol0 + 32, nkk);
+      if (o == F + 2 * MI) h.b[2] = read3(nB, bcol0 + 64, nkk);
+    }
     MOONEP_PIN();
   }
 }
 
-template <int J, int MI>
-__device__ __forceinline__ void kstep3(const RowTileT<2 * MI>& la, const RowTile& lb,
-                                       const Ring& ring, int j, int nk, Frag3<MI>& h, Frag3<MI>& l,
-                                       f32x16 acc[MI][4], int arow0, const int nrow[4]) {
-  const uint32_t koa = j + 1 < nk ? la.koff((int64_t)(j + 1) * BK) : kOob;
-  const uint32_t kob = j + 2 < nk ? lb.koff((int64_t)(j + 2) * BK) : kOob;
+template <int J, int MI, int NJ, bool kDeep>
+__device__ __forceinline__ void kstep3(const RowTileT<2 * MI>& la, const RowTileT<2 * NJ>& lb,
+                                       const Tile3<MI, NJ, kDeep>& ring, int j, int nk,
+                                       Frag3<MI, NJ>& h, Frag3<MI, NJ>& l, f32x16 acc[MI][NJ],
+                                       int arow0, int bcol0) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  const int ja = j + TL::kAheadA, jb = j + TL::kAheadB;
+  const uint32_t koa = ja < nk ? la.koff((int64_t)ja * BK) : kOob;
+  const uint32_t kob = jb < nk ? lb.koff((int64_t)jb * BK) : kOob;
   MOONEP_PIN();
-  khalf3<J, 0, MI>(la, lb, ring, koa, kob, h, l, acc, arow0, nrow);
-  khalf3<J, 1, MI>(la, lb, ring, koa, kob, h, l, acc, arow0, nrow);
+  khalf3<J, 0, MI, NJ, kDeep>(la, lb, ring, koa, kob, h, l, acc, arow0, bcol0);
+  khalf3<J, 1, MI, NJ, kDeep>(la, lb, ring, koa, kob, h, l, acc, arow0, bcol0);
 }
 
-// kTwoSums: the sum of every five steps (160 values of K) starts at zero and is added to `sum`
-// after them, in place of one chain over all of K.
-template <int MI, bool kTwoSums>
-__device__ __forceinline__ void gemm3_loop(const RowTileT<2 * MI>& la, const RowTile& lb,
-                                           const Ring& ring, int nk, f32x16 acc[MI][4], int arow0,
-                                           const int nrow[4]) {
-  lb.issue(ring.b<0>(), 0, true);
-  la.issue(ring.a<0>(), 0, true);
-  lb.issue(ring.b<1>(), BK, 1 < nk);
-  f32x16 sum[kTwoSums ? MI : 1][4];
-  if constexpr (kTwoSums) zero_acc<MI>(sum);
-  zero_acc<MI>(acc);
+// One step of a wave whose part of the tile is not wanted: its loads and barrier only.
+template <int J, int MI, int NJ, bool kDeep>
+__device__ __forceinline__ void kstep3_loads(const RowTileT<2 * MI>& la,
+                                             const RowTileT<2 * NJ>& lb,
+                                             const Tile3<MI, NJ, kDeep>& ring, int j, int nk) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  const int ja = j + TL::kAheadA, jb = j + TL::kAheadB;
+  la.issue(ring.template a<J + TL::kAheadA>(), (int64_t)ja * BK, ja < nk);
+  lb.issue(ring.template b<J + TL::kAheadB>(), (int64_t)jb * BK, jb < nk);
+  wait_dma<TL::kLater>();
+  barrier_reads_done();
+}
+
+// acc = U V^T of the tile.  kTwoSums: the sum of every five steps (160 values
+// of K) starts at zero and is added to `sum` after them, in place of one chain
+// over all of K.  idle: see kstep3_loads (acc is then not set).
+template <int MI, int NJ, bool kDeep, bool kTwoSums>
+__device__ __forceinline__ void gemm3_loop(const RowTileT<2 * MI>& la, const RowTileT<2 * NJ>& lb,
+                                           const Tile3<MI, NJ, kDeep>& ring, int nk,
+                                           f32x16 acc[MI][NJ], int arow0, int bcol0, bool idle) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  lb.issue(ring.template b<0>(), 0, true);
+  la.issue(ring.template a<0>(), 0, true);
+  lb.issue(ring.template b<1>(), BK, 1 < nk);
+  if constexpr (kDeep) {
+    la.issue(ring.template a<1>(), BK, 1 < nk);
+    lb.issue(ring.template b<2>(), 2 * BK, 2 < nk);
+    la.issue(ring.template a<2>(), 2 * BK, 2 < nk);
+    lb.issue(ring.template b<3>(), 3 * BK, 3 < nk);
+    la.issue(ring.template a<3>(), 3 * BK, 3 < nk);
+  }
+  if (idle) {
+    wait_dma<TL::kLater>();
+    barrier_reads_done();
+    for (int j = 0; j < nk; j += kSlots) {
+      kstep3_loads<0>(la, lb, ring, j, nk);
+      if (j + 1 < nk) kstep3_loads<1>(la, lb, ring, j + 1, nk);
+      if (j + 2 < nk) kstep3_loads<2>(la, lb, ring, j + 2, nk);
+      if (j + 3 < nk) kstep3_loads<3>(la, lb, ring, j + 3, nk);
+      if (j + 4 < nk) kstep3_loads<4>(la, lb, ring, j + 4, nk);
+    }
+    wait_loads<0>();
+    barrier_reads_done();
+    return;
+  }
+  f32x16 sum[kTwoSums ? MI : 1][NJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        acc[i][j][v] = 0.0f;
+        if constexpr (kTwoSums) sum[i][j][v] = 0.0f;
+      }
+      // cleared here, while the first tiles are in flight
       if constexpr (kTwoSums) asm volatile("" : "+a"(sum[i][j]));
       else asm volatile("" : "+a"(acc[i][j]));
     }
-  wait_loads<kLoadsPerStep>();
+  wait_dma<TL::kLater>();
   barrier_reads_done();
-  Frag3<MI> h, l;
+  Frag3<MI, NJ> h, l;
 #pragma unroll
-  for (int q = 0; q < 3; ++q) h.b[q] = read3(ring.b<0>(), nrow[q], 0);
+  for (int q = 0; q < NJ - 1; ++q) h.b[q] = read3(ring.template b<0>(), bcol0 + 32 * q, 0);
 #pragma unroll
-  for (int q = 0; q < MI; ++q) h.a[q] = read3(ring.a<0>(), arow0 + 32 * q, 0);
+  for (int q = 0; q < MI; ++q) h.a[q] = read3(ring.template a<0>(), arow0 + 32 * q, 0);
   for (int j = 0; j < nk; j += kSlots) {
-    kstep3<0, MI>(la, lb, ring, j, nk, h, l, acc, arow0, nrow);
-    if (j + 1 < nk) kstep3<1, MI>(la, lb, ring, j + 1, nk, h, l, acc, arow0, nrow);
-    if (j + 2 < nk) kstep3<2, MI>(la, lb, ring, j + 2, nk, h, l, acc, arow0, nrow);
-    if (j + 3 < nk) kstep3<3, MI>(la, lb, ring, j + 3, nk, h, l, acc, arow0, nrow);
-    if (j + 4 < nk) kstep3<4, MI>(la, lb, ring, j + 4, nk, h, l, acc, arow0, nrow);
+    kstep3<0>(la, lb, ring, j, nk, h, l, acc, arow0, bcol0);
+    if (j + 1 < nk) kstep3<1>(la, lb, ring, j + 1, nk, h, l, acc, arow0, bcol0);
+    if (j + 2 < nk) kstep3<2>(la, lb, ring, j + 2, nk, h, l, acc, arow0, bcol0);
+    if (j + 3 < nk) kstep3<3>(la, lb, ring, j + 3, nk, h, l, acc, arow0, bcol0);
+    if (j + 4 < nk) kstep3<4>(la, lb, ring, j + 4, nk, h, l, acc, arow0, bcol0);
     if constexpr (kTwoSums) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
+        for (int jj = 0; jj < NJ; ++jj) {
           sum[i][jj] += acc[i][jj];
           asm volatile("" : "+a"(sum[i][jj]));
 #pragma unroll
@@ -176,10 +264,10 @@ __device__ __forceinline__ void gemm3_loop(const RowTileT<2 * MI>& la, const Row
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) acc[i][jj] = sum[i][jj];
+      for (int jj = 0; jj < NJ; ++jj) acc[i][jj] = sum[i][jj];
   }
   wait_loads<0>();
-  __syncthreads();
+  barrier_reads_done();
 }
 
 // ---------------------------------------------------------- epilogue pieces
@@ -204,26 +292,19 @@ __device__ __forceinline__ void put_row4(lds_t* blk, int r, int c, const f16x4& 
   *(__attribute__((address_space(3))) u32x2*)(blk + blk_off(r, 64 + 2 * c)) =
       __builtin_bit_cast(u32x2, lo);
 }
-// the same four values as column r, rows c .. c + 3
-__device__ __forceinline__ void put_col4(lds_t* blk, int r, int c, const f16x4& hi,
-                                         const f16x4& lo) {
+// 16 bytes of the staged block's transpose: its row n0 + lane % 16, its columns 8 g .. 8 g + 7 (g
+// = lane / 16), hi or lo, by the transposing LDS read (lane q of 16 points at row k0 + q / 4,
+// columns n0 + 4 (q % 4) .. + 3 and gets column n0 + q, rows k0 .. k0 + 3)
+__device__ __forceinline__ u32x4 read_transposed(const lds_t* blk, int n0, int lo) {
+  const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
+  i16x4 h[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    *(__attribute__((address_space(3))) _Float16*)(blk + blk_off(c + e, 2 * r)) = hi[e];
-    *(__attribute__((address_space(3))) _Float16*)(blk + blk_off(c + e, 64 + 2 * r)) = lo[e];
+  for (int t = 0; t < 2; ++t) {
+    const int off = blk_off(8 * g + 4 * t + (q >> 2), 64 * lo + 2 * (n0 + 4 * (q & 3)));
+    h[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) i16x4*)(blk + off));
   }
-}
-// the part on and above the diagonal of a diagonal block, and its mirror image
-__device__ __forceinline__ void put_diag4(lds_t* blk, int r, int c, const f16x4& hi,
-                                          const f16x4& lo) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (c + e < r) continue;
-    *(__attribute__((address_space(3))) _Float16*)(blk + blk_off(r, 2 * (c + e))) = hi[e];
-    *(__attribute__((address_space(3))) _Float16*)(blk + blk_off(r, 64 + 2 * (c + e))) = lo[e];
-    *(__attribute__((address_space(3))) _Float16*)(blk + blk_off(c + e, 2 * r)) = hi[e];
-    *(__attribute__((address_space(3))) _Float16*)(blk + blk_off(c + e, 64 + 2 * r)) = lo[e];
-  }
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 // a staged block to rows row0 .. row0 + 31 (those below `rows`) of a pair matrix, block column cb
 __device__ __forceinline__ void flush_block(const lds_t* blk, uint16_t* dst, int64_t ld, int row0,
@@ -236,21 +317,172 @@ __device__ __forceinline__ void flush_block(const lds_t* blk, uint16_t* dst, int
     if (row0 + r < rows) *(u32x4*)(dst + (int64_t)(row0 + r) * ld + cb * 64 + ch * 8) = v;
   }
 }
+// its transpose likewise
+__device__ __forceinline__ void flush_transposed(const lds_t* blk, uint16_t* dst, int64_t ld,
+                                                 int row0, int rows, int cb) {
+  const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int lo = t & 1, r = 16 * (t >> 1) + q;
+    const u32x4 v = read_transposed(blk, 16 * (t >> 1), lo);
+    if (row0 + r < rows) *(u32x4*)(dst + (int64_t)(row0 + r) * ld + cb * 64 + 32 * lo + 8 * g) = v;
+  }
+}
+// a block on the diagonal: the part below it from the transpose, so that the
+// matrix is symmetric to the bit
+__device__ __forceinline__ void flush_diagonal(const lds_t* blk, uint16_t* dst, int64_t ld,
+                                               int row0, int rows, int cb) {
+  const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int lo = t & 1, r = 16 * (t >> 1) + q;
+    const i16x8 m = __builtin_bit_cast(i16x8, read_transposed(blk, 16 * (t >> 1), lo));
+    i16x8 v = *(const __attribute__((address_space(3))) i16x8*)(blk + blk_off(r, 64 * lo + 16 * g));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (8 * g + e < r) v[e] = m[e];
+    if (row0 + r < rows)
+      *(i16x8*)(dst + (int64_t)(row0 + r) * ld + cb * 64 + 32 * lo + 8 * g) = v;
+  }
+}
+
+// The lane's elements of a 32 x 32 block of a pair matrix, in the layout of the accumulators
+// (row lane % 32; v = 4 q + e holds column 8 q + 4 (lane / 32) + e): 16-byte loads of whole
+// chunks, whose halves the two lanes of a row then trade.
+struct PairBlock {
+  u32x4 c[2][2];                                      // [hi, lo][chunk pair]
+  __device__ __forceinline__ void load(const uint16_t* rowp, int cb) {
+    const int lh = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) c[t][p] = *(const u32x4*)(rowp + cb * 64 + 32 * t + 8 * (2 * p + lh));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) c[t][p] = u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void trade() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const auto r = __builtin_amdgcn_permlane32_swap(c[t][p][d], c[t][p][2 + d], false, false);
+          c[t][p][d] = r[0];                          // q = 2 p, dword d
+          c[t][p][2 + d] = r[1];                      // q = 2 p + 1
+        }
+  }
+  __device__ __forceinline__ float value(int v) const {
+    const int q = v >> 2, e = v & 3;
+    const unsigned hw = c[0][q >> 1][2 * (q & 1) + (e >> 1)];
+    const unsigned lw = c[1][q >> 1][2 * (q & 1) + (e >> 1)];
+    const uint16_t hb = (uint16_t)(e & 1 ? hw >> 16 : hw), lb = (uint16_t)(e & 1 ? lw >> 16 : lw);
+    return (float)__builtin_bit_cast(_Float16, hb) + (float)__builtin_bit_cast(_Float16, lb);
+  }
+};
 
 // ------------------------------------------------------------ m x m products
-// out = alpha U V^T + beta in, symmetric, for nmat matrices and one or two
-// problems (operand and result sets) in one launch.
+// One tile of out = alpha U V^T, or I + alpha U V^T + beta in (kIn), a symmetric m x m matrix of
+// which the tile's part on and above the diagonal is computed and written twice.
+struct SymTile {
+  const uint16_t* u;
+  const uint16_t* v;
+  const uint16_t* in;
+  uint16_t* out;
+  float alpha, beta;
+  int m, uld, ld, nk;        // rows; row strides of u, v and of in, out; K steps
+  int m0, n0;                // the tile's first row and column
+};
+
+template <int MI, int NJ, bool kDeep, bool kTwoSums, bool kIn>
+__device__ __forceinline__ void sym_tile(const SymTile& a, const Tile3<MI, NJ, kDeep>& ring) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  const int m0 = a.m0, n0 = a.n0;
+  const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
+  const int arow0 = wm * 32 * MI, bcol0 = wn * 32 * NJ;
+  // a wave wholly below the diagonal or outside the matrix
+  const bool idle = n0 + bcol0 + 32 * NJ <= m0 + arow0 || m0 + arow0 >= a.m || n0 + bcol0 >= a.m;
+
+  RowTileT<2 * MI> la;
+  RowTileT<2 * NJ> lb;
+  la.init(a.u + (int64_t)m0 * a.uld, a.uld, a.m - m0 < TL::kRows ? a.m - m0 : TL::kRows);
+  lb.init(a.v + (int64_t)n0 * a.uld, a.uld, a.m - n0 < TL::kCols ? a.m - n0 : TL::kCols);
+  f32x16 acc[MI][NJ];
+  gemm3_loop<MI, NJ, kDeep, kTwoSums>(la, lb, ring, a.nk, acc, arow0, bcol0, idle);
+  if (idle) return;
+
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  lds_t* stage = ring.base + wave * TL::kWaveLds;
+  static_assert(NJ * kBlockBytes <= TL::kWaveLds, "a row of blocks is staged");
+  const int ncb = a.ld / 64;                             // blocks along a row
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int row0 = m0 + arow0 + 32 * i, row = row0 + lr;
+    PairBlock in[kIn ? NJ : 1];
+    if constexpr (kIn) {
+      const uint16_t* rowp = a.in + (int64_t)row * a.ld;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        in[j].zero();
+        if (row < a.m && (n0 + bcol0) / 32 + j < ncb) in[j].load(rowp, (n0 + bcol0) / 32 + j);
+      }
+      MOONEP_PIN();
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int col0 = n0 + bcol0 + 32 * j;
+      if (col0 < row0 || col0 / 32 >= ncb) continue;     // below the diagonal its mirror is written
+      if constexpr (kIn) in[j].trade();
+#pragma unroll
+      for (int qd = 0; qd < 4; ++qd) {
+        const int c = acc_col(qd, lh);
+        f16x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = a.alpha * acc[i][j][4 * qd + e];
+          if constexpr (kIn) {
+            v = __builtin_fmaf(a.beta, in[j].value(4 * qd + e), v);
+            if (row == col0 + c + e && row < a.m) v += kScale;
+          }
+          _Float16 h, l;
+          split(v, h, l);
+          hi[e] = h;
+          lo[e] = l;
+        }
+        put_row4(stage + j * kBlockBytes, lr, c, hi, lo);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int col0 = n0 + bcol0 + 32 * j;
+      if (col0 < row0 || col0 / 32 >= ncb) continue;
+      if (col0 == row0) {
+        flush_diagonal(stage + j * kBlockBytes, a.out, a.ld, row0, a.m, col0 / 32);
+      } else {
+        flush_block(stage + j * kBlockBytes, a.out, a.ld, row0, a.m, col0 / 32);
+        if (row0 / 32 < ncb)
+          flush_transposed(stage + j * kBlockBytes, a.out, a.ld, col0, a.m, row0 / 32);
+      }
+    }
+    MOONEP_PIN();
+  }
+}
+
+// One product for nmat matrices, one or two problems (operand and result sets) per launch.
 struct SymArgs {
   const uint16_t* u[2];
   const uint16_t* v[2];
-  const uint16_t* in[2];     // null: no second term
   uint16_t* out[2];
-  uint16_t* out_id;          // null, or where out + I goes (first problem)
+  const uint16_t* in;        // (kIn, one problem)
   int64_t ustride;           // elements between matrices of u and v
-  int64_t ostride;           // of in, out and out_id
+  int64_t ostride;           // of in and out
   float alpha, beta;
-  int m, uld, ld, nk;        // rows; row strides of u, v and of in, out; K steps
-  int nt, tiles, nmat;       // tiles per side, upper tiles per matrix, matrices
+  int m, uld, ld, nk;        // as in SymTile
+  int nt, tiles, nmat;       // tile columns, tiles per matrix, matrices
   int64_t total;             // workgroups in use
 };
 
@@ -261,102 +493,88 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t total) {
   return c < per && t < total ? t : -1;
 }
 
-// MI = 4: tiles of 256 x 256; MI = 2 (the first product, with two sums): the
-// upper and the lower half of such a tile are a workgroup each.
-template <int MI>
+// The tiles of a matrix cover the part on and above the diagonal, by columns
+// of tiles NJ / MI rows of tiles high.
+template <int MI, int NJ, bool kDeep, bool kTwoSums, bool kIn>
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1))) void ortho_sym(SymArgs a) {
-  MOONEP_RING(smem);
-  constexpr int kRows = 64 * MI;
+                          amdgpu_waves_per_eu(Tile3<MI, NJ, kDeep>::kWavesPerSimd,
+                                              Tile3<MI, NJ, kDeep>::kWavesPerSimd)))
+void ortho_sym(SymArgs a) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  __shared__ __attribute__((aligned(16))) char lds_mem[TL::kLds];
+  const TL ring = {(lds_t*)lds_mem};
   const int64_t t = xcd_tile(a.total);
   if (t < 0) return;
   const int64_t mat = t / a.tiles;
   int q = (int)(t - mat * a.tiles), ti = 0;
-  const int part = q % (4 / MI);
-  q /= 4 / MI;
+  const int part = q % (NJ / MI);
+  q /= NJ / MI;
   for (; q >= a.nt - ti; ++ti) q -= a.nt - ti;
-  const int tj = ti + q;
   const int pr = mat >= a.nmat ? 1 : 0;
   const int64_t mi = mat - (pr ? a.nmat : 0);
-  const uint16_t* U = a.u[pr] + mi * a.ustride;
-  const uint16_t* V = a.v[pr] + mi * a.ustride;
-  const uint16_t* in = a.in[pr] ? a.in[pr] + mi * a.ostride : nullptr;
-  uint16_t* out = a.out[pr] + mi * a.ostride;
-  uint16_t* out_id = a.out_id && !pr ? a.out_id + mi * a.ostride : nullptr;
-  const int m0 = ti * BM + part * kRows, n0 = tj * BN;
-  if (m0 >= a.m) return;
-  const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
-  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
+  SymTile s;
+  s.u = a.u[pr] + mi * a.ustride;
+  s.v = a.v[pr] + mi * a.ustride;
+  s.in = a.in + mi * a.ostride;
+  s.out = a.out[pr] + mi * a.ostride;
+  s.alpha = a.alpha; s.beta = a.beta;
+  s.m = a.m; s.uld = a.uld; s.ld = a.ld; s.nk = a.nk;
+  s.m0 = ti * TL::kCols + part * TL::kRows;
+  s.n0 = (ti + q) * TL::kCols;
+  if (s.m0 < a.m) sym_tile<MI, NJ, kDeep, kTwoSums, kIn>(s, ring);
+}
 
-  RowTileT<2 * MI> la;
-  RowTile lb;
-  la.init(U + (int64_t)m0 * a.uld, a.uld, a.m - m0 < kRows ? a.m - m0 : kRows);
-  lb.init(V + (int64_t)n0 * a.uld, a.uld, a.m - n0 < BN ? a.m - n0 : BN);
-  f32x16 acc[MI][4];
-  gemm3_loop<MI, MI == 2>(la, lb, smem, a.nk, acc, wm * 32 * MI, nrow);
+// Matrices of one tile (m <= 128): a workgroup takes all products of its matrix, which saves
+// fourteen launches (four 128 x 256 matrices: 144 us without, 131 us with).  Its own stores are seen after a workgroup barrier.
+constexpr int kChainM = 128;
+struct ChainArgs {
+  const uint16_t* x;         // [nmat] X_0
+  uint16_t* sq[5];           // [nmat] m x m each: A, R, T, P and P again
+  int64_t xstride, ostride;
+  int m, xld, ld, steps;
+  float coef[MOONEP_ORTHO_MAX_STEPS][3];
+};
 
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  lds_t* direct = smem.base + wave * (8 * kBlockBytes);
-  lds_t* mirror = direct + 4 * kBlockBytes;
-  const int ncb = a.ld / 64;                                // blocks along a row
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int row0 = m0 + wm * 32 * MI + 32 * i, row = row0 + lr;
-    // one row of blocks: 4 blocks of this wave; with out_id, a second round for out + I
-    f16x4 ih[4][4], il[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int qd = 0; qd < 4; ++qd) {
-        const int cb = (n0 + nrow[j]) / 32;
-        ih[j][qd] = f16x4{0, 0, 0, 0};
-        il[j][qd] = f16x4{0, 0, 0, 0};
-        if (in && row < a.m && cb < ncb) {
-          const uint16_t* s = in + (int64_t)row * a.ld + cb * 64 + acc_col(qd, lh);
-          ih[j][qd] = *(const f16x4*)s;
-          il[j][qd] = *(const f16x4*)(s + 32);
-        }
-      }
-    MOONEP_PIN();
-    const int rounds = out_id ? 2 : 1;
-    for (int rd = 0; rd < rounds; ++rd) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col0 = n0 + nrow[j];
-        if (col0 < row0) continue;                       // below the diagonal: its mirror is written
-#pragma unroll
-        for (int qd = 0; qd < 4; ++qd) {
-          const int c = acc_col(qd, lh);
-          f16x4 hi, lo;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = a.alpha * acc[i][j][4 * qd + e];
-            v += a.beta * ((float)ih[j][qd][e] + (float)il[j][qd][e]);
-            if (rd && row == col0 + c + e && row < a.m) v += kScale;
-            _Float16 h, l;
-            split(v, h, l);
-            hi[e] = h;
-            lo[e] = l;
-          }
-          if (col0 == row0) {
-            put_diag4(direct + j * kBlockBytes, lr, c, hi, lo);
-          } else {
-            put_row4(direct + j * kBlockBytes, lr, c, hi, lo);
-            put_col4(mirror + j * kBlockBytes, lr, c, hi, lo);
-          }
-        }
-      }
-      uint16_t* dst = rd ? out_id : out;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col0 = n0 + nrow[j];
-        if (col0 < row0) continue;
-        if (col0 / 32 < ncb) flush_block(direct + j * kBlockBytes, dst, a.ld, row0, a.m, col0 / 32);
-        if (col0 != row0 && row0 / 32 < ncb)
-          flush_block(mirror + j * kBlockBytes, dst, a.ld, col0, a.m, row0 / 32);
-      }
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
+                          amdgpu_waves_per_eu(1, 1))) void ortho_chain(ChainArgs a) {
+  typedef Tile3<2, 2, true> TL;
+  __shared__ __attribute__((aligned(16))) char lds_mem[TL::kLds];
+  const TL ring = {(lds_t*)lds_mem};
+  const int64_t off = (int64_t)blockIdx.x * a.ostride;
+  uint16_t *A = a.sq[0] + off, *Tm = a.sq[2] + off, *P = a.sq[3] + off, *P2 = a.sq[4] + off;
+  SymTile s;
+  s.u = s.v = a.x + (int64_t)blockIdx.x * a.xstride;
+  s.in = nullptr;
+  s.out = A;
+  s.alpha = 1.0f / kScale; s.beta = 0.0f;
+  s.m = a.m; s.uld = a.xld; s.ld = a.ld; s.nk = a.xld / BK;
+  s.m0 = 0; s.n0 = 0;
+  sym_tile<2, 2, true, true, false>(s, ring);
+  s.uld = a.ld; s.nk = a.ld / BK;
+  for (int i = 0; i < a.steps; ++i) {
+    const float ca = a.coef[i][0], cb = a.coef[i][1], cc = a.coef[i][2];
+    uint16_t* R = i == 0 ? P : a.sq[1] + off;
+    __syncthreads();
+    s.u = s.v = s.in = A;
+    s.out = R;
+    s.alpha = cc / ca / kScale; s.beta = cb / ca;
+    sym_tile<2, 2, true, false, true>(s, ring);
+    s.in = nullptr;
+    s.u = R;
+    // T = R A, P2 = R P, A = a^2 R T; the last step only needs the second, the first has it
+    for (int k = i + 1 < a.steps ? 0 : 1; k < (i + 1 < a.steps ? 3 : 2); ++k) {
+      if (k == 1 && i == 0) continue;
+      __syncthreads();
+      s.v = k == 0 ? A : k == 1 ? P : Tm;
+      s.out = k == 0 ? Tm : k == 1 ? P2 : A;
+      s.alpha = (k == 2 ? ca * ca : 1.0f) / kScale;
+      sym_tile<2, 2, true, false, false>(s, ring);
     }
-    MOONEP_PIN();
+    if (i > 0) {
+      uint16_t* t = P;
+      P = P2;
+      P2 = t;
+    }
   }
 }
 
@@ -372,57 +590,64 @@ struct OutArgs {
   int64_t total;
 };
 
+template <int MI, int NJ, bool kDeep>
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1))) void ortho_out(OutArgs a) {
-  MOONEP_RING(smem);
+                          amdgpu_waves_per_eu(Tile3<MI, NJ, kDeep>::kWavesPerSimd,
+                                              Tile3<MI, NJ, kDeep>::kWavesPerSimd)))
+void ortho_out(OutArgs a) {
+  typedef Tile3<MI, NJ, kDeep> TL;
+  __shared__ __attribute__((aligned(16))) char lds_mem[TL::kLds];
+  const TL ring = {(lds_t*)lds_mem};
   const int64_t t = xcd_tile(a.total);
   if (t < 0) return;
   const int per = a.ntm * a.ntn;
   const int64_t mi = t / per;
   const int q = (int)(t - mi * per), tm = q / a.ntn, tn = q % a.ntn;
-  const int m0 = tm * BM, n0 = tn * BN;
+  const int m0 = tm * TL::kRows, n0 = tn * TL::kCols;
   const int wave = wave_id(), wm = wave >> 1, wn = wave & 1;
-  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
-  const int rows_valid = a.mu - m0 < BM ? a.mu - m0 : BM;
-  const int cols_valid = a.mv - n0 < BN ? a.mv - n0 : BN;
+  const int arow0 = wm * 32 * MI, bcol0 = wn * 32 * NJ;
+  const int rows_valid = a.mu - m0 < TL::kRows ? a.mu - m0 : TL::kRows;
+  const int cols_valid = a.mv - n0 < TL::kCols ? a.mv - n0 : TL::kCols;
+  const bool idle = arow0 >= rows_valid || bcol0 >= cols_valid;
 
-  RowTile la, lb;
+  RowTileT<2 * MI> la;
+  RowTileT<2 * NJ> lb;
   la.init(a.u + mi * a.ustride + (int64_t)m0 * a.ld, a.ld, rows_valid);
   lb.init(a.v + mi * a.vstride + (int64_t)n0 * a.ld, a.ld, cols_valid);
-  f32x16 acc[4][4];
-  gemm3_loop<4, false>(la, lb, smem, a.nk, acc, wm * 128, nrow);
+  f32x16 acc[MI][NJ];
+  gemm3_loop<MI, NJ, kDeep, false>(la, lb, ring, a.nk, acc, arow0, bcol0, idle);
+  if (idle) return;
 
   uint16_t* out = a.out + (mi * a.mu + m0) * (int64_t)a.mv + n0;
-  if (a.wide) {
-    typedef Stage<128, 128> St;
-    lds_t* reg = smem.base + wave * St::kBytes;
+  typedef Stage<32 * MI, 32 * NJ> St;
+  static_assert(St::kBytes <= TL::kWaveLds, "a wave's sub-tile is staged in its share of the ring");
+  lds_t* reg = ring.base + wave * TL::kWaveLds;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int qd = 0; qd < 4; ++qd)
-          St::put(reg, i, j, qd,
-                  pack_bf16x2(a.alpha * acc[i][j][4 * qd], a.alpha * acc[i][j][4 * qd + 1]),
-                  pack_bf16x2(a.alpha * acc[i][j][4 * qd + 2], a.alpha * acc[i][j][4 * qd + 3]));
-    St::flush(reg, make_rsrc(out, (int64_t)rows_valid * a.mv * 2), wm * 128, a.mv, wn * 128,
-              cols_valid);
-    return;
-  }
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int qd = 0; qd < 4; ++qd)
+        St::put(reg, i, j, qd,
+                pack_bf16x2(a.alpha * acc[i][j][4 * qd], a.alpha * acc[i][j][4 * qd + 1]),
+                pack_bf16x2(a.alpha * acc[i][j][4 * qd + 2], a.alpha * acc[i][j][4 * qd + 3]));
+  if (a.wide) {
+    St::flush(reg, make_rsrc(out, (int64_t)rows_valid * a.mv * 2), arow0, a.mv, bcol0, cols_valid);
+    return;
+  }
+  // rows that do not start on 16 bytes: one column per lane
+  const int lane = threadIdx.x & 63;
+  constexpr int kPer = 64 / (32 * NJ) > 0 ? 64 / (32 * NJ) : 1;      // rows per store
+  for (int r0 = 0; r0 < 32 * MI; r0 += kPer)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = wm * 128 + 32 * i + lr, c = nrow[j] + acc_col(qd, lh) + e;
-          if (r < rows_valid && c < cols_valid)
-            out[(int64_t)r * a.mv + c] =
-                __builtin_bit_cast(uint16_t, (__bf16)(a.alpha * acc[i][j][4 * qd + e]));
-        }
+    for (int c0 = 0; c0 < 32 * NJ; c0 += 64) {
+      const int r = r0 + lane / (64 / kPer), c = c0 + lane % (64 / kPer);
+      const int off = r * St::kRowBytes + (c >> 3) * 16 + 8 * (((c >> 2) & 1) ^ ((r >> 4) & 1)) +
+                      2 * (c & 3);
+      const uint16_t v = *(const __attribute__((address_space(3))) uint16_t*)(reg + off);
+      if (arow0 + r < rows_valid && bcol0 + c < cols_valid)
+        out[(int64_t)(arow0 + r) * a.mv + bcol0 + c] = v;
+    }
 }
 
 // --------------------------------------------------------------- first passes
@@ -464,10 +689,12 @@ __global__ __launch_bounds__(kThreads) void ortho_norm(const T* g, int64_t elems
   if (threadIdx.x == 0) part[(int64_t)blockIdx.y * kParts + blockIdx.x] = sh[0] + sh[1] + sh[2] + sh[3];
 }
 
-// X_0 in both orientations as pairs: a 64 x 64 piece of G per workgroup.
+// X_0 in both orientations as pairs: a 64 x 64 piece of G per workgroup.  A lane
+// stores 16 bytes, hi or lo of eight values, so that eight lanes write a whole
+// 128-byte block row.
 template <class T>
 __global__ __launch_bounds__(kThreads) void ortho_load(const T* g, int rows, int cols, float eps,
-                                                       const double* part, uint16_t* nat,
+                                                       int wide, const double* part, uint16_t* nat,
                                                        uint16_t* tr, int64_t nat_stride,
                                                        int64_t tr_stride) {
   __shared__ float tile[64][65];
@@ -475,48 +702,65 @@ __global__ __launch_bounds__(kThreads) void ortho_load(const T* g, int rows, int
   const int64_t mi = blockIdx.z;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
   double s = part[mi * kParts + tid];
+  const T* p = g + mi * rows * (int64_t)cols;
+  float x[4][4];
+  struct __attribute__((aligned(4 * sizeof(T)))) Four {
+    T v[4];
+  };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int r = r0 + (tid >> 4) + 16 * u, c = c0 + 4 * (tid & 15);
+    const T* q = p + (int64_t)r * cols + c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[u][e] = 0.0f;
+    if (r < rows) {
+      if (wide) {
+        if (c < cols) {
+          const Four v = *(const Four*)q;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = to_f32<T>(v.v[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < cols) x[u][e] = to_f32<T>(q[e]);
+      }
+    }
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
   if ((tid & 63) == 0) sh[tid >> 6] = s;
-  const T* p = g + mi * rows * (int64_t)cols;
-  float x[16];
-#pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const int r = r0 + (tid >> 6) + 4 * u, c = c0 + (tid & 63);
-    x[u] = r < rows && c < cols ? to_f32<T>(p[(int64_t)r * cols + c]) : 0.0f;
-  }
   __syncthreads();
   const double f = (double)kScale / (sqrt(sh[0] + sh[1] + sh[2] + sh[3]) + (double)eps);
 #pragma unroll
-  for (int u = 0; u < 16; ++u)
-    tile[(tid >> 6) + 4 * u][tid & 63] = (float)((double)x[u] * f);
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      tile[(tid >> 4) + 16 * u][4 * (tid & 15) + e] = (float)((double)x[u][e] * f);
   __syncthreads();
   const int nld = (cols + kK - 1) / kK * 64, tld = (rows + kK - 1) / kK * 64;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int unit = tid + kThreads * (u & 1);      // 64 rows x 8 groups of 8 columns
-    const int r = unit >> 3, c = (unit & 7) * 8;
-    const bool t = u >= 2;                          // then the transposed copy
-    const int row = (t ? c0 : r0) + r, col = (t ? r0 : c0) + c;
-    const int nrows = t ? cols : rows, ld = t ? tld : nld;
-    if (row >= nrows || col / 32 * 64 >= ld) continue;
-    f16x8 hi, lo;
+  for (int u = 0; u < 8; ++u) {
+    const bool t = u >= 4;                          // then the transposed copy
+    const int unit = tid + kThreads * (u & 3);      // 64 rows x 2 blocks x 8 pieces
+    const int r = unit >> 4, kb = unit >> 3 & 1, piece = unit & 7, c = 32 * kb + 8 * (piece & 3);
+    const int row = (t ? c0 : r0) + r, blk = (t ? r0 : c0) / 32 + kb;
+    if (row >= (t ? cols : rows) || blk * 64 >= (t ? tld : nld)) continue;
+    f16x8 v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       _Float16 h, l;
       split(t ? tile[c + e][r] : tile[r][c + e], h, l);
-      hi[e] = h;
-      lo[e] = l;
+      v[e] = piece < 4 ? h : l;
     }
-    uint16_t* d = (t ? tr + mi * tr_stride : nat + mi * nat_stride) + (int64_t)row * ld +
-                  col / 32 * 64 + (col & 31);
-    *(f16x8*)d = hi;
-    *(f16x8*)(d + 32) = lo;
+    uint16_t* d = t ? tr + mi * tr_stride + (int64_t)row * tld : nat + mi * nat_stride + (int64_t)row * nld;
+    *(f16x8*)(d + blk * 64 + piece * 8) = v;
   }
 }
 
 // --------------------------------------------------------------------- host
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int ceil_div(int v, int m) { return (v + m - 1) / m; }
 
 struct OrthoLayout {
   int m, n;                       // shorter and longer side
@@ -536,14 +780,53 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
   o.xt = up((int64_t)o.n * o.sld, 128);
   o.sq = up((int64_t)o.m * o.sld, 128);
   o.bytes = 2 * (o.x + o.xt + 5 * o.sq) + kParts * (int64_t)sizeof(double);
-  // Matrices per launch: enough for 8 rounds of tiles on the 256 CUs (the last round is then
-  // at most an eighth of the work); more would only take more memory.
-  const int64_t nt = (o.m + BM - 1) / BM, tiles = nt * (nt + 1) / 2;
+  // Matrices per launch: enough for 8 rounds of 256-wide tiles on the 256 CUs (the last round
+  // is then at most an eighth of the work); more would only take more memory.
+  const int64_t nt = ceil_div(o.m, 256), tiles = nt * (nt + 1) / 2;
   const int64_t cap = (2048 + tiles - 1) / tiles;
   const int64_t groups = n < 1 ? 1 : (n + cap - 1) / cap;
   o.group = n < 1 ? 1 : (int)((n + groups - 1) / groups);
   return o;
 }
+
+constexpr int kCus = 256;
+
+template <int MI, int NJ, bool kTwoSums, bool kIn>
+void run_sym(SymArgs& a, int problems, hipStream_t s) {
+  a.nt = ceil_div(a.m, 64 * NJ);
+  a.tiles = NJ / MI * (a.nt * (a.nt + 1) / 2);
+  a.total = (int64_t)problems * a.nmat * a.tiles;
+  const unsigned grid = (unsigned)pad_grid(a.total);
+  if constexpr (MI == 2 && NJ == 2) {
+    if (a.total <= kCus) {
+      ortho_sym<MI, NJ, true, kTwoSums, kIn><<<grid, kThreads, 0, s>>>(a);
+      return;
+    }
+  }
+  ortho_sym<MI, NJ, false, kTwoSums, kIn><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int MI, int NJ>
+void run_out(OutArgs& r, hipStream_t s) {
+  r.ntm = ceil_div(r.mu, 64 * MI);
+  r.ntn = ceil_div(r.mv, 64 * NJ);
+  r.total = (int64_t)r.nmat * r.ntm * r.ntn;
+  const unsigned grid = (unsigned)pad_grid(r.total);
+  if constexpr (MI == 2 && NJ == 2) {
+    if (r.total <= kCus) {
+      ortho_out<MI, NJ, true><<<grid, kThreads, 0, s>>>(r);
+      return;
+    }
+  }
+  ortho_out<MI, NJ, false><<<grid, kThreads, 0, s>>>(r);
+}
+
+// 256-wide tiles from two rounds of them on; below, 128-wide ones fill the chip more evenly and
+// two of their workgroups on a CU hide each other's prologue and epilogue.  Five steps on 32, 16
+// and 8 matrices of 2048 x 4096 (1152, 576, 288 tiles): 18.5, 9.7, 5.6 ms with 256-wide tiles,
+// 19.8, 10.0, 5.1 ms with 128-wide ones; 32 of 1024 x 2048 (320 tiles): 3.35 and 3.08 ms; one of
+// 512 x 1024: 0.67 and 0.25 ms.
+bool use_large(int64_t tiles256) { return tiles256 >= 512; }
 
 template <class T>
 hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co, int steps,
@@ -562,62 +845,74 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     const int nm = n - i0 < o.group ? n - i0 : o.group;
     const T* gi = g + i0 * elems;
     const bool al = (uintptr_t)gi % 16 == 0 && elems % N == 0;
+    const int wide = (uintptr_t)gi % (4 * sizeof(T)) == 0 && cols % 4 == 0;
     ortho_norm<T><<<dim3(kParts, nm), kThreads, 0, s>>>(gi, elems, al ? elems / N : 0, part);
-    ortho_load<T><<<dim3((cols + 63) / 64, (rows + 63) / 64, nm), kThreads, 0, s>>>(
-        gi, rows, cols, eps, part, tall ? xt : x, tall ? x : xt, tall ? o.xt : o.x,
+    ortho_load<T><<<dim3(ceil_div(cols, 64), ceil_div(rows, 64), nm), kThreads, 0, s>>>(
+        gi, rows, cols, eps, wide, part, tall ? xt : x, tall ? x : xt, tall ? o.xt : o.x,
         tall ? o.x : o.xt);
 
+    const int64_t nt = ceil_div(o.m, 256);
+    const bool large = use_large(nm * (nt * (nt + 1) / 2));
+    const bool chain = o.m <= kChainM;
     SymArgs a;
     a.m = o.m;
     a.ld = o.sld;
     a.ostride = o.sq;
-    a.nt = (o.m + BM - 1) / BM;
-    a.tiles = a.nt * (a.nt + 1) / 2;
     a.nmat = nm;
-    auto sym = [&](int problems) {
-      a.total = (int64_t)problems * nm * a.tiles;
-      ortho_sym<4><<<(unsigned)pad_grid(a.total), kThreads, 0, s>>>(a);
+    auto set = [&](int i, const uint16_t* u, const uint16_t* v, uint16_t* to) {
+      a.u[i] = u; a.v[i] = v; a.out[i] = to;
     };
-    auto set = [&](int i, const uint16_t* u, const uint16_t* v, const uint16_t* in, uint16_t* to) {
-      a.u[i] = u; a.v[i] = v; a.in[i] = in; a.out[i] = to;
+    auto product = [&](int problems) {
+      if (large) run_sym<4, 4, false, false>(a, problems, s);
+      else run_sym<2, 2, false, false>(a, problems, s);
     };
-    uint16_t *A = sq[0], *B = sq[1], *Tm = sq[2], *P = sq[3], *P2 = sq[4];
-    // The first product: a chain of fp32 additions over all of K would round by 2e-7 .. 7e-7
-    // of the sum, which a low-rank result shows thousands of times larger.
-    set(0, x, x, nullptr, A);
-    set(1, nullptr, nullptr, nullptr, nullptr);
-    a.out_id = nullptr;
+    uint16_t *A = sq[0], *R = sq[1], *Tm = sq[2], *P = sq[3], *P2 = sq[4];
+    // The first product with two sums: a chain of fp32 additions over all of n would round by
+    // 2e-7 .. 7e-7 of the sum, which a low-rank result shows thousands of times larger.
+    set(0, x, x, A);
+    set(1, x, x, A);
+    a.in = A;
     a.ustride = o.x; a.uld = o.xld; a.nk = o.xld / BK;
     a.alpha = 1.0f / kScale; a.beta = 0.0f;
-    a.tiles = 2 * (a.nt * (a.nt + 1) / 2);
-    a.total = (int64_t)nm * a.tiles;
-    ortho_sym<2><<<(unsigned)pad_grid(a.total), kThreads, 0, s>>>(a);
-    a.tiles /= 2;
+    if (chain) {
+      ChainArgs c;
+      c.x = x;
+      for (int i = 0; i < 5; ++i) c.sq[i] = sq[i];
+      c.xstride = o.x; c.ostride = o.sq;
+      c.m = o.m; c.xld = o.xld; c.ld = o.sld; c.steps = steps;
+      for (int i = 0; i < 3 * steps; ++i) c.coef[i / 3][i % 3] = co[i];
+      ortho_chain<<<(unsigned)nm, kThreads, 0, s>>>(c);
+    } else if (large) {
+      run_sym<2, 4, true, false>(a, 1, s);
+    } else {
+      run_sym<2, 2, true, false>(a, 1, s);
+    }
     a.ustride = o.sq; a.uld = o.sld; a.nk = o.sld / BK;
     double gain = 1.0;
     for (int i = 0; i < steps; ++i) {
       const float ca = co[3 * i], cb = co[3 * i + 1], cc = co[3 * i + 2];
-      gain *= ca;
-      set(0, A, A, A, B);
-      a.alpha = cc / ca / kScale; a.beta = cb / ca;
-      a.out_id = i == 0 ? P : nullptr;
-      sym(1);
-      a.out_id = nullptr;
-      a.alpha = 1.0f / kScale; a.beta = 1.0f;
       const bool more = i + 1 < steps;
-      int k = 0;
-      if (more) set(k++, B, A, A, Tm);
+      gain *= ca;
       if (i > 0) {
-        set(k++, B, P, P, P2);
         uint16_t* t = P;
         P = P2;
         P2 = t;
       }
-      if (k) sym(k);
+      if (chain) continue;
+      uint16_t* Ri = i == 0 ? P : R;                     // P of the first step is its R
+      set(0, A, A, Ri);
+      a.alpha = cc / ca / kScale; a.beta = cb / ca;
+      if (large) run_sym<4, 4, false, true>(a, 1, s);
+      else run_sym<2, 2, false, true>(a, 1, s);
+      a.alpha = 1.0f / kScale;
+      int k = 0;
+      if (more) set(k++, Ri, A, Tm);
+      if (i > 0) set(k++, Ri, P2, P);
+      if (k) product(k);
       if (more) {
-        set(0, B, Tm, Tm, A);
-        a.alpha = ca * ca / kScale; a.beta = ca * ca;
-        sym(1);
+        set(0, Ri, Tm, A);
+        a.alpha = ca * ca / kScale;
+        product(1);
       }
     }
     OutArgs r;
@@ -628,12 +923,10 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     r.out = out + i0 * elems;
     r.alpha = (float)(gain / ((double)kScale * kScale));
     r.mu = rows; r.mv = cols; r.ld = o.sld; r.nk = o.sld / BK;
-    r.ntm = (rows + BM - 1) / BM;
-    r.ntn = (cols + BN - 1) / BN;
     r.nmat = nm;
     r.wide = cols % 8 == 0 && (uintptr_t)out % 16 == 0;
-    r.total = (int64_t)nm * r.ntm * r.ntn;
-    ortho_out<<<(unsigned)pad_grid(r.total), kThreads, 0, s>>>(r);
+    if (use_large((int64_t)nm * ceil_div(rows, 256) * ceil_div(cols, 256))) run_out<4, 4>(r, s);
+    else run_out<2, 2>(r, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
