@@ -52,7 +52,7 @@ def _dev_ptr(t, dtype, shape, name, nullable=False):
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -84,12 +84,25 @@ def _same_device(device, **tensors):
 
 
 def _apart(name, out, **inputs):
-    """`out` must not share memory with any of `inputs`."""
-    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-    o = span(out)
+    """`out`, a tensor of the caller's, must not share memory with any of `inputs`."""
+    o0 = out.data_ptr()
+    o1 = o0 + out.numel() * out.element_size()
     for n, t in inputs.items():
-        if t is not None and o[0] < span(t)[1] and span(t)[0] < o[1]:
-            raise ValueError(f"{name} must not overlap {n}")
+        if t is not None:
+            p = t.data_ptr()
+            if o0 < p + t.numel() * t.element_size() and p < o1:
+                raise ValueError(f"{name} must not overlap {n}")
+
+
+def _launch(dev, name, *args):
+    """The C call `name` on the current stream of `dev`, which is made current for it."""
+    f = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    _abi.check(status, name)
 
 
 class Plan:
@@ -240,27 +253,31 @@ class Buffer:
         None and y_nvs may be None."""
         R, S, K, NvS = self.R, self.S, self.K, self.NvS
         W = dout.shape[-1]
+        dev = dout.device
         if drw is not None and not need_drw:
             raise ValueError("drw given, but need_drw is False")
-        dev = dout.device
+        args = (_dev_ptr(dout, torch.bfloat16, (R, S, W), "dout"), W,
+                _dev_ptr(y_nvs, torch.bfloat16, (R, NvS, W), "y_nvs", not need_drw),
+                _dev_ptr(rw_nvs, torch.float32, (R, NvS), "rw_nvs"))
+        _same_device(dev, y_nvs=y_nvs, rw_nvs=rw_nvs, plan=plan.dest)
         if dy_nvs is None:
             dy_nvs = torch.empty((R, NvS, W), dtype=torch.bfloat16, device=dev)
-        if drw is None and need_drw:
-            drw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
-        args = (_dev_ptr(dout, torch.bfloat16, (R, S, W), "dout"), int(W),
-                _dev_ptr(y_nvs, torch.bfloat16, (R, NvS, W), "y_nvs", not need_drw),
-                _dev_ptr(rw_nvs, torch.float32, (R, NvS), "rw_nvs"),
-                _dev_ptr(dy_nvs, torch.bfloat16, (R, NvS, W), "dy_nvs"),
-                _dev_ptr(drw, torch.float32, (R, S, K), "drw", True))
-        _same_device(dev, y_nvs=y_nvs, rw_nvs=rw_nvs, dy_nvs=dy_nvs, drw=drw,
-                     plan=plan.dest)
-        inplace = y_nvs is not None and dy_nvs.data_ptr() == y_nvs.data_ptr()
-        _apart("dy_nvs", dy_nvs, dout=dout, y_nvs=None if inplace else y_nvs, rw_nvs=rw_nvs)
+            p_dy = dy_nvs.data_ptr()
+        else:
+            p_dy = _dev_ptr(dy_nvs, torch.bfloat16, (R, NvS, W), "dy_nvs")
+            _same_device(dev, dy_nvs=dy_nvs)
+            _apart("dy_nvs", dy_nvs, dout=dout, rw_nvs=rw_nvs,
+                   y_nvs=None if p_dy == args[2] else y_nvs)
         if drw is not None:
+            p_drw = _dev_ptr(drw, torch.float32, (R, S, K), "drw")
+            _same_device(dev, drw=drw)
             _apart("drw", drw, dout=dout, y_nvs=y_nvs, rw_nvs=rw_nvs, dy_nvs=dy_nvs)
-        with torch.cuda.device(dev):
-            _abi.check(lib().moonep_combine_bwd(self._h, ctypes.byref(plan.struct), *args,
-                                                _stream()), "moonep_combine_bwd")
+        elif need_drw:
+            drw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            p_drw = drw.data_ptr()
+        else:
+            p_drw = None
+        _launch(dev, "moonep_combine_bwd", self._h, ctypes.byref(plan.struct), *args, p_dy, p_drw)
         return dy_nvs, drw
 
     def route(self, logits, bias=None, score="softmax", normalize=True, scale=1.0, topk=None,
@@ -272,21 +289,25 @@ class Buffer:
         multiplies them.  A logit of -inf closes its expert."""
         R, S, K, E = self.R, self.S, self.K, self.E
         dev = logits.device
+        args = (_dev_ptr(logits, logits.dtype, (R, S, E), "logits"),
+                _float_type(logits, "logits"),
+                _dev_ptr(bias, torch.float32, (E,), "bias", True), _score(score),
+                1 if normalize else 0, scale)
+        if bias is not None:
+            _same_device(dev, bias=bias)
         if topk is None:
             topk = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+        else:
+            _dev_ptr(topk, torch.int32, (R, S, K), "topk")
+            _same_device(dev, topk=topk)
+            _apart("topk", topk, logits=logits, bias=bias, rw=rw)
         if rw is None:
             rw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
-        dt = _float_type(logits, "logits")
-        args = (_dev_ptr(logits, logits.dtype, (R, S, E), "logits"), dt,
-                _dev_ptr(bias, torch.float32, (E,), "bias", True), _score(score),
-                int(bool(normalize)), float(scale),
-                _dev_ptr(topk, torch.int32, (R, S, K), "topk"),
-                _dev_ptr(rw, torch.float32, (R, S, K), "rw"))
-        _same_device(dev, bias=bias, topk=topk, rw=rw)
-        _apart("topk", topk, logits=logits, bias=bias, rw=rw)
-        _apart("rw", rw, logits=logits, bias=bias)
-        with torch.cuda.device(dev):
-            _abi.check(lib().moonep_route(self._h, *args, _stream()), "moonep_route")
+        else:
+            _dev_ptr(rw, torch.float32, (R, S, K), "rw")
+            _same_device(dev, rw=rw)
+            _apart("rw", rw, logits=logits, bias=bias)
+        _launch(dev, "moonep_route", self._h, *args, topk.data_ptr(), rw.data_ptr())
         return topk, rw
 
     def route_bwd(self, logits, topk, drw, score="softmax", normalize=True, scale=1.0,
@@ -296,19 +317,19 @@ class Buffer:
         selection bias takes no part).  dlogits may be logits (in place)."""
         R, S, K, E = self.R, self.S, self.K, self.E
         dev = logits.device
+        args = (_dev_ptr(logits, logits.dtype, (R, S, E), "logits"),
+                _float_type(logits, "logits"), _score(score), 1 if normalize else 0, scale,
+                _dev_ptr(topk, torch.int32, (R, S, K), "topk"),
+                _dev_ptr(drw, torch.float32, (R, S, K), "drw"))
+        _same_device(dev, topk=topk, drw=drw)
         if dlogits is None:
             dlogits = torch.empty_like(logits)
-        dt = _float_type(logits, "logits")
-        args = (_dev_ptr(logits, logits.dtype, (R, S, E), "logits"), dt, _score(score),
-                int(bool(normalize)), float(scale),
-                _dev_ptr(topk, torch.int32, (R, S, K), "topk"),
-                _dev_ptr(drw, torch.float32, (R, S, K), "drw"),
-                _dev_ptr(dlogits, logits.dtype, (R, S, E), "dlogits"))
-        _same_device(dev, topk=topk, drw=drw, dlogits=dlogits)
-        inplace = dlogits.data_ptr() == logits.data_ptr()
-        _apart("dlogits", dlogits, topk=topk, drw=drw, logits=None if inplace else logits)
-        with torch.cuda.device(dev):
-            _abi.check(lib().moonep_route_bwd(self._h, *args, _stream()), "moonep_route_bwd")
+        elif dlogits is not logits:
+            p = _dev_ptr(dlogits, logits.dtype, (R, S, E), "dlogits")
+            _same_device(dev, dlogits=dlogits)
+            _apart("dlogits", dlogits, topk=topk, drw=drw,
+                   logits=None if p == args[0] else logits)
+        _launch(dev, "moonep_route_bwd", self._h, *args, dlogits.data_ptr())
         return dlogits
 
     def _weights(self, ts, pool, used=(0, 1, 2)):
@@ -497,19 +518,21 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
     if len(flat) != steps or any(len(c) != 3 for c in flat):
         raise ValueError("coeffs: expected (a, b, c) or one (a, b, c) per step")
     dev = g.device
+    args = (_dev_ptr(g, g.dtype, g.shape, "g"), dt, n, rows, cols,
+            (ctypes.c_float * (3 * steps))(*[v for c in flat for v in c]), steps, eps)
     if out is None:
         out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _dev_ptr(out, torch.bfloat16, g.shape, "out")
+        _same_device(dev, out=out)
+        _apart("out", out, g=g, ws=ws)
     if ws is None:
         ws = orthogonalize_workspace(n, rows, cols, device=dev)
-    args = (_dev_ptr(g, g.dtype, g.shape, "g"), dt, int(n), int(rows), int(cols),
-            (ctypes.c_float * (3 * steps))(*[v for c in flat for v in c]), int(steps), float(eps),
-            _dev_ptr(out, torch.bfloat16, g.shape, "out"),
-            _dev_ptr(ws, torch.uint8, (ws.numel(),), "ws"), int(ws.numel()))
-    _same_device(dev, out=out, ws=ws)
-    _apart("out", out, g=g, ws=ws)
-    _apart("ws", ws, g=g)
-    with torch.cuda.device(dev):
-        _abi.check(lib().moonep_orthogonalize(*args, _stream()), "moonep_orthogonalize")
+    else:
+        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
+        _same_device(dev, ws=ws)
+        _apart("ws", ws, g=g)
+    _launch(dev, "moonep_orthogonalize", *args, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
