@@ -238,7 +238,8 @@ struct Exact {
     const double x = (double)l;
     const double s =
         (BY == kSoftmaxBias ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x))) + (double)bias[e];
-    return s != s ? INFINITY : s;
+    if (s == s) return s;
+    return x != x ? INFINITY : x == INFINITY ? 1e300 : x;   // a NaN before +inf
   }
 };
 
@@ -339,7 +340,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
         // the hardware's exponential and reciprocal: within 2^-20 (see below)
         s = BY == kSigmoidBias ? __builtin_amdgcn_rcpf(1.0f + __expf(-s)) : __expf(s - top) * inv;
         s += b[i];
-        s = l[c + i] == -INFINITY ? -INFINITY : s;
+        // a softmax with a NaN or +inf has no scores: such logits go first, by value
+        s = l[c + i] == -INFINITY || s != s ? l[c + i] : s;
       }
       const double key = key_of(s, e);
       k[i] = e < a.E ? key : no_key();

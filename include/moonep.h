@@ -244,7 +244,8 @@ moonep_status_t moonep_combine(moonep_handle_t h, const moonep_plan_t* plan,
  * combine it is the README's "combine bwd", a re-dispatch).  For dout
  * [R,S,W] bf16, the gradient of combine's output, W % 8 == 0, the forward's
  * y_nvs [R,NvS,W] and rw_nvs [R,NvS] fp32:
- *   dy_nvs[slot_k] = bf16_rne(rw_nvs[slot_k] * dout[r,s,:])  [R,NvS,W],
+ *   dy_nvs[slot_k] = bf16_rne(rw_nvs[slot_k] * dout[r,s,:])  [R,NvS,W]
+ *                    (of the fp32 product),
  *   drw[r,s,k] = sum_w dout[r,s,w] * y_nvs[slot_k,w]          [R,S,K] fp32,
  * the sum in fp32 in an order that depends on W alone.  Padding slots inside a
  * segment get zeros; slots past a rank's last segment are not written.  drw
@@ -371,10 +372,10 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  *   X = a_i X + (b_i A + c_i A A) X, A = X X^T,
  * and out [n,rows,cols] = bf16_rne(X).  coeffs: HOST array [steps][3] of
  * (a, b, c), read before the call returns.  The products are taken on values
- * held to 22 bits and summed in fp32; the rounding left in X is a few parts
- * in 10^4 of its norm at most, below that of its bf16 values.  The a_i scale
- * that rounding up, so their product may be at most
- * MOONEP_ORTHO_MAX_GAIN, each a_i > 0, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS,
+ * held to 22 bits and summed in fp32; with the usual five steps the rounding
+ * left in X is about 10^-4 of its norm, up to 2 10^-3 for a matrix of rank one
+ * (its bf16 values are rounded by 2 10^-3).  The a_i scale that rounding up, so
+ * their product may be at most MOONEP_ORTHO_MAX_GAIN, each a_i > 0, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS,
  * eps > 0.  Coefficients have to keep X's singular values below 1.9, as those
  * of any converging iteration do.  A zero matrix gives zeros; infinities and
  * NaN stay within their own matrix.

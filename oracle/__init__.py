@@ -18,6 +18,9 @@ the pages' statement of the method:
   (swiglu.py) follows from the forward by the chain rule and is pinned by
   finite differences.
 
+* training.py -- the router, the weighted combine's gradient and the
+  orthogonalised direction of a gradient, which the pages leave to the framework.
+
 Floating point: hidden states, weights and expert outputs are bf16 and route
 weights and gradients fp32, as the README's API guide fixes; matrix products
 are taken in float64 and rounded to bf16 where the stored tensor is bf16.
@@ -35,13 +38,13 @@ from .planner import Plan, nvs, plan
 from .moe import (combine, combine_rows, dispatch, expert_ffn, expert_ffn_backward,
                   prefetch_weight, reduce_grad, expert_wgrad, resolve_row)
 from .dense import dense_moe, dense_expert_grad, ffn_token, ffn_token_backward
-from . import swiglu
+from . import swiglu, training
 from .bruteforce import min_duplicates
 
 __all__ = [
     "bf16_to_f32", "f32_to_bf16", "f64_to_bf16", "expert_loads", "maxvio",
     "Plan", "nvs", "plan", "dispatch", "combine", "combine_rows", "prefetch_weight",
-    "expert_ffn_backward", "ffn_token_backward", "swiglu",
+    "expert_ffn_backward", "ffn_token_backward", "swiglu", "training",
     "expert_ffn", "expert_wgrad", "reduce_grad", "resolve_row", "dense_moe",
     "dense_expert_grad", "ffn_token", "min_duplicates",
 ]
