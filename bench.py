@@ -331,6 +331,52 @@ def time_backward(w, buf, plan, batches, x_nvs, z_ws, home, pool, steps, warmup,
                    "dX 4), weight gradients 6 H H'; weight-gradient bytes: fp32 read-modify-"
                    "write of each used (rank, weight row) pair's gradient per projection plus "
                    "the bf16 operand rows once; steps cycle the same maxvio targets")
+    out["weighted"] = time_weighted(w, buf, plan, x, dout, x_nvs, dy_nvs, dx_nvs, z_ws, home, pool,
+                                    grads[0], flush)
+    return out
+
+
+def time_weighted(w, buf, plan, x, dout, x_nvs, dy_nvs, y_nvs, z_ws, home, pool, grad, flush):
+    """The steps that a training step with route weights adds, on the last
+    plan's routing: the router and its gradient, the weighted combine's gradient
+    (in place of the re-dispatch), and the orthogonalised directions of one
+    rank's home rows of one projection.  Medians of five, the cache flushed
+    before each."""
+    import torch
+    from grouped_gemm_moonep_amd import orthogonalize, orthogonalize_workspace
+    dev = x.device
+    g = torch.Generator(device=dev).manual_seed(2)
+    logits = torch.randn((w.R, w.S, w.E), generator=g, device=dev)
+    topk, rw = buf.route(logits)
+    buf.plan(topk, plan=plan)
+    _, rw_nvs = buf.dispatch(plan, x, rw, x_nvs=x_nvs)
+    buf.prefetch_weight(plan, home, pool)
+    buf.expert_ffn(plan, x_nvs, home, pool, z_ws=z_ws, y_nvs=y_nvs)
+    drw = torch.empty_like(rw)
+    L = w.E // w.R
+    ws = orthogonalize_workspace(L, w.H, w.Hp)
+    way = torch.empty((L, w.H, w.Hp), dtype=torch.bfloat16, device=dev)
+    legs = {
+        "route": lambda: buf.route(logits, topk=topk, rw=rw),
+        "combine_bwd": lambda: buf.combine_bwd(plan, dout, y_nvs, rw_nvs, dy_nvs=dy_nvs, drw=drw),
+        "route_bwd": lambda: buf.route_bwd(logits, topk, drw),
+        "orthogonalize_rank": lambda: orthogonalize(grad[:L], out=way, ws=ws),
+    }
+    out = {}
+    for name, f in legs.items():
+        ms = []
+        for _ in range(6):
+            flush()
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            f()
+            b.record()
+            torch.cuda.synchronize()
+            ms.append(a.elapsed_time(b))
+        out[name + "_ms"] = round(float(np.median(ms[1:])), 4)
+    # dout read once, every slot of y read and of dy written once
+    nbytes = 2.0 * w.R * w.S * w.H * (1 + 2 * w.K)
+    out["combine_bwd_GBps"] = round(nbytes / out["combine_bwd_ms"] / 1e6, 1)
     return out
 
 
@@ -684,8 +730,9 @@ def main():
                     help="comma-separated maxvio targets (default: the workload's sweep)")
     ap.add_argument("--train", action="store_true",
                     help="also time a training step's backward (combine bwd, FFN backward, "
-                         "dispatch bwd, three weight gradients, reduce_grad) and report it "
-                         "under 'train'; needs ~90 GB more HBM for the fp32 gradient buffers")
+                         "dispatch bwd, three weight gradients, reduce_grad) and the steps that "
+                         "route weights and an orthogonalising optimiser add (router, weighted "
+                         "combine's gradient, directions) and report it under 'train'; needs ~90 GB more HBM for the fp32 gradient buffers")
     ap.add_argument("--overlap", action="store_true",
                     help="also time two pipelined micro-batches with dispatch/combine on a "
                          "second stream at a 32-CU budget against running them back to back")
