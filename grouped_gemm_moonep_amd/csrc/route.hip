@@ -56,10 +56,18 @@ __device__ __forceinline__ double swap_lanes(double v) {
   const uint32_t hi = (uint32_t)swap_lanes<STEP>((int)(uint32_t)(b >> 32));
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+// The larger of two keys.  An instruction by hand, since the compiler would
+// put each operand through a maximum with itself first, in case it is a signalling
+// NaN; the two wait states are those of a value that a DPP instruction reads next.
+__device__ __forceinline__ double larger(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2\n\ts_nop 1" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
 template <int G, int STEP = 0>
 __device__ __forceinline__ double group_max(double v) {
   if constexpr ((1 << STEP) >= G) return v;
-  else return group_max<G, STEP + 1>(__builtin_fmax(v, swap_lanes<STEP>(v)));
+  else return group_max<G, STEP + 1>(larger(v, swap_lanes<STEP>(v)));
 }
 template <int G, int STEP = 0>
 __device__ __forceinline__ float group_maxf(float v) {       // a NaN is passed over
@@ -100,21 +108,26 @@ template <class T>
 struct __attribute__((aligned(16))) Vec {
   T v[16 / sizeof(T)];
 };
-// wide: E is a multiple of N and the rows are 16-byte aligned
+// wide: E is a multiple of N and the rows are 16-byte aligned.  Elements past
+// the row are -inf: closed, and behind the row's own closed ones by their number.
 template <class T, int G, int VPL>
 __device__ __forceinline__ void load_row(const T* row, int E, int gl, bool wide, float out[VPL]) {
   constexpr int N = 16 / (int)sizeof(T);
   if (wide) {
-    Vec<T> r[VPL / N] = {};
 #pragma unroll
-    for (int j = 0; j < VPL / N; ++j)
-      if (N * (gl + G * j) < E) r[j] = *(const Vec<T>*)(row + N * (gl + G * j));
+    for (int j = 0; j < VPL / N; ++j) {
+      const bool in = N * (gl + G * j) < E;
+      Vec<T> r = {};
+      if (in) r = *(const Vec<T>*)(row + N * (gl + G * j));
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = to_float<T>(r[i / N].v[i % N]);
+      for (int i = 0; i < N; ++i) out[N * j + i] = in ? to_float<T>(r.v[i]) : -INFINITY;
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
+    for (int i = 0; i < VPL; ++i) {
+      out[i] = -INFINITY;
       if (element_of<T, G>(gl, i) < E) out[i] = to_float<T>(row[element_of<T, G>(gl, i)]);
+    }
   }
 }
 
@@ -141,20 +154,16 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 // Softmax over all experts of a row: its maximum and the inverse of its sum.  The exponentials
 // here are the hardware's (their error grows with the distance from the maximum as their
 // share of the sum falls).
-template <class T, int G, int VPL>
-__device__ __forceinline__ void softmax_row(const float l[VPL], int E, int gl, float* top,
-                                            float* inv) {
+template <int G, int VPL>
+__device__ __forceinline__ void softmax_row(const float l[VPL], float* top, float* inv) {
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    m = __builtin_fmaxf(m, element_of<T, G>(gl, i) < E ? l[i] : -INFINITY);
+    m = __builtin_fmaxf(m, l[i]);
   *top = finite_or_zero(group_maxf<G>(m));
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const float p = __expf(l[i] - *top);
-    s += element_of<T, G>(gl, i) < E ? p : 0.0f;
-  }
+  for (int i = 0; i < VPL; ++i) s += __expf(l[i] - *top);
   *inv = inv_or_zero(group_sum<G>(s));
 }
 
@@ -164,7 +173,7 @@ __device__ __forceinline__ void softmax_row(const float l[VPL], int E, int gl, f
 // NaN or infinity of the double), the lower half e for a negative x and its
 // complement otherwise: of equal x the lower expert has the larger key.
 __device__ __forceinline__ double key_of(float x, int e) {
-  const int b = x != x ? 0x7FC00000 : __float_as_int(x + 0.0f);   // -0 as +0
+  const int b = x != x ? 0x7FC00000 : __float_as_int(x);
   const uint32_t lo = (uint32_t)(e ^ ~(b >> 31));
   return __builtin_bit_cast(double, (uint64_t)(uint32_t)b << 32 | lo);
 }
@@ -174,10 +183,8 @@ __device__ __forceinline__ double no_key() {           // below every key
 __device__ __forceinline__ float key_value(double k) {
   return __int_as_float((int)(__builtin_bit_cast(uint64_t, k) >> 32));
 }
-__device__ __forceinline__ int key_expert(double k) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, k);
-  return (int)(uint32_t)b ^ ~((int)(uint32_t)(b >> 32) >> 31);
-}
+__device__ __forceinline__ int key_low(double k) { return (int)(uint32_t)__builtin_bit_cast(uint64_t, k); }
+__device__ __forceinline__ int expert_of(int low) { return low < 0 ? ~low : low; }
 
 __device__ __forceinline__ void order(double& a, double& b) {        // a >= b
   const double x = __builtin_fmax(a, b), y = __builtin_fmin(a, b);
@@ -200,12 +207,14 @@ __device__ __forceinline__ void bitonic8(double* k) {
     for (int i = 0; i < 8; ++i)
       if (!(i & s)) order(k[i], k[i + s]);
 }
-// Two sorted eights: the best eight in t (kept < 16), or all sixteen in t.
-template <int DEPTH>
-__device__ __forceinline__ void merge(double* t, const double c[8]) {
+// Two sorted eights: the best eight in t, and in `next` the best of all that
+// were left out (kNext); or all sixteen in t (DEPTH 16).
+template <int DEPTH, bool kNext>
+__device__ __forceinline__ void merge(double* t, const double c[8], double* next) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (DEPTH == 16) t[15 - i] = __builtin_fmin(t[i], c[7 - i]);
+    if constexpr (kNext) *next = __builtin_fmax(*next, __builtin_fmin(t[i], c[7 - i]));
     t[i] = __builtin_fmax(t[i], c[7 - i]);
   }
   bitonic8(t);
@@ -294,23 +303,24 @@ __device__ __forceinline__ void choose_exact(const Exact<T, G, BY>& ex, int E, i
 }
 
 // ---------------------------------------------------------------- forward
-// A lane's list keeps DEPTH keys: all of its own, or 8 >= K of them.
+// A lane's list keeps DEPTH keys: all of its own, or 8 >= K of them and, with
+// a bias, the next one.
 template <class T, int G, int VPL, int DEPTH, int BY, bool kSigmoid>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
-  constexpr int kSel = G < 32 ? 32 / G : 1;             // chosen experts a lane keeps
+  constexpr bool kShort = VPL > DEPTH;                  // K <= 8
+  constexpr int kMaxSel = kShort ? 8 : 32;
+  constexpr int kSel = G < kMaxSel ? kMaxSel / G : 1;   // chosen experts a lane keeps
+  constexpr bool kNext = kShort && BY != kLogits;
   const int lane = threadIdx.x & 63, gl = lane % G;
   const int64_t row = ((int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6)) * (64 / G) + lane / G;
   if (row >= a.T) return;                               // whole groups
   const T* lrow = (const T*)a.logits + row * a.E;
   float l[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) l[i] = 0.0f;
   load_row<T, G, VPL>(lrow, a.E, gl, a.wide, l);
   float top = 0.0f, inv = 0.0f;
-  if (BY == kSoftmaxBias || (!kSigmoid && !a.normalize))
-    softmax_row<T, G, VPL>(l, a.E, gl, &top, &inv);
+  if (BY == kSoftmaxBias || (!kSigmoid && !a.normalize)) softmax_row<G, VPL>(l, &top, &inv);
 
-  double t[DEPTH];
+  double t[DEPTH], next = no_key();
 #pragma unroll
   for (int c = 0; c < VPL; c += 8) {
     double k[8];
@@ -334,73 +344,90 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int e = element_of<T, G>(gl, c + i);
       float s = l[c + i];
-      if (BY != kLogits) {
-        // the hardware's exponential and reciprocal: within 2^-20 (see below)
-        s = BY == kSigmoidBias ? __builtin_amdgcn_rcpf(1.0f + __expf(-s)) : __expf(s - top) * inv;
-        s += b[i];
-        // a softmax with a NaN or +inf has no scores: such logits go first, by value
+      // The hardware's exponential and reciprocal: within 2^-20 (see below).  A closed expert
+      // keeps its -inf.  A softmax with a NaN or +inf has no scores: its logits order instead.
+      if (BY == kSigmoidBias) {
+        s = __builtin_amdgcn_rcpf(1.0f + __expf(-s)) + b[i];
+        s = l[c + i] == -INFINITY ? -INFINITY : s;
+      } else if (BY == kSoftmaxBias) {
+        s = __expf(s - top) * inv + b[i];
         s = l[c + i] == -INFINITY || s != s ? l[c + i] : s;
       }
-      const double key = key_of(s, e);
-      k[i] = e < a.E ? key : no_key();
+      k[i] = key_of(s + 0.0f, element_of<T, G>(gl, c + i));          // -0 as +0
     }
     sort8(k);
     if (c == 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = k[i];
     } else {
-      merge<DEPTH>(t, k);
+      merge<DEPTH, kNext>(t, k, &next);
     }
   }
 
   int sel[kSel];
 #pragma unroll
   for (int q = 0; q < kSel; ++q) sel[q] = 0;
-  // With a bias the draw goes on past K, up to G experts, while the scores
-  // stay within their rounding of the K-th.  A score in 32 bits is within 2^-20
-  // of the exact one (exponential, reciprocal and product: a few units of 2^-24 of
-  // a value of at most 1, and the exponent's rounding, |x| 2^-24 relative,
-  // where x e^-x < 0.4); its sum with the bias is rounded once more.
-  int limit = BY == kLogits ? a.K : a.K < G ? G : a.K + 1;
-  if (limit > a.E) limit = a.E;
-  int n = a.K;                                          // candidates
-  bool close = false, more = true;
-  float prev = INFINITY, kth = INFINITY;
-  for (int k = 0; k < limit; ++k) {
+  // Draw k: the largest head of the group's lists, kept by lane k % G and taken off its list.
+  auto draw = [&](int k, int deep) {
     const double m = group_max<G>(t[0]);
-    const bool win = t[0] == m;
-    const int e = key_expert(m);
 #pragma unroll
     for (int q = 0; q < kSel; ++q)
-      if (k == q * G + gl) sel[q] = e;
-    if (BY != kLogits) {
-      const float v = key_value(m);
-      const float tol = 0x1p-19f + 0x1p-22f * fabsf(prev);
-      if (k > 0 && k < a.K && !(prev - v > tol)) close = true;
-      if (k >= a.K) {
-        more = more && !(kth - v > tol);
-        if (more) n = k + 1;
-        if (!__any(more)) break;
-      } else {
-        kth = v;
-        prev = v;
+      if (k == q * G + gl) sel[q] = key_low(m);
+    if (t[0] == m) {
+#pragma unroll
+      for (int j = 0; j + 1 < DEPTH; ++j)
+        if (j < deep) t[j] = t[j + 1];
+      if (deep >= DEPTH) {
+        t[DEPTH - 1] = kNext ? next : no_key();
+        if (kNext) next = no_key();
       }
     }
-    if (win) {
+    return m;
+  };
+  if constexpr (BY == kLogits && kShort) {
 #pragma unroll
-      for (int j = 0; j + 1 < DEPTH; ++j) t[j] = t[j + 1];
-      t[DEPTH - 1] = no_key();
-    }
+    for (int k = 0; k < 8; ++k)
+      if (k < a.K) draw(k, 7 - k);                      // a list still has 7 - k draws before it
+  } else if constexpr (BY == kLogits) {
+    for (int k = 0; k < a.K; ++k) draw(k, DEPTH);
   }
-  if (BY != kLogits) {
+  if constexpr (BY != kLogits) {
+    // With a bias the draw goes on past K, up to G experts, while the scores
+    // stay within their rounding of the K-th.  A score in 32 bits is within 2^-20
+    // of the exact one (exponential, reciprocal and product: a few units of 2^-24 of
+    // a value of at most 1, and the exponent's rounding, |x| 2^-24 relative,
+    // where x e^-x < 0.4); its sum with the bias is rounded once more.
+    int limit = a.K < G ? G : a.K + 1;
+    if (limit > a.E) limit = a.E;
+    int n = a.K;                                        // candidates
+    bool close = false, more = true;
+    float prev = INFINITY;
+    for (int k = 0; k < limit; ++k) {
+      const float v = key_value(draw(k, DEPTH));
+      const bool apart = prev - v > 0x1p-19f + 0x1p-22f * fabsf(prev);
+      if (k < a.K) {
+        if (k > 0 && !apart) close = true;
+        prev = v;
+      } else {
+        more = more && !apart;
+        if (more) n = k + 1;
+        if (!__any(more)) break;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) sel[q] = expert_of(sel[q]);
     if (close || n > a.K) {
       Exact<T, G, BY> ex;
       ex.init(lrow, a.bias, a.E, gl);
-      if (n < G || (n == G && n == a.E)) sel[0] = rank_candidates<T, G, BY>(ex, sel[0], n, gl);
+      // a list of nine (next among them) is whole up to the ninth draw
+      const bool whole = (n < G || (n == G && n == a.E)) && (!kNext || n <= 9);
+      if (whole) sel[0] = rank_candidates<T, G, BY>(ex, sel[0], n, gl);
       else choose_exact<T, G, BY, kSel>(ex, a.E, a.K, gl, sel);
     }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kSel; ++q) sel[q] = expert_of(sel[q]);
   }
 
   // weights: lane gl holds the chosen experts gl, gl + G, ...
@@ -471,7 +498,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteArgs a) {
   float top = 0.0f, inv = 1.0f;
   if (dense) {
     load_row<T, G, VPL>(lrow, a.E, gl, a.wide, l);
-    softmax_row<T, G, VPL>(l, a.E, gl, &top, &inv);
+    softmax_row<G, VPL>(l, &top, &inv);
   } else if (!kSigmoid) {
     top = finite_or_zero(group_maxf<G>(mx));
   }
