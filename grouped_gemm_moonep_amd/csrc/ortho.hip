@@ -13,19 +13,20 @@
 //   T = R A,  P = R P                            (P = R in the first)
 //   A = a^2 R T
 //   out = (prod a) P X_0                         (last product)
-// All m x m matrices are symmetric, so only the tiles on and above the
-// diagonal are computed and every element above it is written twice: to the bit, for an
-// antisymmetric part, however small at first, would grow to 1e-2 of the result.  Per step 3.5 m^3 ..
-// 4 m^3 multiply-adds of which half are done, against (2 n/m + 1) m^3 (1.5 n/m + 0.5
-// done) for the steps taken on X itself: at n = 3.5 m 26 m^3 in all against 57 m^3.
+// All m x m matrices are symmetric, so only the tiles on and above the diagonal are
+// computed, and every element above it is written twice: to the bit, for an antisymmetric
+// part, however small at first, would grow to 1e-2 of the result.  Five steps are 17 such
+// products, m^3 / 2 multiply-adds each, and the long side's n m^2 / 2 and n m^2; taken on X
+// itself each step would have n m^2 / 2 + m^3 / 2 + n m^2.  At n = 3.5 m that is 13.75 m^3
+// against 28.75 m^3.
 //
 // Rounding: P amplifies what is lost in A by up to prod a (485 for the usual
 // five steps) in the directions of small singular values, and the gradient of
 // an expert with few tokens has almost only those.  bf16 (2^-9) or fp16
 // (2^-12) operands would leave nothing there, so every matrix is held as a
 // pair of fp16, v = hi + lo (22 bits), and a product is hi hi + hi lo + lo hi
-// on the matrix units, summed in fp32: 1e-5 .. 1e-3 of the result's norm is
-// left for full rank .. rank one, below the 2e-3 of rounding it to bf16.
+// on the matrix units, summed in fp32.  Before its rounding to bf16 (1.7e-3 of its norm) the
+// result is then off by 1e-5 of its norm at full rank, 3e-4 .. 1.1e-3 at rank one.
 // Values are scaled by 2^14, so entries up to 4 are held, and down to 2^-28
 // with 11 or more bits.
 //
@@ -61,7 +62,8 @@ constexpr int kK = 32;                        // values of K per step (a 64-elem
 // ahead, B two), or, kDeep, 5 slots for each (both four steps ahead), which a
 // launch of few workgroups needs: its operands were just written by other XCDs,
 // a load takes as long as several steps, and no second workgroup fills the gap
-// (five steps on five 509 x 1283 matrices: 310 us without, 290 us with).
+// (five steps on four 1024 x 2048 matrices: 517 us without, 466 us with; one of 2048 x
+// 7168: 1023 and 882 us).
 template <int MI, int NJ, bool kDeep>
 struct Tile3 {
   static constexpr int kRows = 64 * MI, kCols = 64 * NJ;
@@ -106,8 +108,9 @@ __device__ __forceinline__ bf16x8 read3(const lds_t* tile, int row0, int kk) {
 // at most N LDS-DMA loads of this wave outstanding
 template <int N>
 __device__ __forceinline__ void wait_dma() {
-  static_assert(N == 4 || N == 8 || N == 24, "outstanding loads");
-  if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+  static_assert(N == 4 || N == 8 || N == 12 || N == 24, "outstanding loads");
+  if constexpr (N == 12) asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+  else if constexpr (N == 4) asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
   else if constexpr (N == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
   else asm volatile("s_waitcnt vmcnt(24)" ::: "memory");
 }
@@ -270,6 +273,83 @@ __device__ __forceinline__ void gemm3_loop(const RowTileT<2 * MI>& la, const Row
   barrier_reads_done();
 }
 
+// The loop of the 64 x 64 tile: a wave has one block and six MFMAs a step, too
+// few to slot the rest between, so the step is kept short instead.  A step's
+// fragments are read while the step before is multiplied; hi hi and the two
+// cross terms go to accumulators of their own (a chain of dependent MFMAs costs
+// twice their issue), which are added to the result every ten steps.
+struct Frag1 {
+  bf16x8 a[4], b[4];                                     // columns kk
+};
+typedef Tile3<1, 1, true> Tile1;
+
+__device__ __forceinline__ void read1(Frag1& f, const lds_t* A, const lds_t* Bt, int arow0,
+                                      int bcol0) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    f.a[kk] = read3(A, arow0, kk);
+    f.b[kk] = read3(Bt, bcol0, kk);
+  }
+}
+
+template <int J>
+__device__ __forceinline__ void kstep1(const RowTileT<2>& la, const RowTileT<2>& lb,
+                                       const Tile1& ring, int j, int nk, const Frag1& f,
+                                       Frag1& next, f32x16 acc[2], int arow0, int bcol0,
+                                       bool idle) {
+  wait_dma<8>();                                         // step j + 1's tiles, in every wave,
+  barrier_reads_done();                                  // and step j's fragments
+  la.issue(ring.a<J + 4>(), (int64_t)(j + 4) * BK, j + 4 < nk);
+  lb.issue(ring.b<J + 4>(), (int64_t)(j + 4) * BK, j + 4 < nk);
+  if (idle) return;
+  read1(next, ring.a<J + 1>(), ring.b<J + 1>(), arow0, bcol0);
+  const auto mma = [&](int x, int i, int k) {
+    acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, f.b[k]),
+                                                    __builtin_bit_cast(f16x8, f.a[i]), acc[x], 0,
+                                                    0, 0);
+  };
+  mma(1, 0, 2); mma(0, 0, 0); mma(1, 2, 0); mma(0, 1, 1); mma(1, 1, 3); mma(1, 3, 1);
+}
+
+__device__ __forceinline__ void gemm1_loop(const RowTileT<2>& la, const RowTileT<2>& lb,
+                                           const Tile1& ring, int nk, f32x16& sum, int arow0,
+                                           int bcol0, bool idle) {
+  la.issue(ring.a<0>(), 0, true);
+  lb.issue(ring.b<0>(), 0, true);
+  la.issue(ring.a<1>(), BK, 1 < nk);
+  lb.issue(ring.b<1>(), BK, 1 < nk);
+  la.issue(ring.a<2>(), 2 * BK, 2 < nk);
+  lb.issue(ring.b<2>(), 2 * BK, 2 < nk);
+  la.issue(ring.a<3>(), 3 * BK, 3 < nk);
+  lb.issue(ring.b<3>(), 3 * BK, 3 < nk);
+  f32x16 acc[2];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) sum[v] = acc[0][v] = acc[1][v] = 0.0f;
+  wait_dma<12>();
+  barrier_reads_done();
+  Frag1 f, g;
+  if (!idle) read1(f, ring.a<0>(), ring.b<0>(), arow0, bcol0);
+  for (int j = 0; j < nk; j += 10) {
+    kstep1<0>(la, lb, ring, j, nk, f, g, acc, arow0, bcol0, idle);
+    if (j + 1 < nk) kstep1<1>(la, lb, ring, j + 1, nk, g, f, acc, arow0, bcol0, idle);
+    if (j + 2 < nk) kstep1<2>(la, lb, ring, j + 2, nk, f, g, acc, arow0, bcol0, idle);
+    if (j + 3 < nk) kstep1<3>(la, lb, ring, j + 3, nk, g, f, acc, arow0, bcol0, idle);
+    if (j + 4 < nk) kstep1<4>(la, lb, ring, j + 4, nk, f, g, acc, arow0, bcol0, idle);
+    if (j + 5 < nk) kstep1<0>(la, lb, ring, j + 5, nk, g, f, acc, arow0, bcol0, idle);
+    if (j + 6 < nk) kstep1<1>(la, lb, ring, j + 6, nk, f, g, acc, arow0, bcol0, idle);
+    if (j + 7 < nk) kstep1<2>(la, lb, ring, j + 7, nk, g, f, acc, arow0, bcol0, idle);
+    if (j + 8 < nk) kstep1<3>(la, lb, ring, j + 8, nk, f, g, acc, arow0, bcol0, idle);
+    if (j + 9 < nk) kstep1<4>(la, lb, ring, j + 9, nk, g, f, acc, arow0, bcol0, idle);
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      sum[v] += acc[0][v] + acc[1][v];
+      acc[0][v] = acc[1][v] = 0.0f;
+    }
+  }
+  wait_loads<0>();
+  barrier_reads_done();
+}
+
 // ---------------------------------------------------------- epilogue pieces
 // A 32 x 32 block of a pair matrix is 32 rows of 128 bytes.  In LDS the
 // 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7), which spreads a
@@ -279,7 +359,11 @@ __device__ __forceinline__ int blk_off(int r, int byte) {
   return r * 128 + (((byte >> 4) ^ ((r >> 1) & 7)) << 4) + (byte & 15);
 }
 
+// v is made before it is split: where hi is rounded from the unrounded product that v comes
+// from (one mixed instruction), and lo from v and another hi, the two are a whole unit of hi
+// apart near a tie, which a low-rank result shows 400-fold.
 __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
+  asm volatile("" : "+v"(v));
   hi = (_Float16)v;
   lo = (_Float16)(v - (float)hi);
 }
@@ -412,7 +496,10 @@ __device__ __forceinline__ void sym_tile(const SymTile& a, const Tile3<MI, NJ, k
   la.init(a.u + (int64_t)m0 * a.uld, a.uld, a.m - m0 < TL::kRows ? a.m - m0 : TL::kRows);
   lb.init(a.v + (int64_t)n0 * a.uld, a.uld, a.m - n0 < TL::kCols ? a.m - n0 : TL::kCols);
   f32x16 acc[MI][NJ];
-  gemm3_loop<MI, NJ, kDeep, kTwoSums>(la, lb, ring, a.nk, acc, arow0, bcol0, idle);
+  if constexpr (MI == 1 && NJ == 1)
+    gemm1_loop(la, lb, ring, a.nk, acc[0][0], arow0, bcol0, idle);
+  else
+    gemm3_loop<MI, NJ, kDeep, kTwoSums>(la, lb, ring, a.nk, acc, arow0, bcol0, idle);
   if (idle) return;
 
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
@@ -524,60 +611,6 @@ void ortho_sym(SymArgs a) {
   if (s.m0 < a.m) sym_tile<MI, NJ, kDeep, kTwoSums, kIn>(s, ring);
 }
 
-// Matrices of one tile (m <= 128): a workgroup takes all products of its matrix, which saves
-// fourteen launches (four 128 x 256 matrices: 144 us without, 131 us with).  Its own stores are seen after a workgroup barrier.
-constexpr int kChainM = 128;
-struct ChainArgs {
-  const uint16_t* x;         // [nmat] X_0
-  uint16_t* sq[5];           // [nmat] m x m each: A, R, T, P and P again
-  int64_t xstride, ostride;
-  int m, xld, ld, steps;
-  float coef[MOONEP_ORTHO_MAX_STEPS][3];
-};
-
-__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1))) void ortho_chain(ChainArgs a) {
-  typedef Tile3<2, 2, true> TL;
-  __shared__ __attribute__((aligned(16))) char lds_mem[TL::kLds];
-  const TL ring = {(lds_t*)lds_mem};
-  const int64_t off = (int64_t)blockIdx.x * a.ostride;
-  uint16_t *A = a.sq[0] + off, *Tm = a.sq[2] + off, *P = a.sq[3] + off, *P2 = a.sq[4] + off;
-  SymTile s;
-  s.u = s.v = a.x + (int64_t)blockIdx.x * a.xstride;
-  s.in = nullptr;
-  s.out = A;
-  s.alpha = 1.0f / kScale; s.beta = 0.0f;
-  s.m = a.m; s.uld = a.xld; s.ld = a.ld; s.nk = a.xld / BK;
-  s.m0 = 0; s.n0 = 0;
-  sym_tile<2, 2, true, true, false>(s, ring);
-  s.uld = a.ld; s.nk = a.ld / BK;
-  for (int i = 0; i < a.steps; ++i) {
-    const float ca = a.coef[i][0], cb = a.coef[i][1], cc = a.coef[i][2];
-    uint16_t* R = i == 0 ? P : a.sq[1] + off;
-    __syncthreads();
-    s.u = s.v = s.in = A;
-    s.out = R;
-    s.alpha = cc / ca / kScale; s.beta = cb / ca;
-    sym_tile<2, 2, true, false, true>(s, ring);
-    s.in = nullptr;
-    s.u = R;
-    // T = R A, P2 = R P, A = a^2 R T; the last step only needs the second, the first has it
-    for (int k = i + 1 < a.steps ? 0 : 1; k < (i + 1 < a.steps ? 3 : 2); ++k) {
-      if (k == 1 && i == 0) continue;
-      __syncthreads();
-      s.v = k == 0 ? A : k == 1 ? P : Tm;
-      s.out = k == 0 ? Tm : k == 1 ? P2 : A;
-      s.alpha = (k == 2 ? ca * ca : 1.0f) / kScale;
-      sym_tile<2, 2, true, false, false>(s, ring);
-    }
-    if (i > 0) {
-      uint16_t* t = P;
-      P = P2;
-      P2 = t;
-    }
-  }
-}
-
 // --------------------------------------------------------------- last product
 // out = alpha U V^T as bf16 [mu][mv], dense.
 struct OutArgs {
@@ -615,7 +648,10 @@ void ortho_out(OutArgs a) {
   la.init(a.u + mi * a.ustride + (int64_t)m0 * a.ld, a.ld, rows_valid);
   lb.init(a.v + mi * a.vstride + (int64_t)n0 * a.ld, a.ld, cols_valid);
   f32x16 acc[MI][NJ];
-  gemm3_loop<MI, NJ, kDeep, false>(la, lb, ring, a.nk, acc, arow0, bcol0, idle);
+  if constexpr (MI == 1 && NJ == 1)
+    gemm1_loop(la, lb, ring, a.nk, acc[0][0], arow0, bcol0, idle);
+  else
+    gemm3_loop<MI, NJ, kDeep, false>(la, lb, ring, a.nk, acc, arow0, bcol0, idle);
   if (idle) return;
 
   uint16_t* out = a.out + (mi * a.mu + m0) * (int64_t)a.mv + n0;
@@ -789,44 +825,65 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
   return o;
 }
 
-constexpr int kCus = 256;
-
-template <int MI, int NJ, bool kTwoSums, bool kIn>
+template <int MI, int NJ, bool kDeep, bool kTwoSums, bool kIn>
 void run_sym(SymArgs& a, int problems, hipStream_t s) {
   a.nt = ceil_div(a.m, 64 * NJ);
   a.tiles = NJ / MI * (a.nt * (a.nt + 1) / 2);
   a.total = (int64_t)problems * a.nmat * a.tiles;
-  const unsigned grid = (unsigned)pad_grid(a.total);
-  if constexpr (MI == 2 && NJ == 2) {
-    if (a.total <= kCus) {
-      ortho_sym<MI, NJ, true, kTwoSums, kIn><<<grid, kThreads, 0, s>>>(a);
-      return;
-    }
-  }
-  ortho_sym<MI, NJ, false, kTwoSums, kIn><<<grid, kThreads, 0, s>>>(a);
+  ortho_sym<MI, NJ, kDeep, kTwoSums, kIn><<<(unsigned)pad_grid(a.total), kThreads, 0, s>>>(a);
 }
 
-template <int MI, int NJ>
+template <int MI, int NJ, bool kDeep>
 void run_out(OutArgs& r, hipStream_t s) {
   r.ntm = ceil_div(r.mu, 64 * MI);
   r.ntn = ceil_div(r.mv, 64 * NJ);
   r.total = (int64_t)r.nmat * r.ntm * r.ntn;
-  const unsigned grid = (unsigned)pad_grid(r.total);
-  if constexpr (MI == 2 && NJ == 2) {
-    if (r.total <= kCus) {
-      ortho_out<MI, NJ, true><<<grid, kThreads, 0, s>>>(r);
-      return;
-    }
-  }
-  ortho_out<MI, NJ, false><<<grid, kThreads, 0, s>>>(r);
+  ortho_out<MI, NJ, kDeep><<<(unsigned)pad_grid(r.total), kThreads, 0, s>>>(r);
 }
 
-// 256-wide tiles from two rounds of them on; below, 128-wide ones fill the chip more evenly and
-// two of their workgroups on a CU hide each other's prologue and epilogue.  Five steps on 32, 16
-// and 8 matrices of 2048 x 4096 (1152, 576, 288 tiles): 18.5, 9.7, 5.6 ms with 256-wide tiles,
-// 19.8, 10.0, 5.1 ms with 128-wide ones; 32 of 1024 x 2048 (320 tiles): 3.35 and 3.08 ms; one of
-// 512 x 1024: 0.67 and 0.25 ms.
-bool use_large(int64_t tiles256) { return tiles256 >= 512; }
+// Which tiles a product takes, by how many there are.
+//
+// 256-wide ones from two rounds of them on; below, 128-wide ones fill the chip
+// more evenly, and from one per CU on two of their workgroups on a CU hide each
+// other's prologue and epilogue.  Five steps on 32, 16 and 8 matrices of 2048 x
+// 4096 (1152, 576, 288 tiles of 256): 18.5, 9.7, 5.6 ms with 256-wide tiles, 19.8, 10.0,
+// 5.1 ms with 128-wide ones; 32 of 1024 x 2048 (320 tiles): 3.3 and 3.0 ms.
+//
+// 64-wide ones where the 128-wide ones would leave half the CUs idle: a step of
+// theirs takes a third of the time.  One of 1024 x 2048 (36 tiles of 128): 271 us
+// against 360 us; five of 509 x 1283 (50): 207 and 280 us; one of 290 x 700 (6): 124
+// and 198 us; four of 1024 x 2048 (144): 618 and 466 us.
+//
+// The last product has 256-wide tiles from half a round on: it is dense, and its
+// epilogue is short (1 to 3% at 128 .. 512 tiles).
+constexpr int kCus = 256, kLarge = 512, kSmall = 128;
+
+// The product of one launch (kTwoSums: the first one, over n; kIn: the one that adds to its
+// operand).
+template <bool kTwoSums, bool kIn>
+void run_product(SymArgs& a, int problems, hipStream_t s) {
+  const int64_t n = (int64_t)problems * a.nmat;
+  const int64_t n256 = ceil_div(a.m, 256), n128 = ceil_div(a.m, 128);
+  const int64_t t256 = n * (n256 * (n256 + 1) / 2), t128 = n * (n128 * (n128 + 1) / 2);
+  if (t256 >= kLarge) {
+    if constexpr (kTwoSums) run_sym<2, 4, false, true, kIn>(a, problems, s);
+    else run_sym<4, 4, false, false, kIn>(a, problems, s);
+  } else if (t128 > kCus) {
+    run_sym<2, 2, false, kTwoSums, kIn>(a, problems, s);
+  } else if (t128 > kSmall) {
+    run_sym<2, 2, true, kTwoSums, kIn>(a, problems, s);
+  } else {
+    run_sym<1, 1, true, false, kIn>(a, problems, s);
+  }
+}
+
+void run_last(OutArgs& r, hipStream_t s) {
+  const int64_t t256 = (int64_t)r.nmat * ceil_div(r.mu, 256) * ceil_div(r.mv, 256);
+  const int64_t t128 = (int64_t)r.nmat * ceil_div(r.mu, 128) * ceil_div(r.mv, 128);
+  if (t256 >= kSmall) run_out<4, 4, false>(r, s);
+  else if (t128 > kSmall) run_out<2, 2, true>(r, s);
+  else run_out<1, 1, true>(r, s);
+}
 
 template <class T>
 hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co, int steps,
@@ -851,9 +908,6 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
         gi, rows, cols, eps, wide, part, tall ? xt : x, tall ? x : xt, tall ? o.xt : o.x,
         tall ? o.x : o.xt);
 
-    const int64_t nt = ceil_div(o.m, 256);
-    const bool large = use_large(nm * (nt * (nt + 1) / 2));
-    const bool chain = o.m <= kChainM;
     SymArgs a;
     a.m = o.m;
     a.ld = o.sld;
@@ -861,10 +915,6 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     a.nmat = nm;
     auto set = [&](int i, const uint16_t* u, const uint16_t* v, uint16_t* to) {
       a.u[i] = u; a.v[i] = v; a.out[i] = to;
-    };
-    auto product = [&](int problems) {
-      if (large) run_sym<4, 4, false, false>(a, problems, s);
-      else run_sym<2, 2, false, false>(a, problems, s);
     };
     uint16_t *A = sq[0], *R = sq[1], *Tm = sq[2], *P = sq[3], *P2 = sq[4];
     // The first product with two sums: a chain of fp32 additions over all of n would round by
@@ -874,19 +924,7 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     a.in = A;
     a.ustride = o.x; a.uld = o.xld; a.nk = o.xld / BK;
     a.alpha = 1.0f / kScale; a.beta = 0.0f;
-    if (chain) {
-      ChainArgs c;
-      c.x = x;
-      for (int i = 0; i < 5; ++i) c.sq[i] = sq[i];
-      c.xstride = o.x; c.ostride = o.sq;
-      c.m = o.m; c.xld = o.xld; c.ld = o.sld; c.steps = steps;
-      for (int i = 0; i < 3 * steps; ++i) c.coef[i / 3][i % 3] = co[i];
-      ortho_chain<<<(unsigned)nm, kThreads, 0, s>>>(c);
-    } else if (large) {
-      run_sym<2, 4, true, false>(a, 1, s);
-    } else {
-      run_sym<2, 2, true, false>(a, 1, s);
-    }
+    run_product<true, false>(a, 1, s);
     a.ustride = o.sq; a.uld = o.sld; a.nk = o.sld / BK;
     double gain = 1.0;
     for (int i = 0; i < steps; ++i) {
@@ -898,21 +936,19 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
         P = P2;
         P2 = t;
       }
-      if (chain) continue;
       uint16_t* Ri = i == 0 ? P : R;                     // P of the first step is its R
       set(0, A, A, Ri);
       a.alpha = cc / ca / kScale; a.beta = cb / ca;
-      if (large) run_sym<4, 4, false, true>(a, 1, s);
-      else run_sym<2, 2, false, true>(a, 1, s);
+      run_product<false, true>(a, 1, s);
       a.alpha = 1.0f / kScale;
       int k = 0;
       if (more) set(k++, Ri, A, Tm);
       if (i > 0) set(k++, Ri, P2, P);
-      if (k) product(k);
+      if (k) run_product<false, false>(a, k, s);
       if (more) {
         set(0, Ri, Tm, A);
         a.alpha = ca * ca / kScale;
-        product(1);
+        run_product<false, false>(a, 1, s);
       }
     }
     OutArgs r;
@@ -925,8 +961,7 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     r.mu = rows; r.mv = cols; r.ld = o.sld; r.nk = o.sld / BK;
     r.nmat = nm;
     r.wide = cols % 8 == 0 && (uintptr_t)out % 16 == 0;
-    if (use_large((int64_t)nm * ceil_div(rows, 256) * ceil_div(cols, 256))) run_out<4, 4>(r, s);
-    else run_out<2, 2>(r, s);
+    run_last(r, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -90,6 +90,26 @@ def test_low_rank_gradients(tokens, rows, cols):
     check(m.bfloat16(), what=f"rank {tokens} bf16")
 
 
+# Rows of very unequal size, where single entries of the first matrices decide.
+# Rounding to bf16 leaves at most 2^-8 / sqrt(3) of the norm (errors uniform over
+# half a step); the roundings before it are independent per entry, so 10^4 times
+# two of 2^-24 / sqrt(3) rather than four times 2^-24: 2.4e-3 together.
+@pytest.mark.parametrize("n,rows,cols,tokens,spread", [(1, 848, 1152, 1, 1), (1, 500, 1100, 4, 1),
+                                                       (2, 114, 111, 4, 0), (1, 1000, 1100, 2, 1),
+                                                       (20, 260, 600, 1, 1)])
+def test_low_rank_gradients_of_unequal_rows(n, rows, cols, tokens, spread):
+    r = gen(tokens)
+    scale = torch.exp(spread * torch.randn((rows,), generator=r, device="cuda"))
+    g = torch.stack([(torch.randn((tokens, rows), generator=r, device="cuda") * scale).t() @
+                     (1e-3 * torch.randn((tokens, cols), generator=r, device="cuda"))
+                     for _ in range(n)]).to(torch.bfloat16)
+    want = reference(g, FIVE)
+    rel = (torch.linalg.matrix_norm(orthogonalize(g).double() - want) /
+           torch.linalg.matrix_norm(want))
+    log(f"ortho {tuple(g.shape)} of {tokens} tokens, unequal rows: {rel.max().item():.2e}")
+    assert (rel <= 2.4e-3).all(), rel
+
+
 def test_headline_gradient():
     g = torch.randn((2, 7168, 2048), generator=gen(1), device="cuda")
     g[1, :, 300:] *= 1e-4
