@@ -569,8 +569,9 @@ struct SymArgs {
   int64_t ostride;           // of in and out
   float alpha, beta;
   int m, uld, ld, nk;        // as in SymTile
-  int nt, tiles, nmat;       // tile columns, tiles per matrix, matrices
-  int64_t total;             // workgroups in use
+  int nt, tiles, nmat;       // square tiles along a side, of a matrix; matrices
+  int64_t total;             // tiles in all
+  int64_t whole;             // (ortho_sym_rounds) those not computed in four parts
 };
 
 __device__ __forceinline__ int64_t xcd_tile(int64_t total) {
@@ -580,8 +581,25 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t total) {
   return c < per && t < total ? t : -1;
 }
 
-// The tiles of a matrix cover the part on and above the diagonal, by columns
-// of tiles NJ / MI rows of tiles high.
+// Square tile t, `side` wide: those of a matrix cover the part on and above the diagonal, row
+// by row.
+__device__ __forceinline__ void sym_tile_at(const SymArgs& a, SymTile& s, int64_t t, int side) {
+  const int64_t mat = t / a.tiles;
+  int q = (int)(t - mat * a.tiles), ti = 0;
+  for (; q >= a.nt - ti; ++ti) q -= a.nt - ti;
+  const int pr = mat >= a.nmat ? 1 : 0;
+  const int64_t mi = mat - (pr ? a.nmat : 0);
+  s.u = a.u[pr] + mi * a.ustride;
+  s.v = a.v[pr] + mi * a.ustride;
+  s.in = a.in + mi * a.ostride;
+  s.out = a.out[pr] + mi * a.ostride;
+  s.alpha = a.alpha; s.beta = a.beta;
+  s.m = a.m; s.uld = a.uld; s.ld = a.ld; s.nk = a.nk;
+  s.m0 = ti * side;
+  s.n0 = (ti + q) * side;
+}
+
+// One workgroup per tile; a square tile is NJ / MI of them.
 template <int MI, int NJ, bool kDeep, bool kTwoSums, bool kIn>
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
                           amdgpu_waves_per_eu(Tile3<MI, NJ, kDeep>::kWavesPerSimd,
@@ -592,23 +610,38 @@ void ortho_sym(SymArgs a) {
   const TL ring = {(lds_t*)lds_mem};
   const int64_t t = xcd_tile(a.total);
   if (t < 0) return;
-  const int64_t mat = t / a.tiles;
-  int q = (int)(t - mat * a.tiles), ti = 0;
-  const int part = q % (NJ / MI);
-  q /= NJ / MI;
-  for (; q >= a.nt - ti; ++ti) q -= a.nt - ti;
-  const int pr = mat >= a.nmat ? 1 : 0;
-  const int64_t mi = mat - (pr ? a.nmat : 0);
   SymTile s;
-  s.u = a.u[pr] + mi * a.ustride;
-  s.v = a.v[pr] + mi * a.ustride;
-  s.in = a.in + mi * a.ostride;
-  s.out = a.out[pr] + mi * a.ostride;
-  s.alpha = a.alpha; s.beta = a.beta;
-  s.m = a.m; s.uld = a.uld; s.ld = a.ld; s.nk = a.nk;
-  s.m0 = ti * TL::kCols + part * TL::kRows;
-  s.n0 = (ti + q) * TL::kCols;
+  const int part = (int)(t % (NJ / MI));
+  sym_tile_at(a, s, t / (NJ / MI), TL::kCols);
+  s.m0 += part * TL::kRows;
   if (s.m0 < a.m) sym_tile<MI, NJ, kDeep, kTwoSums, kIn>(s, ring);
+}
+
+// The same with 256-wide tiles of which the last ones, those that would not fill a round of the
+// CUs, are computed as four 128-wide ones each.
+template <bool kIn>
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads), amdgpu_waves_per_eu(1, 1)))
+void ortho_sym_rounds(SymArgs a) {
+  typedef Tile3<4, 4, false> TL;
+  typedef Tile3<2, 2, true> TS;
+  static_assert(TL::kLds == TS::kLds, "one ring for both");
+  __shared__ __attribute__((aligned(16))) char lds_mem[TL::kLds];
+  const int64_t parts0 = (a.whole + kXcds - 1) / kXcds * kXcds;      // the first of the parts
+  const bool whole = blockIdx.x < parts0;
+  const int64_t b = whole ? blockIdx.x : blockIdx.x - parts0;
+  const int64_t count = whole ? a.whole : 4 * (a.total - a.whole);
+  const int64_t per = (count + kXcds - 1) / kXcds, c = b / kXcds, q = (int64_t)(b % kXcds) * per + c;
+  if (c >= per || q >= count) return;
+  SymTile s;
+  sym_tile_at(a, s, whole ? q : a.whole + q / 4, TL::kCols);
+  if (whole) {
+    sym_tile<4, 4, false, false, kIn>(s, TL{(lds_t*)lds_mem});
+  } else {
+    s.m0 += q & 2 ? TS::kRows : 0;
+    s.n0 += q & 1 ? TS::kCols : 0;
+    if (s.m0 < a.m && s.n0 < a.m && s.m0 <= s.n0)
+      sym_tile<2, 2, true, false, kIn>(s, TS{(lds_t*)lds_mem});
+  }
 }
 
 // --------------------------------------------------------------- last product
@@ -825,12 +858,45 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
   return o;
 }
 
+// Which tiles a product takes, by how many there are.
+//
+// 256-wide ones bring half the operand bytes per multiply-add into LDS, and at the board's power
+// limit bytes are time.  They are taken from one per CU on, where they cover at most 1/8 more
+// than 128-wide ones do (diagonal tiles and the last row and column).  Up to 192 of them that
+// would start another round are done in quarters.  Five steps, without and with quarters, and in
+// 128-wide tiles: 32 of 1024 x 2048 (320 tiles) 3.41, 2.95, 3.15 ms; 8 of 2048 x 4096 (288)
+// 5.77, 4.80, 5.22 ms; 16 of them (576) 10.06, 9.45, 10.2 ms.  Where they cover more: 40 of 896 x
+// 1000 2.78 and 2.44 ms, 16 of 1400 x 1500 3.5 and 3.34 ms, 200 of 509 x 600 3.23 and 2.99 ms.
+//
+// 128-wide ones: from one per CU on two of their workgroups share a CU and hide each other's
+// prologue and epilogue.
+//
+// 64-wide ones where the 128-wide ones would leave half the CUs idle: a step of
+// theirs takes a third of the time.  One of 1024 x 2048 (36 tiles of 128): 271 us
+// against 360 us; five of 509 x 1283 (50): 207 and 280 us; one of 290 x 700 (6): 124
+// and 198 us; four of 1024 x 2048 (144): 618 and 466 us.
+//
+// The last product has 256-wide tiles from half a round on: it is dense, and its
+// epilogue is short (1 to 3% at 128 .. 512 tiles).
+constexpr int kCus = 256, kQuarters = 192, kSmall = 128;
+
 template <int MI, int NJ, bool kDeep, bool kTwoSums, bool kIn>
 void run_sym(SymArgs& a, int problems, hipStream_t s) {
   a.nt = ceil_div(a.m, 64 * NJ);
-  a.tiles = NJ / MI * (a.nt * (a.nt + 1) / 2);
-  a.total = (int64_t)problems * a.nmat * a.tiles;
+  a.tiles = a.nt * (a.nt + 1) / 2;
+  a.total = (int64_t)problems * a.nmat * a.tiles * (NJ / MI);
   ortho_sym<MI, NJ, kDeep, kTwoSums, kIn><<<(unsigned)pad_grid(a.total), kThreads, 0, s>>>(a);
+}
+
+template <bool kIn>
+void run_sym_rounds(SymArgs& a, int problems, hipStream_t s) {
+  a.nt = ceil_div(a.m, 256);
+  a.tiles = a.nt * (a.nt + 1) / 2;
+  a.total = (int64_t)problems * a.nmat * a.tiles;
+  const int64_t rest = a.total % kCus;
+  a.whole = rest <= kQuarters ? a.total - rest : a.total;
+  const int64_t blocks = pad_grid(a.whole) + pad_grid(4 * (a.total - a.whole));
+  ortho_sym_rounds<kIn><<<(unsigned)blocks, kThreads, 0, s>>>(a);
 }
 
 template <int MI, int NJ, bool kDeep>
@@ -841,33 +907,16 @@ void run_out(OutArgs& r, hipStream_t s) {
   ortho_out<MI, NJ, kDeep><<<(unsigned)pad_grid(r.total), kThreads, 0, s>>>(r);
 }
 
-// Which tiles a product takes, by how many there are.
-//
-// 256-wide ones from two rounds of them on; below, 128-wide ones fill the chip
-// more evenly, and from one per CU on two of their workgroups on a CU hide each
-// other's prologue and epilogue.  Five steps on 32, 16 and 8 matrices of 2048 x
-// 4096 (1152, 576, 288 tiles of 256): 18.5, 9.7, 5.6 ms with 256-wide tiles, 19.8, 10.0,
-// 5.1 ms with 128-wide ones; 32 of 1024 x 2048 (320 tiles): 3.3 and 3.0 ms.
-//
-// 64-wide ones where the 128-wide ones would leave half the CUs idle: a step of
-// theirs takes a third of the time.  One of 1024 x 2048 (36 tiles of 128): 271 us
-// against 360 us; five of 509 x 1283 (50): 207 and 280 us; one of 290 x 700 (6): 124
-// and 198 us; four of 1024 x 2048 (144): 618 and 466 us.
-//
-// The last product has 256-wide tiles from half a round on: it is dense, and its
-// epilogue is short (1 to 3% at 128 .. 512 tiles).
-constexpr int kCus = 256, kLarge = 512, kSmall = 128;
-
-// The product of one launch (kTwoSums: the first one, over n; kIn: the one that adds to its
+// The product of one launch (kTwoSums: the first one, over n, whose larger tile is 128 x 256; kIn: the one that adds to its
 // operand).
 template <bool kTwoSums, bool kIn>
 void run_product(SymArgs& a, int problems, hipStream_t s) {
   const int64_t n = (int64_t)problems * a.nmat;
   const int64_t n256 = ceil_div(a.m, 256), n128 = ceil_div(a.m, 128);
   const int64_t t256 = n * (n256 * (n256 + 1) / 2), t128 = n * (n128 * (n128 + 1) / 2);
-  if (t256 >= kLarge) {
+  if (t256 >= (kTwoSums ? 2 * kCus : kCus) && 32 * t256 <= 9 * t128) {
     if constexpr (kTwoSums) run_sym<2, 4, false, true, kIn>(a, problems, s);
-    else run_sym<4, 4, false, false, kIn>(a, problems, s);
+    else run_sym_rounds<kIn>(a, problems, s);
   } else if (t128 > kCus) {
     run_sym<2, 2, false, kTwoSums, kIn>(a, problems, s);
   } else if (t128 > kSmall) {

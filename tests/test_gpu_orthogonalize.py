@@ -58,8 +58,8 @@ def test_reference_is_the_oracle():
     assert np.allclose(reference(g, FIVE).cpu().numpy(), want, atol=1e-12)
 
 
-# one tile per matrix (one launch for all steps), its border, several tiles with few and with many
-# workgroups, the 256-wide tiles, and more matrices than one group takes
+# one tile per matrix, its border, several tiles with few and with many workgroups, and more
+# matrices than one group takes
 SIZES = [(1, 1, 1), (1, 1, 7), (3, 5, 3), (2, 33, 31), (2, 64, 130), (1, 127, 300), (2, 128, 128),
          (1, 128, 129), (1, 129, 128), (1, 129, 131), (2, 200, 515), (3, 257, 256), (1, 512, 513),
          (1, 300, 1000), (90, 130, 140), (40, 250, 272), (520, 256, 256), (180, 300, 310),
@@ -74,6 +74,16 @@ def test_matches_reference(size):
     if n <= 4:
         check(g.transpose(1, 2).contiguous(), what="transposed")
         check(g.bfloat16(), what="bf16")
+
+
+# 256-wide tiles, some of them in quarters, with odd edges; the 128 x 256 ones of the first product
+@pytest.mark.parametrize("size", [(26, 1010, 1025), (8, 2100, 1990), (53, 999, 1024)], ids=str)
+def test_large_tiles(size):
+    n, rows, cols = size
+    r = gen(n)
+    g = torch.randn(size, generator=r, device="cuda")
+    g[1] = torch.randn((rows, 2), generator=r, device="cuda") @ g[1, :2]
+    check(g, what="large tiles")
 
 
 @pytest.mark.parametrize("tokens", [1, 2, 5, 40])
