@@ -514,7 +514,8 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
         raise ValueError(f"g: expected [n,rows,cols] or [rows,cols], got {tuple(g.shape)}")
     n, rows, cols = (1, *g.shape) if g.dim() == 2 else g.shape
     dt = _float_type(g, "g")
-    flat = [tuple(c) for c in coeffs] if hasattr(coeffs[0], "__len__") else [tuple(coeffs)] * steps
+    nested = len(coeffs) == 0 or hasattr(coeffs[0], "__len__")
+    flat = [tuple(c) for c in coeffs] if nested else [tuple(coeffs)] * steps
     if len(flat) != steps or any(len(c) != 3 for c in flat):
         raise ValueError("coeffs: expected (a, b, c) or one (a, b, c) per step")
     dev = g.device

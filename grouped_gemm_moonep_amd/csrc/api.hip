@@ -4,6 +4,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <cmath>
+
 #include "internal.h"
 
 namespace moonep {
@@ -328,7 +330,9 @@ moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, in
     return MOONEP_ERR_ARG;
   double gain = 1.0;
   for (int i = 0; i < steps; ++i) {
-    if (!(coeffs[3 * i] > 0.0f)) return MOONEP_ERR_ARG;
+    if (!(coeffs[3 * i] > 0.0f) || !std::isfinite(coeffs[3 * i + 1]) ||
+        !std::isfinite(coeffs[3 * i + 2]))
+      return MOONEP_ERR_ARG;
     gain *= coeffs[3 * i];
     if (!(gain <= MOONEP_ORTHO_MAX_GAIN)) return MOONEP_ERR_ARG;
   }

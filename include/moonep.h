@@ -373,10 +373,10 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  * and out [n,rows,cols] = bf16_rne(X).  coeffs: HOST array [steps][3] of
  * (a, b, c), read before the call returns.  The products are taken on values
  * held to 22 bits and summed in fp32; with the usual five steps the rounding
- * left in X is about 10^-4 of its norm, up to 2 10^-3 for a matrix of rank one
- * (its bf16 values are rounded by 2 10^-3).  The a_i scale that rounding up, so
- * their product may be at most MOONEP_ORTHO_MAX_GAIN, each a_i > 0, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS,
- * eps > 0.  Coefficients have to keep X's singular values below 1.9, as those
+ * left in X is 10^-5 of its norm at full rank, up to 10^-3 for a matrix of rank
+ * one (its bf16 values are rounded by 2 10^-3).  The a_i scale that rounding up,
+ * so their product may be at most MOONEP_ORTHO_MAX_GAIN; each a_i > 0, b_i and
+ * c_i finite, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS, eps > 0.  Coefficients have to keep X's singular values below 1.9, as those
  * of any converging iteration do.  A zero matrix gives zeros; infinities and
  * NaN stay within their own matrix.
  * ws: device workspace of at least moonep_orthogonalize_ws bytes, 256-byte
@@ -385,8 +385,8 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  * not overlap.  The current device is used; no handle is needed. */
 #define MOONEP_ORTHO_MAX_STEPS 16
 #define MOONEP_ORTHO_MAX_GAIN 2048
-/* Workspace bytes for these sizes (host only): n >= 0, rows, cols >= 1,
- * rows * cols < 2^29; -1 otherwise. */
+/* Workspace bytes for these sizes (host only): n >= 0, 1 <= rows, cols <=
+ * 65536, rows * cols < 2^29; -1 otherwise. */
 int64_t moonep_orthogonalize_ws(int32_t n, int32_t rows, int32_t cols);
 moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
                                      int32_t cols, const float* coeffs, int32_t steps, float eps,

@@ -39,6 +39,7 @@ def ortho(n=1, rows=8, cols=8, g=FAKE, dtype=_abi.F32, coeffs=MUON_COEFFS * 5, s
     (dict(steps=17, coeffs=(1.0, 0.0, 0.0) * 17), ARG),
     (dict(eps=0.0), ARG), (dict(eps=float("nan")), ARG),
     (dict(coeffs=(0.0, 1.0, 1.0) * 5), ARG), (dict(coeffs=(float("nan"), 1.0, 1.0) * 5), ARG),
+    (dict(coeffs=(1.0, float("nan"), 0.0) * 5), ARG), (dict(coeffs=(1.0, 0.0, float("inf")) * 5), ARG),
     (dict(steps=7, coeffs=MUON_COEFFS * 7), ARG),          # 3.4445^7 > 2048
     (dict(g=None), ARG), (dict(out=None), ARG), (dict(ws=None), ARG), (dict(g=FAKE + 2), ARG),
     (dict(out=FAKE + 1), ARG), (dict(ws=FAKE + 16), ARG), (dict(ws_bytes=100), SCRATCH),
@@ -74,6 +75,8 @@ def test_orthogonalize_binding_refuses():
         orthogonalize(torch.zeros(4))
     with pytest.raises(ValueError, match="coeffs"):
         orthogonalize(g, coeffs=[(1.0, 2.0, 3.0)] * 4)
+    with pytest.raises(ValueError, match="coeffs"):
+        orthogonalize(g, coeffs=[])
     with pytest.raises(MoonepError) as e:
         orthogonalize_workspace(1, 0, 4, device="cpu")
     assert e.value.status == CONFIG
