@@ -65,9 +65,10 @@ _FLOATS = {torch.float32: _abi.F32, torch.bfloat16: _abi.BF16}
 
 
 def _float_type(t, name):
-    if t.dtype not in _FLOATS:
+    code = _FLOATS.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
-    return _FLOATS[t.dtype]
+    return code
 
 
 def _score(score):
@@ -86,23 +87,24 @@ def _same_device(device, **tensors):
 def _apart(name, out, **inputs):
     """`out`, a tensor of the caller's, must not share memory with any of `inputs`."""
     o0 = out.data_ptr()
-    o1 = o0 + out.numel() * out.element_size()
+    o1 = o0 + out.nbytes
     for n, t in inputs.items():
         if t is not None:
             p = t.data_ptr()
-            if o0 < p + t.numel() * t.element_size() and p < o1:
+            if p < o1 and o0 < p + t.nbytes:
                 raise ValueError(f"{name} must not overlap {n}")
 
 
 def _launch(dev, name, *args):
     """The C call `name` on the current stream of `dev`, which is made current for it."""
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        status = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    f, i = getattr(lib(), name), dev.index
+    if i == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
-    _abi.check(status, name)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status:
+        _abi.check(status, name)
 
 
 class Plan:
@@ -259,7 +261,7 @@ class Buffer:
         args = (_dev_ptr(dout, torch.bfloat16, (R, S, W), "dout"), W,
                 _dev_ptr(y_nvs, torch.bfloat16, (R, NvS, W), "y_nvs", not need_drw),
                 _dev_ptr(rw_nvs, torch.float32, (R, NvS), "rw_nvs"))
-        _same_device(dev, y_nvs=y_nvs, rw_nvs=rw_nvs, plan=plan.dest)
+        _same_device(dev, y_nvs=y_nvs, rw_nvs=rw_nvs, plan=plan.arrays["dest"])
         if dy_nvs is None:
             dy_nvs = torch.empty((R, NvS, W), dtype=torch.bfloat16, device=dev)
             p_dy = dy_nvs.data_ptr()
@@ -273,7 +275,7 @@ class Buffer:
             _same_device(dev, drw=drw)
             _apart("drw", drw, dout=dout, y_nvs=y_nvs, rw_nvs=rw_nvs, dy_nvs=dy_nvs)
         elif need_drw:
-            drw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            drw = torch.empty(R, S, K, dtype=torch.float32, device=dev)
             p_drw = drw.data_ptr()
         else:
             p_drw = None
@@ -293,16 +295,16 @@ class Buffer:
                 _float_type(logits, "logits"),
                 _dev_ptr(bias, torch.float32, (E,), "bias", True), _score(score),
                 1 if normalize else 0, scale)
-        if bias is not None:
+        if bias is not None and bias.device != dev:
             _same_device(dev, bias=bias)
         if topk is None:
-            topk = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+            topk = torch.empty(R, S, K, dtype=torch.int32, device=dev)
         else:
             _dev_ptr(topk, torch.int32, (R, S, K), "topk")
             _same_device(dev, topk=topk)
             _apart("topk", topk, logits=logits, bias=bias, rw=rw)
         if rw is None:
-            rw = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            rw = torch.empty(R, S, K, dtype=torch.float32, device=dev)
         else:
             _dev_ptr(rw, torch.float32, (R, S, K), "rw")
             _same_device(dev, rw=rw)

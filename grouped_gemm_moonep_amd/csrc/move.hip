@@ -233,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
 // butterfly over the lanes), so the result does not depend on the launch.
 // A chunk is read before it is written, so dy may be y itself.
 //
-// 262144 slots of 7168: 1580 us, 5.3 TB/s with the padding rows, the rate of a
+// 262144 slots of 7168: 1580 us, 5.2 TB/s with the padding rows, the rate of a
 // large copy on the same card.  It does not depend on the chunk (1 to 8 vectors
 // per lane, one item per wave: within 0.7%; 14 in flight 6% slower); plain
 // stores are 3% slower.  Non-temporal loads of y measure the same there, but
