@@ -86,6 +86,38 @@ def test_large_tiles(size):
     check(g, what="large tiles")
 
 
+@pytest.mark.parametrize("size", [(1, 65536, 8), (2, 8, 65536), (1, 40, 65533)], ids=str)
+def test_longest_sides(size):
+    check(torch.randn(size, generator=gen(1), device="cuda"), what="longest sides")
+
+
+# One entry per row, in columns of its own: its size is a singular value, so the result has the
+# same pattern and every entry goes through the steps alone.  Nearly as many elements as the call
+# takes, in both orientations; offsets pass 2^31 bytes in g, X_0 and the workspace.
+@pytest.mark.parametrize("transposed", [False, True])
+def test_largest_matrix(transposed):
+    m, n = 16384, 32760
+    r = gen(3)
+    col = torch.randperm(n, generator=r, device="cuda")[:m]
+    row = torch.arange(m, device="cuda")
+    value = torch.randn((m,), generator=r, device="cuda")
+    g = torch.zeros((n, m) if transposed else (m, n), device="cuda")
+    at = (col, row) if transposed else (row, col)
+    g[at] = value
+    out = orthogonalize(g)
+    x = value.double() / (torch.linalg.vector_norm(value.double()) + 1e-7)
+    for a, b, c in FIVE:
+        x = x * (a + b * x ** 2 + c * x ** 4)
+    got = out[at].double()
+    assert ((got - x).abs() <= 2.0 ** -8 * x.abs() + 4e4 * 2.0 ** -24).all()
+    out[at] = 0
+    assert not out.any()
+
+
+def test_no_matrices():
+    assert orthogonalize(torch.empty((0, 5, 7), device="cuda")).shape == (0, 5, 7)
+
+
 @pytest.mark.parametrize("tokens", [1, 2, 5, 40])
 @pytest.mark.parametrize("rows,cols", [(64, 96), (200, 515), (509, 1283)])
 def test_low_rank_gradients(tokens, rows, cols):
