@@ -4,8 +4,6 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include <cmath>
-
 #include "internal.h"
 
 namespace moonep {
@@ -328,14 +326,7 @@ moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, in
   if ((dtype != MOONEP_F32 && dtype != MOONEP_BF16) || !coeffs || !(eps > 0.0f) ||
       steps < 1 || steps > MOONEP_ORTHO_MAX_STEPS)
     return MOONEP_ERR_ARG;
-  double gain = 1.0;
-  for (int i = 0; i < steps; ++i) {
-    if (!(coeffs[3 * i] > 0.0f) || !std::isfinite(coeffs[3 * i + 1]) ||
-        !std::isfinite(coeffs[3 * i + 2]))
-      return MOONEP_ERR_ARG;
-    gain *= coeffs[3 * i];
-    if (!(gain <= MOONEP_ORTHO_MAX_GAIN)) return MOONEP_ERR_ARG;
-  }
+  if (!ortho_coeffs_ok(coeffs, steps)) return MOONEP_ERR_ARG;
   if (n == 0) return MOONEP_OK;
   if (!g || !out || !ws || !aligned(g, type_bytes(dtype)) || !aligned(out, 2) || !aligned(ws, 256))
     return MOONEP_ERR_ARG;

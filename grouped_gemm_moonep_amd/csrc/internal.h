@@ -136,6 +136,7 @@ hipError_t launch_route_bwd(const Ctx& c, const void* logits, const RouteForm& f
 
 // Newton-Schulz orthogonalisation (ortho.hip).
 bool ortho_shape_ok(int32_t n, int32_t rows, int32_t cols);
+bool ortho_coeffs_ok(const float* coeffs, int32_t steps);
 int64_t ortho_ws_bytes(int32_t n, int32_t rows, int32_t cols);
 hipError_t launch_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
                                 int32_t cols, const float* coeffs, int32_t steps, float eps,

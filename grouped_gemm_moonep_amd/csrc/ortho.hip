@@ -35,6 +35,8 @@
 // rows, as in gemm_core.h, whose loads, swizzle and ring are used as they are.  All
 // products are C = U V^T with both operands contiguous along K: the
 // m x m matrices are symmetric, and X_0 is written in both orientations.
+#include <cmath>
+
 #include "gemm_core.h"
 
 namespace moonep {
@@ -1022,6 +1024,41 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
 bool ortho_shape_ok(int32_t n, int32_t rows, int32_t cols) {
   return n >= 0 && rows >= 1 && cols >= 1 && rows <= 65536 && cols <= 65536 &&
          (int64_t)rows * cols < (int64_t(1) << 29);
+}
+
+// Whether every matrix stays within what a pair holds, whatever the input.  The eigenvalues of
+// A, R, T and P are functions of X's singular values, which start in [0, 1]; with x the largest
+// they can be before a step, and l = x^2 that of A, the step's
+//   r(l) = 1 + (b l + c l^2) / a  and  x' = max a x r(x^2)
+// have their extremes at the ends, at the vertex of r and where a + 3 b l + 5 c l^2 = 0.
+bool ortho_coeffs_ok(const float* coeffs, int32_t steps) {
+  constexpr double kMax = 3.99;                          // of 65504 / 2^14
+  double gain = 1.0, x = 1.0, p = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    const double a = coeffs[3 * i], b = coeffs[3 * i + 1], c = coeffs[3 * i + 2];
+    if (!(a > 0.0) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    gain *= a;
+    if (!(gain <= MOONEP_ORTHO_MAX_GAIN)) return false;
+    const double top = x * x;
+    const auto r = [&](double l) { return std::fabs(1.0 + (b * l + c * l * l) / a); };
+    double most = std::fmax(1.0, r(top)), next = a * x * r(top);
+    const auto at = [&](double l) {
+      if (!(l > 0.0 && l < top)) return;                 // (a NaN or infinity: no such point)
+      most = std::fmax(most, r(l));
+      next = std::fmax(next, a * std::sqrt(l) * r(l));
+    };
+    at(-b / (2.0 * c));
+    const double root = std::sqrt(9.0 * b * b - 20.0 * a * c);
+    at((-3.0 * b + root) / (10.0 * c));
+    at((-3.0 * b - root) / (10.0 * c));
+    at(-a / (3.0 * b));                                  // c = 0
+    p *= most;
+    // R, P and T = R A; the last step's result is not held as a pair
+    if (!(most <= kMax && p <= kMax && most * top <= kMax)) return false;
+    x = next;
+    if (i + 1 < steps && !(x * x <= kMax)) return false;
+  }
+  return true;
 }
 
 int64_t ortho_ws_bytes(int32_t n, int32_t rows, int32_t cols) {

@@ -376,9 +376,10 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  * left in X is 10^-5 of its norm at full rank, up to 10^-3 for a matrix of rank
  * one (its bf16 values are rounded by 2 10^-3).  The a_i scale that rounding up,
  * so their product may be at most MOONEP_ORTHO_MAX_GAIN; each a_i > 0, b_i and
- * c_i finite, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS, eps > 0.  Coefficients have
- * to keep X's singular values below 1.9, as those of any converging iteration
- * do.  A zero matrix gives zeros; infinities and NaN stay within their own
+ * c_i finite, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS, eps > 0.  Coefficients whose
+ * steps can take X's singular values past 1.99, or 1 + (b A + c A A) / a or the
+ * product of those past 3.99, are refused too (MOONEP_ERR_ARG): those of
+ * converging iterations stay well inside.  A zero matrix gives zeros; infinities and NaN stay within their own
  * matrix.
  * ws: device workspace of at least moonep_orthogonalize_ws bytes, 256-byte
  * aligned; its contents need not be kept between calls, and calls that overlap

@@ -40,12 +40,23 @@ def ortho(n=1, rows=8, cols=8, g=FAKE, dtype=_abi.F32, coeffs=MUON_COEFFS * 5, s
     (dict(eps=0.0), ARG), (dict(eps=float("nan")), ARG),
     (dict(coeffs=(0.0, 1.0, 1.0) * 5), ARG), (dict(coeffs=(float("nan"), 1.0, 1.0) * 5), ARG),
     (dict(coeffs=(1.0, float("nan"), 0.0) * 5), ARG), (dict(coeffs=(1.0, 0.0, float("inf")) * 5), ARG),
+    (dict(steps=1, coeffs=(0.1, 1.0, 0.0)), ARG),          # 1 + b / a = 11
+    (dict(steps=2, coeffs=(2.5, 0.0, 0.0) * 2), ARG),      # singular values up to 2.5 after one
+    (dict(steps=1, coeffs=(1.0, -20.0, 20.0)), ARG),       # 1 - 20 l + 20 l^2 is -4 at l = 1/2
+    (dict(steps=3, coeffs=(0.5, 0.4, 0.0) * 3), ARG),      # R at most 1.8, their product 5.8
     (dict(steps=7, coeffs=MUON_COEFFS * 7), ARG),          # 3.4445^7 > 2048
     (dict(g=None), ARG), (dict(out=None), ARG), (dict(ws=None), ARG), (dict(g=FAKE + 2), ARG),
     (dict(out=FAKE + 1), ARG), (dict(ws=FAKE + 16), ARG), (dict(ws_bytes=100), SCRATCH),
 ])
 def test_orthogonalize_refuses(bad, status):
     assert ortho(**bad) == status
+
+
+@pytest.mark.parametrize("coeffs", [MUON_COEFFS * 6, (1.5, -0.5, 0.0) * 16, (1.0, 0.0, 0.0) * 16,
+                                    (2.5, 0.0, 0.0), (1.875, -1.25, 0.375) * 10,
+                                    (8.0, -22.0, 15.8) + (3.9, -2.8, 0.5) * 2])
+def test_orthogonalize_takes_converging_coefficients(coeffs):
+    assert ortho(n=0, steps=len(coeffs) // 3, coeffs=coeffs) == _abi.MOONEP_OK
 
 
 def test_orthogonalize_of_nothing_is_nothing():
