@@ -47,7 +47,10 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kScale = 16384.0f;            // stored = value * 2^14
-constexpr int kParts = 256;                   // partial sums of a matrix's norm
+// Doubles per matrix in front of the workspace: partial sums of the squared norm, then |G| / (|G| +
+// eps), which is kept apart from the pairs (X_0 is held as G / |G|), for a gradient far below eps
+// would leave nothing in them.
+constexpr int kParts = 255, kNormLd = 256;
 constexpr int kK = 32;                        // values of K per step (a 64-element block)
 
 // ------------------------------------------------------------- K loop
@@ -569,6 +572,7 @@ struct SymArgs {
   const uint16_t* in;        // (kIn, one problem)
   int64_t ustride;           // elements between matrices of u and v
   int64_t ostride;           // of in and out
+  const double* factor;      // null, or a factor of each matrix's u and v, kNormLd apart
   float alpha, beta;
   int m, uld, ld, nk;        // as in SymTile
   int nt, tiles, nmat;       // square tiles along a side, of a matrix; matrices
@@ -616,6 +620,10 @@ void ortho_sym(SymArgs a) {
   const int part = (int)(t % (NJ / MI));
   sym_tile_at(a, s, t / (NJ / MI), TL::kCols);
   s.m0 += part * TL::kRows;
+  if (a.factor) {
+    const double f = a.factor[(t / (NJ / MI) / a.tiles % a.nmat) * kNormLd];
+    s.alpha = (float)(s.alpha * f * f);
+  }
   if (s.m0 < a.m) sym_tile<MI, NJ, kDeep, kTwoSums, kIn>(s, ring);
 }
 
@@ -653,6 +661,7 @@ struct OutArgs {
   const uint16_t* v;         // [nmat][mv][ld]
   uint16_t* out;             // [nmat][mu][mv]
   int64_t ustride, vstride;
+  const double* factor;      // of each matrix, kNormLd apart
   float alpha;
   int mu, mv, ld, nk, ntm, ntn, nmat, wide;   // wide: 16-byte stores are aligned
   int64_t total;
@@ -690,6 +699,8 @@ void ortho_out(OutArgs a) {
   if (idle) return;
 
   uint16_t* out = a.out + (mi * a.mu + m0) * (int64_t)a.mv + n0;
+  const float factor = (float)a.factor[mi * kNormLd];
+  const auto value = [&](float v) { return factor * (a.alpha * v); };
   typedef Stage<32 * MI, 32 * NJ> St;
   static_assert(St::kBytes <= TL::kWaveLds, "a wave's sub-tile is staged in its share of the ring");
   lds_t* reg = ring.base + wave * TL::kWaveLds;
@@ -700,8 +711,8 @@ void ortho_out(OutArgs a) {
 #pragma unroll
       for (int qd = 0; qd < 4; ++qd)
         St::put(reg, i, j, qd,
-                pack_bf16x2(a.alpha * acc[i][j][4 * qd], a.alpha * acc[i][j][4 * qd + 1]),
-                pack_bf16x2(a.alpha * acc[i][j][4 * qd + 2], a.alpha * acc[i][j][4 * qd + 3]));
+                pack_bf16x2(value(acc[i][j][4 * qd]), value(acc[i][j][4 * qd + 1])),
+                pack_bf16x2(value(acc[i][j][4 * qd + 2]), value(acc[i][j][4 * qd + 3])));
   if (a.wide) {
     St::flush(reg, make_rsrc(out, (int64_t)rows_valid * a.mv * 2), arow0, a.mv, bcol0, cols_valid);
     return;
@@ -757,22 +768,22 @@ __global__ __launch_bounds__(kThreads) void ortho_norm(const T* g, int64_t elems
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * kParts + blockIdx.x] = sh[0] + sh[1] + sh[2] + sh[3];
+  if (threadIdx.x == 0) part[(int64_t)blockIdx.y * kNormLd + blockIdx.x] = sh[0] + sh[1] + sh[2] + sh[3];
 }
 
-// X_0 in both orientations as pairs: a 64 x 64 piece of G per workgroup.  A lane
+// G / |G| in both orientations as pairs: a 64 x 64 piece of G per workgroup.  A lane
 // stores 16 bytes, hi or lo of eight values, so that eight lanes write a whole
 // 128-byte block row.
 template <class T>
 __global__ __launch_bounds__(kThreads) void ortho_load(const T* g, int rows, int cols, float eps,
-                                                       int wide, const double* part, uint16_t* nat,
+                                                       int wide, double* part, uint16_t* nat,
                                                        uint16_t* tr, int64_t nat_stride,
                                                        int64_t tr_stride) {
   __shared__ float tile[64][65];
   __shared__ double sh[kThreads / 64];
   const int64_t mi = blockIdx.z;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tid = threadIdx.x;
-  double s = part[mi * kParts + tid];
+  double s = tid < kParts ? part[mi * kNormLd + tid] : 0.0;
   const T* p = g + mi * rows * (int64_t)cols;
   float x[4][4];
   struct __attribute__((aligned(4 * sizeof(T)))) Four {
@@ -802,7 +813,9 @@ __global__ __launch_bounds__(kThreads) void ortho_load(const T* g, int rows, int
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
   if ((tid & 63) == 0) sh[tid >> 6] = s;
   __syncthreads();
-  const double f = (double)kScale / (sqrt(sh[0] + sh[1] + sh[2] + sh[3]) + (double)eps);
+  const double norm = sqrt(sh[0] + sh[1] + sh[2] + sh[3]);
+  const double f = norm > 0.0 ? (double)kScale / norm : norm;         // (a NaN stays one)
+  if (r0 == 0 && c0 == 0 && tid == 0) part[mi * kNormLd + kParts] = norm / (norm + (double)eps);
 #pragma unroll
   for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -850,7 +863,7 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
   o.x = up((int64_t)o.m * o.xld, 128);
   o.xt = up((int64_t)o.n * o.sld, 128);
   o.sq = up((int64_t)o.m * o.sld, 128);
-  o.bytes = 2 * (o.x + o.xt + 5 * o.sq) + kParts * (int64_t)sizeof(double);
+  o.bytes = 2 * (o.x + o.xt + 5 * o.sq) + kNormLd * (int64_t)sizeof(double);
   // Matrices per launch: enough for 8 rounds of 256-wide tiles on the 256 CUs (the last round
   // is then at most an eighth of the work); more would only take more memory.
   const int64_t nt = ceil_div(o.m, 256), tiles = nt * (nt + 1) / 2;
@@ -942,7 +955,7 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
   const OrthoLayout o = ortho_layout(n, rows, cols);
   const int64_t elems = (int64_t)rows * cols;
   double* part = (double*)ws;
-  uint16_t* x = (uint16_t*)(ws + (int64_t)o.group * kParts * sizeof(double));
+  uint16_t* x = (uint16_t*)(ws + (int64_t)o.group * kNormLd * sizeof(double));
   uint16_t* xt = x + o.group * o.x;
   uint16_t* sq[5];
   for (int i = 0; i < 5; ++i) sq[i] = xt + o.group * o.xt + i * (o.group * o.sq);
@@ -974,9 +987,11 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     set(1, x, x, A);
     a.in = A;
     a.ustride = o.x; a.uld = o.xld; a.nk = o.xld / BK;
+    a.factor = part + kParts;
     a.alpha = 1.0f / kScale; a.beta = 0.0f;
     run_product<true, false>(a, 1, s);
     a.ustride = o.sq; a.uld = o.sld; a.nk = o.sld / BK;
+    a.factor = nullptr;
     double gain = 1.0;
     for (int i = 0; i < steps; ++i) {
       const float ca = co[3 * i], cb = co[3 * i + 1], cc = co[3 * i + 2];
@@ -1008,6 +1023,7 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     r.ustride = tall ? o.xt : o.sq;
     r.vstride = tall ? o.sq : o.xt;
     r.out = out + i0 * elems;
+    r.factor = part + kParts;
     r.alpha = (float)(gain / ((double)kScale * kScale));
     r.mu = rows; r.mv = cols; r.ld = o.sld; r.nk = o.sld / BK;
     r.nmat = nm;

@@ -160,7 +160,8 @@ enum { MOONEP_SCORE_SOFTMAX = 0, MOONEP_SCORE_SIGMOID = 1 };
  *   rw [R,S,K] fp32 = scale * score_k, divided by the sum of the K chosen
  *   scores if `normalize` is nonzero.
  * A logit of -inf closes its expert: it comes after every open one, with a
- * weight of 0; a token without an open expert has weights of 0.  NaN logits
+ * weight of 0; a token without an open expert has weights of 0, and so has one
+ * whose chosen scores are all below 2^-126 (they count as 0).  NaN logits
  * come first and show in the weights.  The ids of a token are always distinct
  * and in range, as moonep_plan needs them.  The handle's R, S, K and E count;
  * no scratch is used, and outputs must not overlap the inputs. */

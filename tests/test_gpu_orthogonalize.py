@@ -169,6 +169,15 @@ def test_sizes_of_values():
     assert not torch.equal(small, want)
 
 
+@pytest.mark.parametrize("scale", [1e-8, 1e-13, 1e-20, 1e-30])
+def test_gradients_far_below_eps(scale):
+    """The result is then about the gains' product times G / eps, small but not lost."""
+    g = torch.randn((3, 60, 100), generator=gen(2), device="cuda") * scale
+    g[1] *= 1e3
+    check(g, what=f"times {scale:g}, eps 1e-7")
+    check(g.transpose(1, 2).contiguous().bfloat16(), what=f"times {scale:g}, eps 1e-7")
+
+
 def test_zero_and_bad_matrices_stay_by_themselves():
     for shape in ((5, 40, 60), (5, 140, 200)):
         g = torch.randn(shape, generator=gen(3), device="cuda")
