@@ -281,8 +281,9 @@ __device__ __forceinline__ void gemm3_loop(const RowTileT<2 * MI>& la, const Row
 // The loop of the 64 x 64 tile: a wave has one block and six MFMAs a step, too
 // few to slot the rest between, so the step is kept short instead.  A step's
 // fragments are read while the step before is multiplied; hi hi and the two
-// cross terms go to accumulators of their own (a chain of dependent MFMAs costs
-// twice their issue), which are added to the result every ten steps.
+// cross terms go to accumulators of their own (with two accumulators, chains of
+// four dependent MFMAs: 283 us in place of 239 us for one of 1024 x 2048), which are
+// added to the result every ten steps.
 struct Frag1 {
   bf16x8 a[4], b[4];                                     // columns kk
 };
@@ -300,7 +301,7 @@ __device__ __forceinline__ void read1(Frag1& f, const lds_t* A, const lds_t* Bt,
 template <int J>
 __device__ __forceinline__ void kstep1(const RowTileT<2>& la, const RowTileT<2>& lb,
                                        const Tile1& ring, int j, int nk, const Frag1& f,
-                                       Frag1& next, f32x16 acc[2], int arow0, int bcol0,
+                                       Frag1& next, f32x16 acc[3], int arow0, int bcol0,
                                        bool idle) {
   wait_dma<8>();                                         // step j + 1's tiles, in every wave,
   barrier_reads_done();                                  // and step j's fragments
@@ -313,7 +314,7 @@ __device__ __forceinline__ void kstep1(const RowTileT<2>& la, const RowTileT<2>&
                                                     __builtin_bit_cast(f16x8, f.a[i]), acc[x], 0,
                                                     0, 0);
   };
-  mma(1, 0, 2); mma(0, 0, 0); mma(1, 2, 0); mma(0, 1, 1); mma(1, 1, 3); mma(1, 3, 1);
+  mma(1, 0, 2); mma(0, 0, 0); mma(2, 2, 0); mma(1, 1, 3); mma(0, 1, 1); mma(2, 3, 1);
 }
 
 __device__ __forceinline__ void gemm1_loop(const RowTileT<2>& la, const RowTileT<2>& lb,
@@ -327,9 +328,9 @@ __device__ __forceinline__ void gemm1_loop(const RowTileT<2>& la, const RowTileT
   lb.issue(ring.b<2>(), 2 * BK, 2 < nk);
   la.issue(ring.a<3>(), 3 * BK, 3 < nk);
   lb.issue(ring.b<3>(), 3 * BK, 3 < nk);
-  f32x16 acc[2];
+  f32x16 acc[3];
 #pragma unroll
-  for (int v = 0; v < 16; ++v) sum[v] = acc[0][v] = acc[1][v] = 0.0f;
+  for (int v = 0; v < 16; ++v) sum[v] = acc[0][v] = acc[1][v] = acc[2][v] = 0.0f;
   wait_dma<12>();
   barrier_reads_done();
   Frag1 f, g;
@@ -347,8 +348,8 @@ __device__ __forceinline__ void gemm1_loop(const RowTileT<2>& la, const RowTileT
     if (j + 9 < nk) kstep1<4>(la, lb, ring, j + 9, nk, g, f, acc, arow0, bcol0, idle);
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-      sum[v] += acc[0][v] + acc[1][v];
-      acc[0][v] = acc[1][v] = 0.0f;
+      sum[v] += acc[0][v] + (acc[1][v] + acc[2][v]);
+      acc[0][v] = acc[1][v] = acc[2][v] = 0.0f;
     }
   }
   wait_loads<0>();
@@ -886,10 +887,12 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
 // 128-wide ones: from one per CU on two of their workgroups share a CU and hide each other's
 // prologue and epilogue.
 //
-// 64-wide ones where the 128-wide ones would leave half the CUs idle: a step of
-// theirs takes a third of the time.  One of 1024 x 2048 (36 tiles of 128): 271 us
-// against 360 us; five of 509 x 1283 (50): 207 and 280 us; one of 290 x 700 (6): 124
-// and 198 us; four of 1024 x 2048 (144): 618 and 466 us.
+// 64-wide ones where the 128-wide ones would leave half the CUs idle (a step of theirs takes a
+// third of the time), where up to two per CU of them would be a quarter or more empty, and where a
+// matrix is one of either.  One of 1024 x 2048 (36 tiles of 128): 239 us against 360 us; five of
+// 509 x 1283 (50): 196 and 280 us; one of 290 x 700 (6): 108 and 198 us; 24 of 290 x 700 (144, 5/8
+// of them filled) 232 and 282 us; 1000 of 50 x 100 400 and 470 us; but four of 1024 x 2048 (144)
+// 545 and 510 us.
 //
 // The last product has 256-wide tiles from half a round on: it is dense, and its
 // epilogue is short (1 to 3% at 128 .. 512 tiles).
@@ -929,12 +932,14 @@ void run_product(SymArgs& a, int problems, hipStream_t s) {
   const int64_t n = (int64_t)problems * a.nmat;
   const int64_t n256 = ceil_div(a.m, 256), n128 = ceil_div(a.m, 128);
   const int64_t t256 = n * (n256 * (n256 + 1) / 2), t128 = n * (n128 * (n128 + 1) / 2);
+  const int64_t n64 = ceil_div(a.m, 64), t64 = n * (n64 * (n64 + 1) / 2);
+  const bool small = t128 <= kSmall || t64 <= t128 || (t128 <= 2 * kCus && t64 <= 3 * t128);
   if (t256 >= (kTwoSums ? 2 * kCus : kCus) && 32 * t256 <= 9 * t128) {
     if constexpr (kTwoSums) run_sym<2, 4, false, true, kIn>(a, problems, s);
     else run_sym_rounds<kIn>(a, problems, s);
-  } else if (t128 > kCus) {
+  } else if (!small && t128 > kCus) {
     run_sym<2, 2, false, kTwoSums, kIn>(a, problems, s);
-  } else if (t128 > kSmall) {
+  } else if (!small) {
     run_sym<2, 2, true, kTwoSums, kIn>(a, problems, s);
   } else {
     run_sym<1, 1, true, false, kIn>(a, problems, s);
