@@ -153,9 +153,10 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 
 // Softmax over all experts of a row: its maximum and the inverse of its sum.  The exponentials
 // here are the hardware's (their error grows with the distance from the maximum as their
-// share of the sum falls).
-template <int G, int VPL>
-__device__ __forceinline__ void softmax_row(const float l[VPL], float* top, float* inv) {
+// share of the sum falls: |x| 2^-23 relative at e^x, under 2^-24 of the largest).
+// kKeep: l becomes the exponentials.
+template <int G, int VPL, bool kKeep = false>
+__device__ __forceinline__ void softmax_row(float l[VPL], float* top, float* inv) {
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
@@ -163,7 +164,11 @@ __device__ __forceinline__ void softmax_row(const float l[VPL], float* top, floa
   *top = finite_or_zero(group_maxf<G>(m));
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) s += __expf(l[i] - *top);
+  for (int i = 0; i < VPL; ++i) {
+    const float e = __expf(l[i] - *top);
+    s += e;
+    if (kKeep) l[i] = e;
+  }
   *inv = inv_or_zero(group_sum<G>(s));
 }
 
@@ -498,7 +503,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteArgs a) {
   float top = 0.0f, inv = 1.0f;
   if (dense) {
     load_row<T, G, VPL>(lrow, a.E, gl, a.wide, l);
-    softmax_row<G, VPL>(l, &top, &inv);
+    softmax_row<G, VPL, true>(l, &top, &inv);
   } else if (!kSigmoid) {
     top = finite_or_zero(group_maxf<G>(mx));
   }
@@ -531,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       d[i + e] = v[e];
-      if (dense) d[i + e] = expf(l[i + e] - top) * inv * (v[e] - gq);
+      if (dense) d[i + e] = l[i + e] * inv * (v[e] - gq);
     }
   }
   if (a.wide) {
