@@ -403,30 +403,44 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     // of the exact one (exponential, reciprocal and product: a few units of 2^-24 of
     // a value of at most 1, and the exponent's rounding, |x| 2^-24 relative,
     // where x e^-x < 0.4); its sum with the bias is rounded once more.
-    int limit = a.K < G ? G : a.K + 1;
-    if (limit > a.E) limit = a.E;
+    const int limit = a.K + 1 > a.E ? a.E : a.K < G ? (G < a.E ? G : a.E) : a.K + 1;
     int n = a.K;                                        // candidates
     bool close = false, more = true;
     float prev = INFINITY;
-    for (int k = 0; k < limit; ++k) {
-      const float v = key_value(draw(k, DEPTH));
+    const auto take = [&](int k, int deep) {            // false: no further draw is needed
+      const float v = key_value(draw(k, deep));
       const bool apart = prev - v > 0x1p-19f + 0x1p-22f * fabsf(prev);
       if (k < a.K) {
         if (k > 0 && !apart) close = true;
         prev = v;
-      } else {
-        more = more && !apart;
-        if (more) n = k + 1;
-        if (!__any(more)) break;
+        return true;
       }
+      more = more && !apart;
+      if (more) n = k + 1;
+      return (bool)__any(more);
+    };
+    if constexpr (kShort) {
+      // Ten draws at most, so only the 9 - k first keys of a list matter behind draw k.  The
+      // first nine find every list whole (next is its ninth key); the tenth, which says whether
+      // nine candidates are all, does unless one list gave those nine.
+      bool on = true, empty = false;
+#pragma unroll
+      for (int k = 0; k < 10; ++k)
+        if (on) {
+          if (k == 9) empty = __ballot(t[0] == no_key()) >> (lane - gl) & ((1ull << G) - 1);
+          on = take(k, 9 - k);
+        }
+      if (more || (empty && n == 9)) n = G + 1;
+    } else {
+      for (int k = 0; k < limit; ++k)
+        if (!take(k, DEPTH)) break;
     }
 #pragma unroll
     for (int q = 0; q < kSel; ++q) sel[q] = expert_of(sel[q]);
     if (close || n > a.K) {
       Exact<T, G, BY> ex;
       ex.init(lrow, a.bias, a.E, gl);
-      // a list of nine (next among them) is whole up to the ninth draw
-      const bool whole = (n < G || (n == G && n == a.E)) && (!kNext || n <= 9);
+      const bool whole = n < G || (n == G && n == a.E);
       if (whole) sel[0] = rank_candidates<T, G, BY>(ex, sel[0], n, gl);
       else choose_exact<T, G, BY, kSel>(ex, a.E, a.K, gl, sel);
     }

@@ -108,6 +108,25 @@ def test_ties_and_close_scores(E, K, score, kind):
     check(x, bias, K, score, True, 1.0)
 
 
+@pytest.mark.parametrize("K", [5, 8])
+@pytest.mark.parametrize("E", [256, 384, 512])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ahead", [0, 4, 7, 8])
+def test_best_experts_of_one_lane_are_close(E, K, dtype, ahead):
+    """Experts that one lane reads (16 bytes of every 256), of which `ahead` lead and the others
+    have one score in 32 bits and exact ones that rise with the expert: more candidates
+    than the lane keeps, and the last of them is the right one."""
+    per = 16 // torch.empty((), dtype=dtype).element_size()
+    mine = [e for e in range(E) if e // per % 16 == 3]
+    x = torch.full((1, 3, E), -6.0, device="cuda")
+    x[..., mine] = 1.0
+    x[..., mine[:ahead]] = 3.0
+    bias = torch.zeros((E,), device="cuda")
+    bias[mine] = torch.arange(1, len(mine) + 1, device="cuda") * 2.0 ** -30
+    check(x.to(dtype), bias, K, "sigmoid", True, 1.0)
+    check(x.to(dtype), bias, K, "softmax", True, 1.0)
+
+
 @pytest.mark.parametrize("score,normalize", [("softmax", True), ("softmax", False),
                                              ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("biased", [False, True])
