@@ -34,7 +34,8 @@
 // lo, zero behind the last value; a GEMM operand is then a 256-row tile of 128-byte
 // rows, as in gemm_core.h, whose loads, swizzle and ring are used as they are.  All
 // products are C = U V^T with both operands contiguous along K: the
-// m x m matrices are symmetric, and X_0 is written in both orientations.
+// m x m matrices are symmetric, and G / |G| is written in both orientations (X_0 is that times
+// |G| / (|G| + eps), which the first product's scale and the last one's take in).
 #include <cmath>
 
 #include "gemm_core.h"
@@ -925,8 +926,8 @@ void run_out(OutArgs& r, hipStream_t s) {
   ortho_out<MI, NJ, kDeep><<<(unsigned)pad_grid(r.total), kThreads, 0, s>>>(r);
 }
 
-// The product of one launch (kTwoSums: the first one, over n, whose larger tile is 128 x 256; kIn: the one that adds to its
-// operand).
+// The product of one launch (kTwoSums: the first one, over n, whose larger tile is 128 x 256;
+// kIn: the one that adds to its operand).
 template <bool kTwoSums, bool kIn>
 void run_product(SymArgs& a, int problems, hipStream_t s) {
   const int64_t n = (int64_t)problems * a.nmat;
