@@ -538,7 +538,8 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteArgs a) {
 #pragma unroll
   for (int q = 0; q < kSel; ++q) {
     float d = g[q];
-    if (!dense) d = (d - gq) * inv * p[q];
+    // the quotient first: it is at most 1, while the inverse of a sum of low sigmoids nears 2^128
+    if (!dense) d = (d - gq) * (p[q] * inv);
     if (kSigmoid) d *= sigmoid(-x[q]);
     if (id[q] >= 0) lds[id[q]] = d;
   }

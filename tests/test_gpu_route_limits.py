@@ -1,0 +1,74 @@
+"""moonep_route and moonep_route_bwd at the limits of fp32: chosen sigmoids that
+are nearly zero."""
+import pytest
+import torch
+
+from grouped_gemm_moonep_amd import Buffer
+from gpu_util import log
+from oracle import training as T
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def tiny_sigmoid_units(K):
+    """Roundings, in units of 2^-24, of a normalised weight s_k / t of sigmoids
+    below 2^-115: 2 for the exponential, 2 for the sum with 1 and the division, 4
+    for a result below 2^-126 (multiples of 2^-149 from 2^-128 on), K more for
+    the sum t of them, and 3 for its inverse and the products."""
+    return 8 + (8 + K) + 3
+
+
+@pytest.mark.parametrize("shape", [(1, 33, 2, 8), (2, 9, 8, 64), (3, 5, 20, 129), (2, 11, 8, 384),
+                                   (1, 7, 32, 512), (1, 3, 32, 1024)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1.0, 20.0, 500.0])
+def test_gradient_of_sigmoids_near_zero(shape, dtype, size):
+    """Every logit so low that the inverse of the chosen sigmoids' sum is 2^115
+    .. 2^128: the weights are ordinary and so are the gradients."""
+    R, S, K, E = shape
+    g = gen(E + K)
+    x = (-80 - 8.5 * torch.rand((R, S, E), generator=g, device="cuda")).to(dtype)
+    drw = size * torch.randn((R, S, K), generator=g, device="cuda")
+    drw[0, 0] = size                                     # equal: no gradient but the rounding's
+    buf = Buffer(R=R, S=S, K=K, E=E, H=64, Hp=64)
+    form = dict(score="sigmoid", normalize=True, scale=2.5)
+    ids, w = buf.route(x, **form)
+    d = buf.route_bwd(x, ids, drw, **form)
+    buf.destroy()
+    log(f"sigmoids near zero {shape} {dtype} drw {size}")
+    x64, dw = x.double().cpu().numpy(), drw.double().cpu().numpy()
+    want_ids, want_w = T.route(x64, K, **form)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    unit = tiny_sigmoid_units(K)
+    err = np.abs(w.double().cpu().numpy() - want_w)
+    assert (err <= (unit + 1) * U * want_w).all(), (err / want_w).max() / U
+    # (g_k - sum_j g_j w_j) w_k: the weights sum to 1, so the sum is off by a weight's roundings,
+    # its products' and its additions', the difference is at most twice the largest g
+    want = T.route_bwd(x64, want_ids, dw, **form)
+    tol = 2.5 * np.abs(dw).max(-1, keepdims=True) * U * (3 * unit + K + 12)
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * np.abs(want)
+    got = d.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+
+
+def test_gradient_of_two_equal_sigmoids_near_zero():
+    buf = Buffer(R=1, S=2, K=2, E=8, H=64, Hp=64)
+    x = torch.full((1, 2, 8), -88.0, device="cuda")
+    x[0, 0] = -87.0
+    ids, w = buf.route(x, score="sigmoid")
+    assert (w == 0.5).all()
+    drw = torch.tensor([[[20.0, -20.0], [4.0, -4.0]]], device="cuda")
+    d = buf.route_bwd(x, ids, drw, score="sigmoid")
+    buf.destroy()
+    want = torch.zeros_like(d)
+    want[0, 0, :2] = torch.tensor([10.0, -10.0])
+    want[0, 1, :2] = torch.tensor([2.0, -2.0])
+    assert torch.allclose(d, want, rtol=16 * U, atol=0)
