@@ -1,5 +1,6 @@
 """moonep_route and moonep_route_bwd at the limits of fp32: chosen sigmoids that
 are nearly zero."""
+import numpy as np
 import pytest
 import torch
 
