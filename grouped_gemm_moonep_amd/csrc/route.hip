@@ -153,7 +153,9 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 
 // Softmax over all experts of a row: its maximum and the inverse of its sum.  The exponentials
 // here are the hardware's (their error grows with the distance from the maximum as their
-// share of the sum falls: |x| 2^-23 relative at e^x, under 2^-24 of the largest).
+// share of the sum falls: |x| 2^-23 relative at e^x, under 2^-24 of the largest).  A lane adds
+// its own in four chains, so that no value passes more than VPL / 4 + 1 + log2 G <= 13 additions,
+// each of which may round a sum just above one up by 2^-24 of it.
 // kKeep: l becomes the exponentials.
 template <int G, int VPL, bool kKeep = false>
 __device__ __forceinline__ void softmax_row(float l[VPL], float* top, float* inv) {
@@ -162,14 +164,14 @@ __device__ __forceinline__ void softmax_row(float l[VPL], float* top, float* inv
   for (int i = 0; i < VPL; ++i)
     m = __builtin_fmaxf(m, l[i]);
   *top = finite_or_zero(group_maxf<G>(m));
-  float s = 0.0f;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const float e = __expf(l[i] - *top);
-    s += e;
+    s[i % 4] += e;
     if (kKeep) l[i] = e;
   }
-  *inv = inv_or_zero(group_sum<G>(s));
+  *inv = inv_or_zero(group_sum<G>((s[0] + s[1]) + (s[2] + s[3])));
 }
 
 // ------------------------------------------------------------------- keys
@@ -399,11 +401,13 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   }
   if constexpr (BY != kLogits) {
     // With a bias the draw goes on past K, up to G experts, while the scores
-    // stay within their rounding of the K-th.  A score in 32 bits is within 2^-20
-    // of the exact one (exponential, reciprocal and product: a few units of 2^-24 of
-    // a value of at most 1, and the exponent's rounding, |x| 2^-24 relative,
-    // where x e^-x < 0.4); a softmax's sum adds up to 35 half units, which scale all
-    // scores, and two of them are one at most.  The sum with the bias is rounded once more.
+    // stay within their rounding of the K-th, 32 units of 2^-24 for two scores together.
+    // A sigmoid is off by 2 units for the hardware's exponential and under 1 for its
+    // argument (|x| 2^-23 relative, where x e^-x < 0.4), 1 for the sum and 2 for the
+    // reciprocal.  A softmax's score likewise by 2 and 1 and 1 for the product, but two of them
+    // are at most 1 together; the sum, which scales both, by 13 for its additions, 2 and under
+    // 4 for its exponentials (the mean of |x| times the score is below 1.8 for 1024
+    // experts) and 1 for its inverse: 24 in all.  The sum with the bias is rounded once more.
     const int limit = a.K + 1 > a.E ? a.E : a.K < G ? (G < a.E ? G : a.E) : a.K + 1;
     int n = a.K;                                        // candidates
     bool close = false, more = true;

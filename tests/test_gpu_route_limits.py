@@ -1,5 +1,5 @@
 """moonep_route and moonep_route_bwd at the limits of fp32: chosen sigmoids that
-are nearly zero."""
+are nearly zero, softmax sums whose additions all round one way."""
 import numpy as np
 import pytest
 import torch
@@ -73,3 +73,41 @@ def test_gradient_of_two_equal_sigmoids_near_zero():
     want[0, 0, :2] = torch.tensor([10.0, -10.0])
     want[0, 1, :2] = torch.tensor([2.0, -2.0])
     assert torch.allclose(d, want, rtol=16 * U, atol=0)
+
+
+@pytest.mark.parametrize("dtype,E", [(torch.float32, 256), (torch.float32, 384), (torch.float32, 452),
+                                     (torch.float32, 512), (torch.float32, 1024),
+                                     (torch.bfloat16, 130), (torch.bfloat16, 384),
+                                     (torch.bfloat16, 392), (torch.bfloat16, 512),
+                                     (torch.bfloat16, 600)])
+@pytest.mark.parametrize("K", [1, 8, 9])
+def test_choice_by_a_softmax_whose_sum_rounds_up_throughout(dtype, E, K):
+    """One score near one, and 2^-24 of it for every other expert of its lane (16
+    bytes of every 256) and for one of each lane that its sum meets: each
+    addition to the sum rounds up.  The score with its bias stands a few units of
+    2^-24 above that of an expert with hardly a score, whose bias alone decides."""
+    R, S = 1, 3
+    per = 16 // torch.empty((), dtype=dtype).element_size()
+    low = -16.625 if dtype == torch.bfloat16 else float(np.log(1.02 * U))
+    buf = Buffer(R=R, S=S, K=K, E=E, H=64, Hp=64)
+    lane = (np.arange(E) // per) % 16
+    for lead in (0, per - 1, 5 * per, 16 * per):
+        x = np.full((R, S, E), -100.0)
+        mine = lane == lane[lead]
+        for q in (1, 2, 4, 8):
+            mine[np.flatnonzero(lane == lane[lead] ^ q)[0]] = True
+        x[..., mine] = low
+        x[..., lead] = 0
+        x = torch.from_numpy(x).to(dtype).cuda()
+        other = int(np.flatnonzero(~mine)[-1])
+        score = 1 - T.scores(x.double().cpu().numpy(), "softmax")[0, 0, lead]
+        for gap in range(-60, 61, 4):                    # units of 2^-24 between the two keys
+            bias = torch.full((E,), -10.0, device="cuda")
+            bias[lead] = -1
+            bias[other] = -score - (gap + 0.5) * U
+            want, w = T.route(x.double().cpu().numpy(), K, bias.double().cpu().numpy())
+            ids, rw = buf.route(x, bias)
+            assert np.array_equal(ids.cpu().numpy(), want), (lead, gap)
+            # 64 units for sums, products and exponentials, 2 for each of an argument of up to 100
+            assert np.allclose(rw.cpu().numpy(), w, rtol=(64 + 200) * U, atol=1e-30)
+    buf.destroy()
