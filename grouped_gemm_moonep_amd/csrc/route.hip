@@ -14,8 +14,9 @@
 //   sigmoid:    dl_k = dq_k sigma(l_k) sigma(-l_k), 0 elsewhere
 // A logit of -inf closes its expert: it comes after every open one and its
 // weight and gradient are 0; a token without an open expert has weights and
-// gradients of 0.  A NaN comes first, so it shows in the weights; whatever the
-// logits, the K ids of a token are distinct and in range.
+// gradients of 0.  A NaN comes first, so it shows in the weights (one in the bias comes
+// first too, though no weight shows it); whatever the logits and the bias, the K ids of a
+// token are distinct and in range.
 //
 // Design for CDNA4: the rows are short, so the kernels are bound by
 // instructions and by the latency of a row's few dependent steps, not by their
@@ -252,10 +253,10 @@ struct Exact {
     const float l = to_float<T>(row[e]);
     if (l == -INFINITY) return -INFINITY;
     const double x = (double)l;
-    const double s =
-        (BY == kSoftmaxBias ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x))) + (double)bias[e];
-    if (s == s) return s;
-    return x != x ? INFINITY : x == INFINITY ? 1e300 : x;   // a NaN before +inf
+    const double b = (double)bias[e];
+    const double s = (BY == kSoftmaxBias ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x))) + b;
+    if (x != x || b != b) return INFINITY;              // before all finite ones and +inf
+    return fmin(s == s ? s : x, 0x1.fffffffffffffp+1023);
   }
 };
 
@@ -354,12 +355,13 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       float s = l[c + i];
       // The hardware's exponential and reciprocal: within 2^-20 (see below).  A closed expert
       // keeps its -inf.  A softmax with a NaN or +inf has no scores: its logits order instead.
+      // A NaN in the bias comes first, as one in the logit does.
       if (BY == kSigmoidBias) {
         s = __builtin_amdgcn_rcpf(1.0f + __expf(-s)) + b[i];
         s = l[c + i] == -INFINITY ? -INFINITY : s;
       } else if (BY == kSoftmaxBias) {
         s = __expf(s - top) * inv + b[i];
-        s = l[c + i] == -INFINITY || s != s ? l[c + i] : s;
+        s = l[c + i] == -INFINITY || (s != s && b[i] == b[i]) ? l[c + i] : s;
       }
       k[i] = key_of(s + 0.0f, element_of<T, G>(gl, c + i));          // -0 as +0
     }

@@ -162,8 +162,10 @@ enum { MOONEP_SCORE_SOFTMAX = 0, MOONEP_SCORE_SIGMOID = 1 };
  * A logit of -inf closes its expert: it comes after every open one, with a
  * weight of 0; a token without an open expert has weights of 0, and so has one
  * whose chosen scores are all below 2^-126 (they count as 0).  NaN logits
- * come first and show in the weights.  The ids of a token are always distinct
- * and in range, as moonep_plan needs them.  The handle's R, S, K and E count;
+ * come first and show in the weights; an open expert with a NaN bias comes first
+ * too (its weight, which has no bias in it, does not show it), and one with a
+ * bias of -inf is chosen like a closed one.  The ids of a token are always
+ * distinct and in range, as moonep_plan needs them.  The handle's R, S, K and E count;
  * no scratch is used, and outputs must not overlap the inputs. */
 moonep_status_t moonep_route(moonep_handle_t h, const void* logits, int32_t dtype,
                              const float* bias, int32_t score, int32_t normalize, float scale,

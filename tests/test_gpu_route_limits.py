@@ -1,5 +1,6 @@
 """moonep_route and moonep_route_bwd at the limits of fp32: chosen sigmoids that
-are nearly zero, softmax sums whose additions all round one way."""
+are nearly zero, softmax sums whose additions all round one way, biases that
+are not finite."""
 import numpy as np
 import pytest
 import torch
@@ -111,3 +112,39 @@ def test_choice_by_a_softmax_whose_sum_rounds_up_throughout(dtype, E, K):
             # 64 units for sums, products and exponentials, 2 for each of an argument of up to 100
             assert np.allclose(rw.cpu().numpy(), w, rtol=(64 + 200) * U, atol=1e-30)
     buf.destroy()
+
+
+@pytest.mark.parametrize("E,K", [(16, 4), (64, 8), (129, 3), (256, 8), (384, 8), (512, 8), (300, 12),
+                                 (1024, 32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("close", [False, True])
+def test_a_bias_that_is_not_finite(E, K, score, close):
+    """Open experts with a NaN bias first, by their ids, then those with +inf,
+    last the closed ones and those with -inf, whether or not the other scores
+    are so close that they are compared in 64 bits."""
+    S = 9
+    g = gen(E)
+    x = 0.5 * torch.randn((1, S, E), generator=g, device="cuda")
+    bias = 0.3 * torch.randn((E,), generator=g, device="cuda")
+    if close:
+        x, bias = x.round(), torch.zeros_like(bias)
+    odd = torch.randperm(E, generator=g, device="cuda")[:7].tolist()
+    bias[odd[:2]] = float("nan")
+    bias[odd[2]] = -float("nan")
+    bias[odd[3:5]] = float("inf")
+    bias[odd[5]] = -float("inf")
+    x[0, 1::3, odd[0]] = -float("inf")                   # closed all the same
+    x[0, 2, :] = -float("inf")
+    x[0, 2, odd[1:4]] = 0.5
+    x64 = x.double().cpu().numpy()
+    key = T.scores(x64, score) + bias.double().cpu().numpy()
+    key = np.where(np.isposinf(key), 1e300, key)
+    key = np.where(np.isnan(key), np.inf, key)
+    key[np.isneginf(x64)] = -np.inf
+    want = np.argsort(-key, axis=-1, kind="stable")[..., :K]
+    buf = Buffer(R=1, S=S, K=K, E=E, H=64, Hp=64)
+    ids, w = buf.route(x, bias, score=score, normalize=False)
+    buf.destroy()
+    assert np.array_equal(ids.cpu().numpy(), want)
+    want_w = np.take_along_axis(T.scores(x64, score), want, -1)
+    assert np.allclose(w.cpu().numpy(), want_w, rtol=80 * U, atol=0)
