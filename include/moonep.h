@@ -156,17 +156,18 @@ enum { MOONEP_SCORE_SOFTMAX = 0, MOONEP_SCORE_SIGMOID = 1 };
  *   the choice goes by l_e, or by score_e + bias_e if bias [E] fp32 is given
  *   (a selection bias: it takes no part in the weights);
  *   topk [R,S,K]: the K largest in descending order, equal ones by ascending
- *   id (scores with a bias are compared as if computed exactly);
+ *   id (scores with a bias are compared as computed in 64 bits);
  *   rw [R,S,K] fp32 = scale * score_k, divided by the sum of the K chosen
  *   scores if `normalize` is nonzero.
  * A logit of -inf closes its expert: it comes after every open one, with a
  * weight of 0; a token without an open expert has weights of 0, and so has one
- * whose chosen scores are all below 2^-126 (they count as 0).  NaN logits
- * come first and show in the weights; an open expert with a NaN bias comes first
- * too (its weight, which has no bias in it, does not show it), and one with a
- * bias of -inf is chosen like a closed one.  The ids of a token are always
- * distinct and in range, as moonep_plan needs them.  The handle's R, S, K and E count;
- * no scratch is used, and outputs must not overlap the inputs. */
+ * whose chosen sigmoids are all 0 in fp32 (logits below -88.73; down to there
+ * normalized weights and their gradient are ordinary).  NaN logits come first
+ * and show in the weights; an open expert with a NaN bias comes first too (its
+ * weight, which has no bias in it, does not show it), and one with a bias of
+ * -inf is chosen like a closed one.  The ids of a token are always distinct and
+ * in range, as moonep_plan needs them.  The handle's R, S, K and E count; no
+ * scratch is used, and outputs must not overlap the inputs. */
 moonep_status_t moonep_route(moonep_handle_t h, const void* logits, int32_t dtype,
                              const float* bias, int32_t score, int32_t normalize, float scale,
                              int32_t* topk, float* rw, hipStream_t stream);

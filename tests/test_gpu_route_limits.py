@@ -148,3 +148,46 @@ def test_a_bias_that_is_not_finite(E, K, score, close):
     assert np.array_equal(ids.cpu().numpy(), want)
     want_w = np.take_along_axis(T.scores(x64, score), want, -1)
     assert np.allclose(w.cpu().numpy(), want_w, rtol=80 * U, atol=0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("biased", [False, True])
+def test_where_sigmoids_count_as_zero(dtype, biased):
+    """The sigmoid in fp32 is 0 from -88.73 down: a token with no other has weights and
+    gradients of 0, one with a logit on the other side has them of that one alone."""
+    S, E, K = 4, 40, 4
+    above, below = (-88.5, -89.0) if dtype == torch.bfloat16 else (-88.72, -88.73)
+    x = torch.full((1, S, E), below, device="cuda")
+    x[0, 1] = above
+    x[0, 2, 7] = above
+    x[0, 3, :36] = -float("inf")
+    bias = torch.zeros((E,), device="cuda") if biased else None
+    buf = Buffer(R=1, S=S, K=K, E=E, H=64, Hp=64)
+    ids, w = buf.route(x.to(dtype), bias, score="sigmoid", scale=2.0)
+    drw = torch.tensor([9.0, -9.0, 5.0, 1.0], device="cuda").expand(1, S, K).contiguous()
+    d = buf.route_bwd(x.to(dtype), ids, drw, score="sigmoid", scale=2.0)
+    buf.destroy()
+    assert not w[0, [0, 3]].any() and not d[0, [0, 3]].any()
+    assert ids[0, 2, 0] == 7 and w[0, 2].tolist() == [2.0, 0.0, 0.0, 0.0] and not d[0, 2].any()
+    assert torch.allclose(w[0, 1], torch.full((K,), 0.5, device="cuda"), rtol=16 * U, atol=0)
+    want = 2 * (drw[0, 1] - 1.5) / K
+    got = d[0, 1, ids[0, 1].long()].float()
+    tol = 2.0 ** -8 * want.abs() + (3 * tiny_sigmoid_units(K) + K + 12) * U * 18
+    assert (got - want).abs().le(tol).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_equal_in_64_bits_go_by_expert(score):
+    """A sigmoid of 41 is above one of 40, and a softmax of -800 above one of -900,
+    but not in 64 bits."""
+    x = torch.full((1, 1, 32), -50.0 if score == "sigmoid" else -1000.0, device="cuda")
+    high = (40.0, 41.0, 42.0) if score == "sigmoid" else (-900.0, -850.0, -800.0)
+    x[0, 0, [5, 11, 30]] = torch.tensor(high, device="cuda")
+    x[0, 0, 20] = 39.9 if score == "sigmoid" else 0.0
+    buf = Buffer(R=1, S=1, K=4, E=32, H=64, Hp=64)
+    bias = torch.zeros((32,), device="cuda")
+    bias[[5, 11, 30]] = 0.25
+    ids, _ = buf.route(x, bias, score=score)
+    buf.destroy()
+    want = [5, 11, 30, 20] if score == "sigmoid" else [20, 5, 11, 30]
+    assert ids[0, 0].tolist() == want
