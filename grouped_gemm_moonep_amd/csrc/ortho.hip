@@ -26,7 +26,8 @@
 // (2^-12) operands would leave nothing there, so every matrix is held as a
 // pair of fp16, v = hi + lo (22 bits), and a product is hi hi + hi lo + lo hi
 // on the matrix units, summed in fp32.  Before its rounding to bf16 (1.7e-3 of its norm) the
-// result is then off by 1e-5 of its norm at full rank, 3e-4 .. 1.1e-3 at rank one.
+// result is then off by 1e-5 of its norm at full rank, at rank one by 3e-4 .. 2.4e-3 for m up to
+// 2048 (the more the fewer rows hold its norm).
 // Values are scaled by 2^14, so entries up to 4 are held, and down to 2^-28
 // with 11 or more bits.
 //
@@ -926,8 +927,8 @@ void run_out(OutArgs& r, hipStream_t s) {
   ortho_out<MI, NJ, kDeep><<<(unsigned)pad_grid(r.total), kThreads, 0, s>>>(r);
 }
 
-// The product of one launch (kTwoSums: the first one, over n, whose larger tile is 128 x 256;
-// kIn: the one that adds to its operand).
+// The product of one launch (kTwoSums: the one over n and the first step's, whose larger tile is
+// 128 x 256; kIn: the one that adds to its operand).
 template <bool kTwoSums, bool kIn>
 void run_product(SymArgs& a, int problems, hipStream_t s) {
   const int64_t n = (int64_t)problems * a.nmat;
@@ -988,7 +989,12 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
     };
     uint16_t *A = sq[0], *R = sq[1], *Tm = sq[2], *P = sq[3], *P2 = sq[4];
     // The first product with two sums: a chain of fp32 additions over all of n would round by
-    // 2e-7 .. 7e-7 of the sum, which a low-rank result shows thousands of times larger.
+    // 2e-7 .. 7e-7 of the sum, which a low-rank result shows thousands of times larger.  So it does
+    // what the first step's products lose: T = R A is a fifth of its terms where a singular value
+    // is one, and its rounding reaches the result 6800 times larger, that of the second step's
+    // 1700 times and the third's 400 times.  Rank one, most of the norm in few rows, worst of 32 of
+    // 2048 x 7168: 4.1e-3 with one chain, 2.0e-3 with two sums here, 1.8e-3 in the second step too,
+    // 1.3e-3 in all (21.2, 21.6, 22.2 and 23.7 ms).
     set(0, x, x, A);
     set(1, x, x, A);
     a.in = A;
@@ -1011,16 +1017,19 @@ hipError_t orthogonalize(const T* g, int n, int rows, int cols, const float* co,
       uint16_t* Ri = i == 0 ? P : R;                     // P of the first step is its R
       set(0, A, A, Ri);
       a.alpha = cc / ca / kScale; a.beta = cb / ca;
-      run_product<false, true>(a, 1, s);
+      if (i == 0) run_product<true, true>(a, 1, s);
+      else run_product<false, true>(a, 1, s);
       a.alpha = 1.0f / kScale;
       int k = 0;
       if (more) set(k++, Ri, A, Tm);
       if (i > 0) set(k++, Ri, P2, P);
-      if (k) run_product<false, false>(a, k, s);
+      if (k && i == 0) run_product<true, false>(a, k, s);
+      else if (k) run_product<false, false>(a, k, s);
       if (more) {
         set(0, Ri, Tm, A);
         a.alpha = ca * ca / kScale;
-        run_product<false, false>(a, 1, s);
+        if (i == 0) run_product<true, false>(a, 1, s);
+        else run_product<false, false>(a, 1, s);
       }
     }
     OutArgs r;

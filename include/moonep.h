@@ -377,8 +377,10 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  * and out [n,rows,cols] = bf16_rne(X).  coeffs: HOST array [steps][3] of
  * (a, b, c), read before the call returns.  The products are taken on values
  * held to 22 bits and summed in fp32; with the usual five steps the rounding
- * left in X is 10^-5 of its norm at full rank, up to 10^-3 for a matrix of rank
- * one (its bf16 values are rounded by 2 10^-3).  The a_i scale that rounding up,
+ * left in X is 10^-5 of its norm at full rank; at rank one, with 2048 or fewer
+ * on the shorter side, 3 10^-4 where all rows share the norm and up to 3 10^-3
+ * where a few hold most of it, which grows with the shorter side (4.4 10^-3 at
+ * 16384).  Rounding X to bf16 leaves 2 10^-3.  The a_i scale that rounding up,
  * so their product may be at most MOONEP_ORTHO_MAX_GAIN; each a_i > 0, b_i and
  * c_i finite, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS, eps > 0.  Coefficients whose
  * steps can take X's singular values past 1.99, or 1 + (b A + c A A) / a or the
