@@ -76,6 +76,7 @@ def lib():
         "moonep_route": (i32, [vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp]),
         "moonep_route_bwd": (i32, [vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp]),
         "moonep_orthogonalize_ws": (i64, [i32, i32, i32]),
+        "moonep_orthogonalize_tile": (i32, [i32, i32, i32, i32]),
         "moonep_orthogonalize": (i32, [vp, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_float), i32,
                                        ctypes.c_float, vp, vp, i64, vp]),
         "moonep_copy_rows": (i32, [vp, ctypes.POINTER(MoonepPlan), vp, i32, vp, vp]),
@@ -133,6 +134,8 @@ def plan_len(cfg: MoonepConfig, which: int) -> int:
  GRID_COMBINE_BWD) = range(6)
 F32, BF16 = range(2)
 SCORES = {"softmax": 0, "sigmoid": 1}
+ORTHO_PRODUCTS = ORTHO_FIRST, ORTHO_R, ORTHO_TP, ORTHO_A, ORTHO_LAST = tuple(range(5))
+TILE_64, TILE_128_DEEP, TILE_128, TILE_128X256, TILE_256 = range(5)
 
 
 def launch_grid(cfg: MoonepConfig, which: int, W: int = 0, device_cus: int = 256) -> int:

@@ -318,6 +318,10 @@ int64_t moonep_orthogonalize_ws(int32_t n, int32_t rows, int32_t cols) {
   return ortho_shape_ok(n, rows, cols) ? ortho_ws_bytes(n, rows, cols) : -1;
 }
 
+int32_t moonep_orthogonalize_tile(int32_t n, int32_t rows, int32_t cols, int32_t product) {
+  return n >= 1 && ortho_shape_ok(n, rows, cols) ? ortho_tile(n, rows, cols, product) : -1;
+}
+
 moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
                                      int32_t cols, const float* coeffs, int32_t steps, float eps,
                                      uint16_t* out, void* ws, int64_t ws_bytes,

@@ -138,6 +138,7 @@ hipError_t launch_route_bwd(const Ctx& c, const void* logits, const RouteForm& f
 bool ortho_shape_ok(int32_t n, int32_t rows, int32_t cols);
 bool ortho_coeffs_ok(const float* coeffs, int32_t steps);
 int64_t ortho_ws_bytes(int32_t n, int32_t rows, int32_t cols);
+int32_t ortho_tile(int32_t n, int32_t rows, int32_t cols, int32_t product);
 hipError_t launch_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
                                 int32_t cols, const float* coeffs, int32_t steps, float eps,
                                 uint16_t* out, void* ws, hipStream_t s);

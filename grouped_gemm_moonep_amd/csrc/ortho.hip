@@ -876,7 +876,7 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
   return o;
 }
 
-// Which tiles a product takes, by how many there are.
+// Which tiles a product takes, by how many there are (MOONEP_ORTHO_TILE_*).
 //
 // 256-wide ones bring half the operand bytes per multiply-add into LDS, and at the board's power
 // limit bytes are time.  They are taken from one per CU on, where they cover at most 1/8 more
@@ -927,33 +927,45 @@ void run_out(OutArgs& r, hipStream_t s) {
   ortho_out<MI, NJ, kDeep><<<(unsigned)pad_grid(r.total), kThreads, 0, s>>>(r);
 }
 
-// The product of one launch (kTwoSums: the one over n and the first step's, whose larger tile is
-// 128 x 256; kIn: the one that adds to its operand).
+// The tile of a launch over n symmetric m x m products (two_sums: the one over the long side and
+// the first step's, whose larger tile is 128 x 256).
+int sym_tile_of(int m, int64_t n, bool two_sums) {
+  const int64_t n256 = ceil_div(m, 256), n128 = ceil_div(m, 128), n64 = ceil_div(m, 64);
+  const int64_t t256 = n * (n256 * (n256 + 1) / 2), t128 = n * (n128 * (n128 + 1) / 2);
+  const int64_t t64 = n * (n64 * (n64 + 1) / 2);
+  const bool small = t128 <= kSmall || t64 <= t128 || (t128 <= 2 * kCus && t64 <= 3 * t128);
+  if (t256 >= (two_sums ? 2 * kCus : kCus) && 32 * t256 <= 9 * t128)
+    return two_sums ? MOONEP_ORTHO_TILE_128X256 : MOONEP_ORTHO_TILE_256;
+  if (small) return MOONEP_ORTHO_TILE_64;
+  return t128 > kCus ? MOONEP_ORTHO_TILE_128 : MOONEP_ORTHO_TILE_128_DEEP;
+}
+
+int last_tile_of(int mu, int mv, int64_t n) {
+  const int64_t t256 = n * ceil_div(mu, 256) * ceil_div(mv, 256);
+  const int64_t t128 = n * ceil_div(mu, 128) * ceil_div(mv, 128);
+  if (t256 >= kSmall) return MOONEP_ORTHO_TILE_256;
+  return t128 > kSmall ? MOONEP_ORTHO_TILE_128_DEEP : MOONEP_ORTHO_TILE_64;
+}
+
+// The product of one launch (kIn: the one that adds to its operand).
 template <bool kTwoSums, bool kIn>
 void run_product(SymArgs& a, int problems, hipStream_t s) {
-  const int64_t n = (int64_t)problems * a.nmat;
-  const int64_t n256 = ceil_div(a.m, 256), n128 = ceil_div(a.m, 128);
-  const int64_t t256 = n * (n256 * (n256 + 1) / 2), t128 = n * (n128 * (n128 + 1) / 2);
-  const int64_t n64 = ceil_div(a.m, 64), t64 = n * (n64 * (n64 + 1) / 2);
-  const bool small = t128 <= kSmall || t64 <= t128 || (t128 <= 2 * kCus && t64 <= 3 * t128);
-  if (t256 >= (kTwoSums ? 2 * kCus : kCus) && 32 * t256 <= 9 * t128) {
-    if constexpr (kTwoSums) run_sym<2, 4, false, true, kIn>(a, problems, s);
-    else run_sym_rounds<kIn>(a, problems, s);
-  } else if (!small && t128 > kCus) {
-    run_sym<2, 2, false, kTwoSums, kIn>(a, problems, s);
-  } else if (!small) {
-    run_sym<2, 2, true, kTwoSums, kIn>(a, problems, s);
-  } else {
-    run_sym<1, 1, true, false, kIn>(a, problems, s);
+  switch (sym_tile_of(a.m, (int64_t)problems * a.nmat, kTwoSums)) {
+    case MOONEP_ORTHO_TILE_64: run_sym<1, 1, true, false, kIn>(a, problems, s); break;
+    case MOONEP_ORTHO_TILE_128_DEEP: run_sym<2, 2, true, kTwoSums, kIn>(a, problems, s); break;
+    case MOONEP_ORTHO_TILE_128: run_sym<2, 2, false, kTwoSums, kIn>(a, problems, s); break;
+    default:
+      if constexpr (kTwoSums) run_sym<2, 4, false, true, kIn>(a, problems, s);
+      else run_sym_rounds<kIn>(a, problems, s);
   }
 }
 
 void run_last(OutArgs& r, hipStream_t s) {
-  const int64_t t256 = (int64_t)r.nmat * ceil_div(r.mu, 256) * ceil_div(r.mv, 256);
-  const int64_t t128 = (int64_t)r.nmat * ceil_div(r.mu, 128) * ceil_div(r.mv, 128);
-  if (t256 >= kSmall) run_out<4, 4, false>(r, s);
-  else if (t128 > kSmall) run_out<2, 2, true>(r, s);
-  else run_out<1, 1, true>(r, s);
+  switch (last_tile_of(r.mu, r.mv, r.nmat)) {
+    case MOONEP_ORTHO_TILE_64: run_out<1, 1, true>(r, s); break;
+    case MOONEP_ORTHO_TILE_128_DEEP: run_out<2, 2, true>(r, s); break;
+    default: run_out<4, 4, false>(r, s);
+  }
 }
 
 template <class T>
@@ -1096,6 +1108,17 @@ int64_t ortho_ws_bytes(int32_t n, int32_t rows, int32_t cols) {
   if (n == 0) return 0;
   const OrthoLayout o = ortho_layout(n, rows, cols);
   return o.group * o.bytes;
+}
+
+int32_t ortho_tile(int32_t n, int32_t rows, int32_t cols, int32_t product) {
+  const OrthoLayout o = ortho_layout(n, rows, cols);
+  switch (product) {
+    case MOONEP_ORTHO_FIRST: return sym_tile_of(o.m, o.group, true);
+    case MOONEP_ORTHO_R: case MOONEP_ORTHO_A: return sym_tile_of(o.m, o.group, false);
+    case MOONEP_ORTHO_TP: return sym_tile_of(o.m, 2 * (int64_t)o.group, false);
+    case MOONEP_ORTHO_LAST: return last_tile_of(rows, cols, o.group);
+    default: return -1;
+  }
 }
 
 hipError_t launch_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,

@@ -385,8 +385,8 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  * c_i finite, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS, eps > 0.  Coefficients whose
  * steps can take X's singular values past 1.99, or 1 + (b A + c A A) / a or the
  * product of those past 3.99, are refused too (MOONEP_ERR_ARG): those of
- * converging iterations stay well inside.  A zero matrix gives zeros; infinities and NaN stay within their own
- * matrix.
+ * converging iterations stay well inside.  A zero matrix gives zeros; infinities
+ * and NaN stay within their own matrix.
  * ws: device workspace of at least moonep_orthogonalize_ws bytes, 256-byte
  * aligned; its contents need not be kept between calls, and calls that overlap
  * need one each (MOONEP_ERR_SCRATCH if it is too small).  g, out and ws must
@@ -396,6 +396,23 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
 /* Workspace bytes for these sizes (host only): n >= 0, 1 <= rows, cols <=
  * 65536, rows * cols < 2^29; -1 otherwise. */
 int64_t moonep_orthogonalize_ws(int32_t n, int32_t rows, int32_t cols);
+/* Tile (MOONEP_ORTHO_TILE_*) that a product (MOONEP_ORTHO_*) of n >= 1 such
+ * matrices is computed in (host only): FIRST is X X^T and all of the first
+ * step's, then in every step R = I + (b A + c A A) / a, TP the launch of both T =
+ * R A and P = R P, and A = a^2 R T, LAST is P X.  Many matrices are taken in
+ * groups; this is the first group's.  -1 for sizes or a product that there is
+ * not. */
+enum {
+  MOONEP_ORTHO_FIRST = 0, MOONEP_ORTHO_R, MOONEP_ORTHO_TP, MOONEP_ORTHO_A, MOONEP_ORTHO_LAST
+};
+enum {
+  MOONEP_ORTHO_TILE_64 = 0,
+  MOONEP_ORTHO_TILE_128_DEEP,  /* operands fetched four steps ahead          */
+  MOONEP_ORTHO_TILE_128,       /* two workgroups per CU                      */
+  MOONEP_ORTHO_TILE_128X256,
+  MOONEP_ORTHO_TILE_256        /* of the m x m products the last in quarters */
+};
+int32_t moonep_orthogonalize_tile(int32_t n, int32_t rows, int32_t cols, int32_t product);
 moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t rows,
                                      int32_t cols, const float* coeffs, int32_t steps, float eps,
                                      uint16_t* out, void* ws, int64_t ws_bytes,
