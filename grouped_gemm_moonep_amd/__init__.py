@@ -95,14 +95,23 @@ def _apart(name, out, **inputs):
                 raise ValueError(f"{name} must not overlap {n}")
 
 
+def _stream_of(i):
+    return torch.cuda.current_stream(i).cuda_stream
+
+
+# What torch.cuda's own functions call, a microsecond less each; torch does not promise them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _launch(dev, name, *args):
     """The C call `name` on the current stream of `dev`, which is made current for it."""
     f, i = getattr(lib(), name), dev.index
-    if i == torch._C._cuda_getDevice():
-        status = f(*args, torch._C._cuda_getCurrentRawStream(i))
+    if i == _current_device():
+        status = f(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch._C._cuda_getCurrentRawStream(i))
+            status = f(*args, _raw_stream(i))
     if status:
         _abi.check(status, name)
 
