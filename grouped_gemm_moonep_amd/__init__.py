@@ -31,6 +31,7 @@ experts purely by row index.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -514,6 +515,27 @@ def orthogonalize_workspace(n, rows, cols, device="cuda"):
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
+def _refused_steps(flat, eps):
+    """What moonep_orthogonalize refuses of the steps (a, b, c) and eps, or None."""
+    args = (ctypes.c_float * (3 * len(flat)))(*[v for c in flat for v in c])
+    # of no matrices it looks at nothing else
+    if not lib().moonep_orthogonalize(None, _abi.F32, 0, 1, 1, args, len(flat), eps, None, None, 0,
+                                      None):
+        return None
+    if not 1 <= len(flat) <= _abi.ORTHO_MAX_STEPS:
+        return f"{len(flat)} steps, 1 to {_abi.ORTHO_MAX_STEPS} are taken"
+    if not eps > 0:
+        return f"eps {eps}, it has to be positive"
+    if not all(math.isfinite(v) for c in flat for v in c) or not all(c[0] > 0 for c in flat):
+        return "coefficients that are not finite, or an a that is not positive"
+    gain = math.prod(c[0] for c in flat)
+    if gain > _abi.ORTHO_MAX_GAIN:
+        return (f"{len(flat)} steps whose a multiply to {gain:.5g}, at most {_abi.ORTHO_MAX_GAIN}: "
+                "they scale the rounding up (take fewer)")
+    return ("coefficients that can take a singular value past 1.99, or 1 + (b A + c A A) / a or "
+            "the product of those past 3.99")
+
+
 def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
     """Newton-Schulz directions of weight gradients (moonep_orthogonalize): g
     [n,rows,cols] or [rows,cols], float32 (such as grad_home [E,H,Hp]) or
@@ -544,7 +566,13 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
         _dev_ptr(ws, torch.uint8, ws.shape, "ws")
         _same_device(dev, ws=ws)
         _apart("ws", ws, g=g)
-    _launch(dev, "moonep_orthogonalize", *args, out.data_ptr(), ws.data_ptr(), ws.numel())
+    try:
+        _launch(dev, "moonep_orthogonalize", *args, out.data_ptr(), ws.data_ptr(), ws.numel())
+    except MoonepError as e:
+        why = _refused_steps(flat, eps) if e.status == _abi.MOONEP_ERR_ARG else None
+        if why is None:
+            raise
+        raise MoonepError(e.status, f"moonep_orthogonalize: {why}") from None
     return out
 
 

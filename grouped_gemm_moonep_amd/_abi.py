@@ -134,6 +134,7 @@ def plan_len(cfg: MoonepConfig, which: int) -> int:
  GRID_COMBINE_BWD) = range(6)
 F32, BF16 = range(2)
 SCORES = {"softmax": 0, "sigmoid": 1}
+ORTHO_MAX_STEPS, ORTHO_MAX_GAIN = 16, 2048
 ORTHO_PRODUCTS = ORTHO_FIRST, ORTHO_R, ORTHO_TP, ORTHO_A, ORTHO_LAST = tuple(range(5))
 TILE_64, TILE_128_DEEP, TILE_128, TILE_128X256, TILE_256 = range(5)
 
