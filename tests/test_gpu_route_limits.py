@@ -191,3 +191,34 @@ def test_scores_equal_in_64_bits_go_by_expert(score):
     buf.destroy()
     want = [5, 11, 30, 20] if score == "sigmoid" else [20, 5, 11, 30]
     assert ids[0, 0].tolist() == want
+
+
+@pytest.mark.parametrize("E,K", [(16, 4), (64, 8), (256, 8), (384, 8), (300, 12), (1024, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_softmax_without_scores_goes_by_its_logits(E, K, dtype):
+    """Rows with a NaN or +inf beside ordinary ones: NaN logits and biases first, then +inf,
+    then the other logits, whatever their biases."""
+    S = 8
+    g = gen(E)
+    x = torch.randn((1, S, E), generator=g, device="cuda").to(dtype)
+    bias = torch.randn((E,), generator=g, device="cuda")
+    odd = torch.randperm(E, generator=g, device="cuda")[:6].tolist()
+    bias[odd[0]] = float("nan")
+    bias[odd[1]] = -float("inf")
+    x[0, 1::2, odd[2]] = float("inf")
+    x[0, 2::4, odd[3]] = float("nan")
+    x[0, 1::2, odd[4]] = -float("inf")
+    x64 = x.double().cpu().numpy()
+    b64 = bias.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        key = T.scores(x64, "softmax") + b64
+    rows = ~np.isfinite(np.where(np.isneginf(x64), 0, x64)).all(-1)
+    key[rows] = x64[rows]
+    key = np.where(np.isposinf(key), 1e300, key)
+    key = np.where(np.isnan(key) | np.isnan(b64), np.inf, key)
+    key[np.isneginf(x64)] = -np.inf
+    want = np.argsort(-key, axis=-1, kind="stable")[..., :K]
+    buf = Buffer(R=1, S=S, K=K, E=E, H=64, Hp=64)
+    ids, _ = buf.route(x, bias)
+    buf.destroy()
+    assert rows.sum() == 6 and np.array_equal(ids.cpu().numpy(), want)
