@@ -233,12 +233,12 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(CombineArgs a) {
 // butterfly over the lanes), so the result does not depend on the launch.
 // A chunk is read before it is written, so dy may be y itself.
 //
-// 262144 slots of 7168: 1580 us, 5.2 TB/s with the padding rows, the rate of a
-// large copy on the same card.  It does not depend on the chunk (1 to 8 vectors
+// 262144 slots of 7168: 1553 us, 5.3 TB/s with the padding rows, the rate at which
+// copy_rows copies them on the same card.  It does not depend on the chunk (1 to 8 vectors
 // per lane, one item per wave: within 0.7%; 14 in flight 6% slower); plain
 // stores are 3% slower.  Non-temporal loads of y measure the same there, but
 // they pass the last-level cache by: with 32672 slots of 1032 columns (134 MB in
-// all) they take 36 us, plain loads 27 us.
+// y and dy) they take 36 us, plain loads 27 us.
 struct CombineBwdArgs {
   const u32x4* dout;     // [R*S][W/8]
   const u32x4* y;        // [R*NvS][W/8] (unused without drw)

@@ -69,8 +69,8 @@ constexpr int kK = 32;                        // values of K per step (a 64-elem
 // ahead, B two), or, kDeep, 5 slots for each (both four steps ahead), which a
 // launch of few workgroups needs: its operands were just written by other XCDs,
 // a load takes as long as several steps, and no second workgroup fills the gap
-// (five steps on four 1024 x 2048 matrices: 517 us without, 466 us with; one of 2048 x
-// 7168: 1023 and 882 us).
+// (five steps on four 1024 x 2048 matrices: 537 us without, 492 us with; one of 2048 x
+// 7168: 1064 and 927 us).
 template <int MI, int NJ, bool kDeep>
 struct Tile3 {
   static constexpr int kRows = 64 * MI, kCols = 64 * NJ;
@@ -284,7 +284,7 @@ __device__ __forceinline__ void gemm3_loop(const RowTileT<2 * MI>& la, const Row
 // few to slot the rest between, so the step is kept short instead.  A step's
 // fragments are read while the step before is multiplied; hi hi and the two
 // cross terms go to accumulators of their own (with two accumulators, chains of
-// four dependent MFMAs: 283 us in place of 239 us for one of 1024 x 2048), which are
+// four dependent MFMAs: 18% slower for one of 1024 x 2048), which are
 // added to the result every ten steps.
 struct Frag1 {
   bf16x8 a[4], b[4];                                     // columns kk
@@ -882,19 +882,20 @@ OrthoLayout ortho_layout(int n, int rows, int cols) {
 // limit bytes are time.  They are taken from one per CU on, where they cover at most 1/8 more
 // than 128-wide ones do (diagonal tiles and the last row and column).  Up to 192 of them that
 // would start another round are done in quarters.  Five steps, without and with quarters, and in
-// 128-wide tiles: 32 of 1024 x 2048 (320 tiles) 3.41, 2.95, 3.15 ms; 8 of 2048 x 4096 (288)
-// 5.77, 4.80, 5.22 ms; 16 of them (576) 10.06, 9.45, 10.2 ms.  Where they cover more: 40 of 896 x
-// 1000 2.78 and 2.44 ms, 16 of 1400 x 1500 3.5 and 3.34 ms, 200 of 509 x 600 3.23 and 2.99 ms.
+// 128-wide tiles: 32 of 1024 x 2048 (320 tiles) 3.19, 2.93, 3.08 ms; 8 of 2048 x 4096 (288)
+// 5.43, 4.73, 5.04 ms; 16 of them (576) 9.72, 9.52, 9.77 ms.  Where they cover more, with them and
+// by the rule: 40 of 896 x 1000 2.59 and 2.37 ms, 16 of 1400 x 1500 3.37 and 3.25 ms, 200 of 509 x
+// 600 3.16 and 2.94 ms.
 //
 // 128-wide ones: from one per CU on two of their workgroups share a CU and hide each other's
 // prologue and epilogue.
 //
 // 64-wide ones where the 128-wide ones would leave half the CUs idle (a step of theirs takes a
 // third of the time), where up to two per CU of them would be a quarter or more empty, and where a
-// matrix is one of either.  One of 1024 x 2048 (36 tiles of 128): 239 us against 360 us; five of
-// 509 x 1283 (50): 196 and 280 us; one of 290 x 700 (6): 108 and 198 us; 24 of 290 x 700 (144, 5/8
-// of them filled) 232 and 282 us; 1000 of 50 x 100 400 and 470 us; but four of 1024 x 2048 (144)
-// 545 and 510 us.
+// matrix is one of either.  One of 1024 x 2048 (36 tiles of 128): 227 us against 380 us; five of
+// 509 x 1283 (50): 183 and 291 us; one of 290 x 700 (6): 112 and 199 us; 24 of 290 x 700 (144, 5/8
+// of them filled) 218 and 280 us; 1000 of 50 x 100 401 and 476 us; but four of 1024 x 2048 (144)
+// 532 and 492 us.
 //
 // The last product has 256-wide tiles from half a round on: it is dense, and its
 // epilogue is short (1 to 3% at 128 .. 512 tiles).

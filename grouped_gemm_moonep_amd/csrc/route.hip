@@ -29,7 +29,10 @@
 // best; the K largest of the row are drawn from the heads of its lanes' lists by
 // a DPP maximum.  (One row per wave, 32-bit keys with the expert beside them and a
 // ballot for the lane: 21.6 us for 32768 rows of 256 fp32 logits, K = 8, and 89 us
-// for 65536 rows of 384 bf16 logits with a bias; this form 9.6 us and 33 us.)
+// for 65536 rows of 384 bf16 logits with a bias; this form 9.4 us and 33 us under the
+// profiler, 9.0 us and 29.6 us a call without it.)  Rows in which two of the first scores with a
+// bias are equal or nearly so cost the exact ranking: the second case takes 144 us with a bias
+// of zero, where bf16 logits often tie.
 #include "internal.h"
 
 namespace moonep {
