@@ -26,8 +26,9 @@
 // (2^-12) operands would leave nothing there, so every matrix is held as a
 // pair of fp16, v = hi + lo (22 bits), and a product is hi hi + hi lo + lo hi
 // on the matrix units, summed in fp32.  Before its rounding to bf16 (1.7e-3 of its norm) the
-// result is then off by 1e-5 of its norm at full rank, at rank one by 3e-4 .. 2.4e-3 for m up to
-// 2048 (the more the fewer rows hold its norm).
+// result is then off by 1e-5 of its norm at full rank, at rank one and m up to 2048 by 3e-4 (all
+// rows share its norm) to 1e-3 (two rows hold it; 4.4e-3 the worst of 40000), half of which the
+// 22 bits leave even if all sums were exact.
 // Values are scaled by 2^14, so entries up to 4 are held, and down to 2^-28
 // with 11 or more bits.
 //

@@ -378,9 +378,10 @@ moonep_status_t moonep_reduce_grad(moonep_handle_t h,
  * (a, b, c), read before the call returns.  The products are taken on values
  * held to 22 bits and summed in fp32; with the usual five steps the rounding
  * left in X is 10^-5 of its norm at full rank; at rank one, with 2048 or fewer
- * on the shorter side, 3 10^-4 where all rows share the norm and up to 3 10^-3
- * where a few hold most of it, which grows with the shorter side (4.4 10^-3 at
- * 16384).  Rounding X to bf16 leaves 2 10^-3.  The a_i scale that rounding up,
+ * on the shorter side, 3 10^-4 where all rows share the norm, and where two of
+ * them hold it 10^-3 as the root mean square of many matrices and 5 10^-3 at
+ * worst.  It grows with the shorter side (4.4 10^-3 at 16384).  Rounding X to
+ * bf16 leaves 2 10^-3.  The a_i scale that rounding up,
  * so their product may be at most MOONEP_ORTHO_MAX_GAIN; each a_i > 0, b_i and
  * c_i finite, 1 <= steps <= MOONEP_ORTHO_MAX_STEPS, eps > 0.  Coefficients whose
  * steps can take X's singular values past 1.99, or 1 + (b A + c A A) / a or the
