@@ -540,7 +540,8 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
     """Newton-Schulz directions of weight gradients (moonep_orthogonalize): g
     [n,rows,cols] or [rows,cols], float32 (such as grad_home [E,H,Hp]) or
     bfloat16, each matrix on its own, to bfloat16 of the same shape.  coeffs:
-    one (a, b, c) for every step, or a sequence of `steps` of them.  ws: a
+    one (a, b, c) for every step, or a sequence of `steps` of them; the a may
+    multiply to 2048 (six of the default), for they scale rounding up.  ws: a
     workspace of orthogonalize_workspace(n, rows, cols); without one it is
     allocated per call."""
     if g.dim() not in (2, 3):
