@@ -39,7 +39,8 @@ from . import _abi
 from ._abi import MoonepError, lib  # noqa: F401
 
 __all__ = ["Buffer", "Plan", "SymmetricBuffer", "MoonepError", "lib", "vmm_granularity",
-           "orthogonalize", "orthogonalize_workspace"]
+           "orthogonalize", "orthogonalize_workspace", "block_norm", "block_norm_bwd",
+           "block_norm_bwd_workspace"]
 
 
 def _stream():
@@ -575,6 +576,153 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
             raise
         raise MoonepError(e.status, f"moonep_orthogonalize: {why}") from None
     return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _gate(gate, shape):
+    """(kind, the gate as the library takes it) of a gate that broadcasts over `shape`."""
+    if gate is None:
+        return _abi.GATE_NONE
+    W = shape[-1]
+    if gate.dtype == torch.bfloat16:
+        _dev_ptr(gate, torch.bfloat16, shape, "gate")
+        return _abi.GATE_FULL
+    if gate.shape == (W,):
+        _dev_ptr(gate, torch.float32, (W,), "gate")
+        return _abi.GATE_CHANNEL
+    if gate.dtype == torch.float32 and gate.shape != (*shape[:-1], 1):
+        raise ValueError(f"gate: expected shape {(W,)} or {(*shape[:-1], 1)} in float32 or "
+                         f"{tuple(shape)} in bfloat16, got {tuple(gate.shape)}")
+    _dev_ptr(gate, torch.float32, (*shape[:-1], 1), "gate")
+    return _abi.GATE_TOKEN
+
+
+def _norm_inputs(h, y, y2, gate, w_post, w_pre):
+    """What block_norm and its backward check alike: (shape, T, W, gate kind)."""
+    shape = h.shape
+    if len(shape) == 0:
+        raise ValueError("h: expected [...,W], got a scalar")
+    W = shape[-1]
+    _dev_ptr(h, h.dtype, shape, "h")
+    _dev_ptr(y, torch.bfloat16, shape, "y", True)
+    _dev_ptr(y2, torch.bfloat16, shape, "y2", True)
+    _dev_ptr(w_post, torch.float32, (W,), "w_post", True)
+    _dev_ptr(w_pre, torch.float32, (W,), "w_pre", True)
+    kind = _gate(gate, shape)
+    if y is None:
+        for name, t in (("y2", y2), ("gate", gate), ("w_post", w_post)):
+            if t is not None:
+                raise ValueError(f"{name} given, but y is None")
+        if w_pre is None:
+            raise ValueError("one of y and w_pre is needed")
+    _same_device(h.device, y=y, y2=y2, gate=gate, w_post=w_post, w_pre=w_pre)
+    return shape, (math.prod(shape[:-1])), W, kind
+
+
+def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0, eps=1e-6,
+               h_out=None, u=None):
+    """A block's end and the next one's start in one pass (moonep_block_norm):
+
+        h_out = h + scale * gate * norm(y + y2) * w_post
+        u     = norm(h_out) * w_pre,   norm(v) = v / sqrt(mean(v^2) + eps)
+
+    h [...,W] float32 or bfloat16 (the residual stream); y, y2 [...,W] bfloat16
+    (the block's outputs: combine's, shared_ffn's); w_post, w_pre [W] float32,
+    either may be None (no norm there); gate None, [W] or [...,1] float32, or
+    [...,W] bfloat16.  Returns (h_out in the stream's type, u in bfloat16 or
+    None).  Without y the stream is only normalised and h_out is h.  h_out may
+    be h (in place), u may be y or y2."""
+    shape, T, W, kind = _norm_inputs(h, y, y2, gate, w_post, w_pre)
+    dev, dt = h.device, _float_type(h, "h")
+    if y is None:
+        if h_out is not None and h_out is not h:
+            raise ValueError("h_out given, but y is None: the stream stays as it is")
+        h_out = h
+    elif h_out is None:
+        h_out = torch.empty_like(h)
+    elif h_out is not h:
+        p = _dev_ptr(h_out, h.dtype, shape, "h_out")
+        _same_device(dev, h_out=h_out)
+        _apart("h_out", h_out, h=None if p == h.data_ptr() else h, y=y, y2=y2, gate=gate,
+               w_post=w_post, w_pre=w_pre)
+    if w_pre is None:
+        if u is not None:
+            raise ValueError("u given, but w_pre is None")
+    elif u is None:
+        u = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        p = _dev_ptr(u, torch.bfloat16, shape, "u")
+        _same_device(dev, u=u)
+        _apart("u", u, h=h, h_out=h_out, gate=gate, w_post=w_post, w_pre=w_pre,
+               y=None if p == _ptr(y) else y, y2=None if p == _ptr(y2) else y2)
+    _launch(dev, "moonep_block_norm", h.data_ptr(), dt, _ptr(y), _ptr(y2), _ptr(gate), kind,
+            _ptr(w_post), _ptr(w_pre), scale, eps, T, W, None if y is None else h_out.data_ptr(),
+            _ptr(u))
+    return h_out, u
+
+
+def block_norm_bwd_workspace(T, W, device="cuda"):
+    """Workspace tensor of `block_norm_bwd` for T rows of W elements."""
+    nbytes = int(lib().moonep_block_norm_bwd_ws(T, W))
+    if nbytes < 0:
+        raise MoonepError(_abi.MOONEP_ERR_CONFIG, "moonep_block_norm_bwd_ws")
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0,
+                   eps=1e-6, need_dw=True, dres=None, dy=None, ws=None):
+    """Gradients of block_norm (moonep_block_norm_bwd): h is the stream behind
+    the block (block_norm's h_out), dh its gradient from later blocks in the
+    stream's type (or None), du that of u in bfloat16 (with w_pre); the other
+    arguments as in the forward.  Returns (dres, dy, dgate, dw_post, dw_pre):
+    dres for the stream before the block (its type), dy for y and for y2 alike
+    (bfloat16), dgate in the gate's shape and type, the weights' in float32; None
+    where there is no such input.  need_dw=False leaves dgate, dw_post and dw_pre
+    out.  dres may be dh, dy may be y, y2 or du.  ws: a workspace of
+    block_norm_bwd_workspace(T, W); without one it is allocated per call."""
+    shape, T, W, kind = _norm_inputs(h, y, y2, gate, w_post, w_pre)
+    dev, dt = h.device, _float_type(h, "h")
+    if dh is None and du is None:
+        raise ValueError("one of dh and du is needed")
+    if (du is None) != (w_pre is None):
+        raise ValueError("du and w_pre go together")
+    _dev_ptr(dh, h.dtype, shape, "dh", True)
+    _dev_ptr(du, torch.bfloat16, shape, "du", True)
+    _same_device(dev, dh=dh, du=du)
+    if dres is None:
+        dres = torch.empty_like(h)
+    else:
+        p = _dev_ptr(dres, h.dtype, shape, "dres")
+        _same_device(dev, dres=dres)
+        _apart("dres", dres, dh=None if p == _ptr(dh) else dh, h=h, du=du, y=y, y2=y2, gate=gate,
+               w_post=w_post, w_pre=w_pre, ws=ws)
+    if y is None:
+        if dy is not None:
+            raise ValueError("dy given, but y is None")
+    elif dy is None:
+        dy = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        p = _dev_ptr(dy, torch.bfloat16, shape, "dy")
+        _same_device(dev, dy=dy)
+        _apart("dy", dy, h=h, dh=dh, dres=dres, gate=gate, w_post=w_post, w_pre=w_pre, ws=ws,
+               **{n: None if p == _ptr(t) else t for n, t in (("du", du), ("y", y), ("y2", y2))})
+    new = lambda t: torch.empty_like(t) if need_dw and t is not None else None
+    dgate, dw_post, dw_pre = new(gate), new(w_post), new(w_pre)
+    if ws is not None:
+        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
+        _same_device(dev, ws=ws)
+        _apart("ws", ws, h=h, dh=dh, du=du, y=y, y2=y2, gate=gate, w_post=w_post, w_pre=w_pre)
+    elif dw_post is not None or dw_pre is not None or (dgate is not None and
+                                                       kind == _abi.GATE_CHANNEL):
+        ws = block_norm_bwd_workspace(T, W, device=dev)
+    _launch(dev, "moonep_block_norm_bwd", h.data_ptr(), dt, _ptr(dh), _ptr(du), _ptr(y), _ptr(y2),
+            _ptr(gate), kind, _ptr(w_post), _ptr(w_pre), scale, eps, T, W, dres.data_ptr(),
+            _ptr(dy), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
+            0 if ws is None else ws.numel())
+    return dres, dy, dgate, dw_post, dw_pre
 
 
 class SymmetricBuffer:

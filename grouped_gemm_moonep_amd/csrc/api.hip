@@ -1,6 +1,7 @@
 // Host side of the C ABI: configuration checks, handle scratch, argument
 // validation, and the launches.  Nothing here runs on the CPU instead of the
 // GPU: every step of the path is a kernel.
+#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -337,6 +338,77 @@ moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, in
   if (ws_bytes < ortho_ws_bytes(n, rows, cols)) return MOONEP_ERR_SCRATCH;
   return hip_status(launch_orthogonalize(g, dtype, n, rows, cols, coeffs, steps, eps, out, ws,
                                          stream));
+}
+
+// What the forward and the backward of a block's norms take alike.
+// (arrays of no rows may be NULL).
+static bool norm_form_ok(int64_t T, int32_t dtype, const void* y, const void* y2, const void* gate,
+                         int32_t gate_kind, const void* w_post, const void* w_pre, float scale,
+                         float eps) {
+  if (dtype != MOONEP_F32 && dtype != MOONEP_BF16) return false;
+  if (gate_kind < MOONEP_GATE_NONE || gate_kind > MOONEP_GATE_FULL) return false;
+  if (!(eps > 0.0f && eps < INFINITY) || scale != scale) return false;
+  if (T == 0) return true;
+  if ((gate == nullptr) != (gate_kind == MOONEP_GATE_NONE)) return false;
+  if (!y && (y2 || gate || w_post)) return false;
+  return y || w_pre;
+}
+
+static bool all_aligned(const void* const* p, int n, size_t a) {
+  for (int i = 0; i < n; ++i)
+    if (!aligned(p[i], a)) return false;
+  return true;
+}
+
+moonep_status_t moonep_block_norm(const void* h, int32_t dtype, const uint16_t* y,
+                                  const uint16_t* y2, const void* gate, int32_t gate_kind,
+                                  const float* w_post, const float* w_pre, float scale, float eps,
+                                  int64_t T, int32_t W, void* h_out, uint16_t* u,
+                                  hipStream_t stream) {
+  if (!norm_shape_ok(T, W)) return MOONEP_ERR_CONFIG;
+  if (!norm_form_ok(T, dtype, y, y2, gate, gate_kind, w_post, w_pre, scale, eps))
+    return MOONEP_ERR_ARG;
+  if (T == 0) return MOONEP_OK;
+  if (!h || (y == nullptr) != (h_out == nullptr) || (w_pre == nullptr) != (u == nullptr))
+    return MOONEP_ERR_ARG;
+  const void* p[] = {h, y, y2, gate, w_post, w_pre, h_out, u};
+  if (gate_kind == MOONEP_GATE_TOKEN) p[3] = nullptr;      // read a number at a time
+  if (!all_aligned(p, 8, 16) || !aligned(gate, 4)) return MOONEP_ERR_ARG;
+  if ((const void*)u == h || (u && (const void*)u == h_out)) return MOONEP_ERR_ARG;
+  const NormArgs a = {h, y, y2, gate, w_post, w_pre, gate_kind, scale, eps, T, W, h_out, u};
+  return hip_status(launch_norm(a, dtype, stream));
+}
+
+int64_t moonep_block_norm_bwd_ws(int64_t T, int32_t W) {
+  return norm_shape_ok(T, W) ? norm_ws_bytes(T, W) : -1;
+}
+
+moonep_status_t moonep_block_norm_bwd(const void* h, int32_t dtype, const void* dh,
+                                      const uint16_t* du, const uint16_t* y, const uint16_t* y2,
+                                      const void* gate, int32_t gate_kind, const float* w_post,
+                                      const float* w_pre, float scale, float eps, int64_t T,
+                                      int32_t W, void* dres, uint16_t* dy, void* dgate,
+                                      float* dw_post, float* dw_pre, void* ws, int64_t ws_bytes,
+                                      hipStream_t stream) {
+  if (!norm_shape_ok(T, W)) return MOONEP_ERR_CONFIG;
+  if (!norm_form_ok(T, dtype, y, y2, gate, gate_kind, w_post, w_pre, scale, eps))
+    return MOONEP_ERR_ARG;
+  if ((dgate && gate_kind == MOONEP_GATE_NONE) || (dw_post && !w_post) || (dw_pre && !w_pre))
+    return MOONEP_ERR_ARG;
+  if (T > 0 && dy && !y) return MOONEP_ERR_ARG;
+  if (T > 0 && (!dres || (du == nullptr) != (w_pre == nullptr) || (w_pre && !h) || (!dh && !du)))
+    return MOONEP_ERR_ARG;
+  const void* p[] = {h, dh, du, y, y2, gate, w_post, w_pre, dres, dy, dgate, dw_post, dw_pre, ws};
+  if (gate_kind == MOONEP_GATE_TOKEN) p[5] = p[10] = nullptr;
+  if (!all_aligned(p, 14, 16) || !aligned(gate, 4) || !aligned(dgate, 4)) return MOONEP_ERR_ARG;
+  if (dres && (dres == dy || dres == du || dres == y || dres == h)) return MOONEP_ERR_ARG;
+  const bool sums = dw_post || dw_pre || (dgate && gate_kind == MOONEP_GATE_CHANNEL);
+  if (sums && T > 0 && !ws) return MOONEP_ERR_ARG;
+  if (sums && ws_bytes < norm_ws_bytes(T, W)) return MOONEP_ERR_SCRATCH;
+  const NormBwdArgs a = {h, dh, du, y, y2, gate, w_post, w_pre, gate_kind, scale, eps, T, W,
+                         norm_shares(T, W), dres, dy, dgate, dw_post, dw_pre,
+                         sums ? (float*)ws : nullptr};
+  return hip_status(launch_norm_bwd(a, dtype, stream));
 }
 
 moonep_status_t moonep_copy_rows(moonep_handle_t h, const moonep_plan_t* plan,

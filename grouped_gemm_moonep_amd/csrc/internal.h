@@ -143,6 +143,47 @@ hipError_t launch_orthogonalize(const void* g, int32_t dtype, int32_t n, int32_t
                                 int32_t cols, const float* coeffs, int32_t steps, float eps,
                                 uint16_t* out, void* ws, hipStream_t s);
 
+// A block's norms, gate and residual scale (norm.hip).
+struct NormArgs {
+  const void* h;             // [T,W] stream
+  const uint16_t* y;         // [T,W] or NULL
+  const uint16_t* y2;        // [T,W] or NULL
+  const void* gate;
+  const float* w_post;       // [W] or NULL
+  const float* w_pre;        // [W] or NULL
+  int32_t gate_kind;
+  float scale, eps;
+  int64_t T;
+  int32_t W;
+  void* h_out;               // [T,W] stream
+  uint16_t* u;               // [T,W]
+};
+struct NormBwdArgs {
+  const void* h;             // [T,W] stream behind the block
+  const void* dh;            // [T,W] stream or NULL
+  const uint16_t* du;        // [T,W], with w_pre
+  const uint16_t* y;
+  const uint16_t* y2;
+  const void* gate;
+  const float* w_post;
+  const float* w_pre;
+  int32_t gate_kind;
+  float scale, eps;
+  int64_t T;
+  int32_t W, shares;
+  void* dres;                // [T,W] stream
+  uint16_t* dy;              // [T,W] or NULL
+  void* dgate;               // as gate, or NULL
+  float* dw_post;            // [W] or NULL
+  float* dw_pre;             // [W] or NULL
+  float* part;               // [3][shares][W]
+};
+bool norm_shape_ok(int64_t T, int32_t W);
+int32_t norm_shares(int64_t T, int32_t W);
+int64_t norm_ws_bytes(int64_t T, int32_t W);
+hipError_t launch_norm(const NormArgs& a, int32_t dtype, hipStream_t s);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int32_t dtype, hipStream_t s);
+
 hipError_t launch_wgrad(const Ctx& c, const moonep_plan_t& p, int rank,
                         const uint16_t* a, const uint16_t* b, float* gh,
                         float* rb, hipStream_t s);

@@ -1,0 +1,445 @@
+// A block's end and the next one's start on gfx950: the block's outputs are
+// summed, normalised, gated, scaled and added to the residual stream, and the
+// stream is normalised for what comes next, in one pass; and its gradients.
+// In a block with experts y is combine's output (MoonEP README, "API guide >
+// combine fwd": output_sh) and y2 the shared expert's.
+//
+//   a  = y (+ y2)
+//   n  = a rstd(a) w_post          rstd(v) = (mean(v^2) + eps)^(-1/2); n = a without w_post
+//   h' = h + scale gate n          gate: one, [W], [T] or [T,W]
+//   u  = h' rstd(h') w_pre
+// and backward, with dh the gradient of h', du that of u, s = rstd(h'), r = rstd(a):
+//   v  = du w_pre,  D = dh + s (v - h' s^2 mean(v h'))     the stream's gradient
+//   dw_pre = sum_t du h' s
+//   dn = scale gate D,  dgate = scale D n  (summed over what the gate is shared by)
+//   v  = dn w_post,  dy = r (v - a r^2 mean(v a)),  dw_post = sum_t dn a r
+//
+// Design for CDNA4: every operand is read once and every result written once,
+// so a row stays in registers between its sums.  A row of up to 1024 elements
+// belongs to a wave, whose sums need no barrier; a longer one to a workgroup
+// of up to 16 waves with two 8-element vectors a lane.
+#include "internal.h"
+
+namespace moonep {
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxWaves = 16;      // per workgroup
+constexpr int kVals = 3;           // sums taken together
+
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
+}
+
+// Eight elements of a row as they lie in memory.
+template <class T> struct Raw;
+template <> struct Raw<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *(const u32x4*)p; }
+  __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ float get(int i) const {
+    const unsigned w = v[i >> 1];
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+};
+template <> struct Raw<float> {
+  f32x4 v[2];
+  __device__ __forceinline__ void load(const float* p) {
+    v[0] = *(const f32x4*)p;
+    v[1] = *(const f32x4*)(p + 4);
+  }
+  __device__ __forceinline__ void zero() { v[0] = v[1] = f32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ float get(int i) const { return v[i >> 2][i & 3]; }
+};
+__device__ __forceinline__ void store8(uint16_t* p, const float f[8]) {
+  *(u32x4*)p = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+}
+__device__ __forceinline__ void store8(float* p, const float f[8]) {
+  *(f32x4*)p = f32x4{f[0], f[1], f[2], f[3]};
+  *(f32x4*)(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+}
+
+// Sum of 16 lanes, the same in each of them.
+__device__ __forceinline__ float sum16(float v) {
+#define MOONEP_STEP(ctrl) \
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xF, 0xF, true))
+  MOONEP_STEP(0xB1);    // quad 1,0,3,2
+  MOONEP_STEP(0x4E);    // quad 2,3,0,1
+  MOONEP_STEP(0x141);   // half-row mirror
+  MOONEP_STEP(0x140);   // row mirror
+#undef MOONEP_STEP
+  return v;
+}
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+// Sums of N values over the lanes of a row: a wave's, or a workgroup's through
+// LDS, where two buffers take turns, so that one barrier a sum is enough (a
+// buffer is written again only behind the barrier of the sum in between).
+template <bool kWave>
+struct RowSum {
+  float (*buf)[kVals][16];
+  int turn;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    static_assert(N <= kVals, "one row of 16 lanes a value");
+    float t[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = sum16(v[i]);
+      t[i] = (lane_of(s, 0) + lane_of(s, 16)) + (lane_of(s, 32) + lane_of(s, 48));
+    }
+    if constexpr (!kWave) {
+      const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+      float (*b)[16] = buf[turn];
+      turn ^= 1;
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) b[i][wave] = t[i];
+      }
+      __syncthreads();
+      const int row = lane >> 4, col = lane & 15;
+      const float s = sum16(row < N && col < (int)(blockDim.x >> 6) ? b[row < N ? row : 0][col] : 0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) t[i] = lane_of(s, 16 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = t[i];
+  }
+};
+
+// The lanes of a row and the rows of a workgroup.
+template <bool kWave>
+struct Place {
+  int lane, lanes;           // of the row
+  int64_t row, step;         // first row and distance to the next
+  __device__ __forceinline__ Place() {
+    if constexpr (kWave) {
+      lane = threadIdx.x & 63;
+      lanes = 64;
+      row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+      step = (int64_t)gridDim.x * 4;
+    } else {
+      lane = threadIdx.x;
+      lanes = blockDim.x;
+      row = blockIdx.x;
+      step = gridDim.x;
+    }
+  }
+};
+
+__device__ __forceinline__ float rstd(float ss, float inv_w, float eps) {
+  return 1.0f / sqrtf(ss * inv_w + eps);
+}
+
+template <class TS, int VPT, bool kWave>
+__global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(NormArgs a) {
+  __shared__ float red[2][kVals][16];
+  RowSum<kWave> sum{red, 0};
+  const Place<kWave> at;
+  const int W = a.W;
+  const float inv_w = 1.0f / (float)W;
+  for (int64_t r = at.row; r < a.T; r += at.step) {
+    const int64_t base = r * W;
+    Raw<TS> hv[VPT];
+    Raw<uint16_t> yv[VPT], y2v[VPT], gv[VPT];
+    const float gt = a.gate_kind == MOONEP_GATE_TOKEN ? ((const float*)a.gate)[r] : 1.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      hv[p].zero();
+      yv[p].zero();
+      y2v[p].zero();
+      gv[p].zero();
+      if (c < W) {
+        hv[p].load((const TS*)a.h + base + c);
+        if (a.y) yv[p].load(a.y + base + c);
+        if (a.y2) y2v[p].load(a.y2 + base + c);
+        if (a.gate_kind == MOONEP_GATE_FULL) gv[p].load((const uint16_t*)a.gate + base + c);
+      }
+    }
+    float h[VPT][8];
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[p][i] = yv[p].get(i) + y2v[p].get(i);
+        ss[0] += h[p][i] * h[p][i];
+      }
+    float ra = 1.0f;
+    if (a.w_post) {
+      sum(ss);
+      ra = rstd(ss[0], inv_w, a.eps);
+    }
+    const float f = a.scale * gt;
+    ss[0] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      if (c < W) {
+        if (a.y) {
+          Raw<float> w, g;
+          if (a.w_post) w.load(a.w_post + c);
+          if (a.gate_kind == MOONEP_GATE_CHANNEL) g.load((const float*)a.gate + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float n = h[p][i];
+            if (a.w_post) n *= ra * w.get(i);
+            if (a.gate_kind == MOONEP_GATE_CHANNEL) n *= g.get(i);
+            if (a.gate_kind == MOONEP_GATE_FULL) n *= gv[p].get(i);
+            h[p][i] = hv[p].get(i) + f * n;
+          }
+          store8((TS*)a.h_out + base + c, h[p]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[p][i] = hv[p].get(i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss[0] += h[p][i] * h[p][i];
+      }
+    }
+    if (a.w_pre) {
+      sum(ss);
+      const float rh = rstd(ss[0], inv_w, a.eps);
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+        const int c = 8 * (at.lane + p * at.lanes);
+        if (c < W) {
+          Raw<float> w;
+          w.load(a.w_pre + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[p][i] *= rh * w.get(i);
+          store8(a.u + base + c, h[p]);
+        }
+      }
+    }
+  }
+}
+
+// Sums over tokens stay in a lane's registers, for its columns, over all rows
+// of its wave or workgroup; each then writes its share to part [3][shares][W]
+// and norm_bwd_sum adds the shares, in an order that the launch fixes.
+template <class TS, int VPT, bool kWave>
+__global__ __launch_bounds__(kWave ? 256 : 1024) void norm_bwd_kernel(NormBwdArgs a) {
+  __shared__ float red[2][kVals][16];
+  RowSum<kWave> sum{red, 0};
+  const Place<kWave> at;
+  const int W = a.W;
+  const float inv_w = 1.0f / (float)W;
+  const bool need_a = a.y && (a.w_post || a.gate_kind != MOONEP_GATE_NONE);
+  float s_pre[VPT][8], s_post[VPT][8], s_gate[VPT][8];
+#pragma unroll
+  for (int p = 0; p < VPT; ++p)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_pre[p][i] = s_post[p][i] = s_gate[p][i] = 0.0f;
+  for (int64_t r = at.row; r < a.T; r += at.step) {
+    const int64_t base = r * W;
+    Raw<TS> hv[VPT], dhv[VPT];
+    Raw<uint16_t> duv[VPT], yv[VPT], y2v[VPT], gv[VPT];
+    const float gt = a.gate_kind == MOONEP_GATE_TOKEN ? ((const float*)a.gate)[r] : 1.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      hv[p].zero();
+      dhv[p].zero();
+      duv[p].zero();
+      yv[p].zero();
+      y2v[p].zero();
+      gv[p].zero();
+      if (c < W) {
+        if (a.w_pre) {
+          hv[p].load((const TS*)a.h + base + c);
+          duv[p].load(a.du + base + c);
+        }
+        if (a.dh) dhv[p].load((const TS*)a.dh + base + c);
+        if (need_a) {
+          yv[p].load(a.y + base + c);
+          if (a.y2) y2v[p].load(a.y2 + base + c);
+        }
+        if (a.gate_kind == MOONEP_GATE_FULL) gv[p].load((const uint16_t*)a.gate + base + c);
+      }
+    }
+    float d[VPT][8], av[VPT][8];
+    float s3[3] = {0.0f, 0.0f, 0.0f};       // h'^2, v h', a^2
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      Raw<float> w;
+      w.zero();
+      if (a.w_pre && c < W) w.load(a.w_pre + c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = hv[p].get(i);
+        av[p][i] = yv[p].get(i) + y2v[p].get(i);
+        d[p][i] = duv[p].get(i) * w.get(i);
+        s3[0] += h * h;
+        s3[1] += d[p][i] * h;
+        s3[2] += av[p][i] * av[p][i];
+      }
+    }
+    if (a.w_pre || a.w_post) sum(s3);
+    const float rh = a.w_pre ? rstd(s3[0], inv_w, a.eps) : 0.0f;
+    const float ra = a.w_post ? rstd(s3[2], inv_w, a.eps) : 1.0f;
+    const float mh = s3[1] * inv_w * rh * rh;
+    float s2[2] = {0.0f, 0.0f};             // D n, w_post dn a
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      if (c < W) {
+        Raw<float> w, g;
+        if (a.w_post) w.load(a.w_post + c);
+        if (a.gate_kind == MOONEP_GATE_CHANNEL) g.load((const float*)a.gate + c);
+        float dg[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float h = hv[p].get(i);
+          s_pre[p][i] += duv[p].get(i) * (h * rh);
+          d[p][i] = dhv[p].get(i) + rh * (d[p][i] - h * mh);
+        }
+        store8((TS*)a.dres + base + c, d[p]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float hat = av[p][i] * ra;
+          const float n = a.w_post ? hat * w.get(i) : hat;
+          const float sd = a.scale * d[p][i];
+          const float t = sd * n;
+          dg[i] = t;
+          s_gate[p][i] += t;
+          s2[0] += t;
+          float dn = sd * gt;
+          if (a.gate_kind == MOONEP_GATE_CHANNEL) dn *= g.get(i);
+          if (a.gate_kind == MOONEP_GATE_FULL) dn *= gv[p].get(i);
+          s_post[p][i] += dn * hat;
+          d[p][i] = a.w_post ? dn * w.get(i) : dn;
+          s2[1] += d[p][i] * av[p][i];
+        }
+        if (a.gate_kind == MOONEP_GATE_FULL && a.dgate) store8((uint16_t*)a.dgate + base + c, dg);
+      }
+    }
+    const bool token = a.gate_kind == MOONEP_GATE_TOKEN && a.dgate;
+    if (token || (a.dy && a.w_post)) sum(s2);
+    if (token && at.lane == 0) ((float*)a.dgate)[r] = s2[0];
+    if (a.dy) {
+      const float ma = a.w_post ? s2[1] * inv_w * ra * ra : 0.0f;
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+        const int c = 8 * (at.lane + p * at.lanes);
+        if (c < W) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[p][i] = ra * (d[p][i] - av[p][i] * ma);
+          store8(a.dy + base + c, d[p]);
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+  const int64_t share = kWave ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t slab = (int64_t)a.shares * W;
+#pragma unroll
+  for (int p = 0; p < VPT; ++p) {
+    const int c = 8 * (at.lane + p * at.lanes);
+    if (c < W) {
+      float* q = a.part + share * W + c;
+      if (a.dw_pre) store8(q, s_pre[p]);
+      if (a.dw_post) store8(q + slab, s_post[p]);
+      if (a.gate_kind == MOONEP_GATE_CHANNEL && a.dgate) store8(q + 2 * slab, s_gate[p]);
+    }
+  }
+}
+
+// out_k [W] = the sum of the shares of part[k]: a workgroup takes 64 columns,
+// each of its 16 waves every 16th share.
+__global__ __launch_bounds__(1024) void norm_bwd_sum(const float* part, int shares, int W,
+                                                     float* dw_pre, float* dw_post, float* dgate) {
+  float* out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
+  if (!out) return;
+  __shared__ float s[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  const float* p = part + (int64_t)blockIdx.y * shares * W + c;
+  float v = 0.0f;
+  if (c < W) {
+#pragma unroll 8
+    for (int i = wave; i < shares; i += 16) v += p[(int64_t)i * W];
+  }
+  s[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && c < W) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += s[i][lane];
+    out[c] = t;
+  }
+}
+
+// Workgroups of a launch and the lanes of each.
+struct NormGrid {
+  int vpt, threads;
+  bool wave;
+  int64_t blocks;
+};
+NormGrid norm_grid(int64_t T, int W, int64_t most) {
+  NormGrid g;
+  const int vecs = W / 8;
+  g.wave = vecs <= 128;
+  g.vpt = vecs <= 64 || (vecs > 128 && vecs <= 1024) ? 1 : 2;
+  g.threads = g.wave ? 256 : (vecs + 64 * g.vpt - 1) / (64 * g.vpt) * 64;
+  const int64_t need = g.wave ? (T + 3) / 4 : T;
+  g.blocks = need < most ? need : most;
+  return g;
+}
+constexpr int64_t kNormBlocks = 4096, kNormBwdBlocks = 512;
+
+}  // namespace
+
+bool norm_shape_ok(int64_t T, int32_t W) {
+  return T >= 0 && T < (int64_t(1) << 31) && W >= 8 && W % 8 == 0 && W <= MOONEP_NORM_MAX_W;
+}
+
+int32_t norm_shares(int64_t T, int32_t W) {
+  return (int32_t)(norm_grid(T, W, kNormBwdBlocks).blocks * (W <= 1024 ? 4 : 1));
+}
+
+int64_t norm_ws_bytes(int64_t T, int32_t W) { return 3LL * norm_shares(T, W) * W * 4; }
+
+template <class TS>
+static hipError_t norm_as(const NormArgs& a, hipStream_t s) {
+  const NormGrid g = norm_grid(a.T, a.W, kNormBlocks);
+  if (g.wave && g.vpt == 1) norm_kernel<TS, 1, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.wave) norm_kernel<TS, 2, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.vpt == 1) norm_kernel<TS, 1, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else norm_kernel<TS, 2, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm(const NormArgs& a, int32_t dtype, hipStream_t s) {
+  return dtype == MOONEP_F32 ? norm_as<float>(a, s) : norm_as<uint16_t>(a, s);
+}
+
+template <class TS>
+static hipError_t norm_bwd_as(const NormBwdArgs& a, hipStream_t s) {
+  const NormGrid g = norm_grid(a.T, a.W, kNormBwdBlocks);
+  if (g.blocks == 0) {}                              // no tokens: the sums below are zeros
+  else if (g.wave && g.vpt == 1) norm_bwd_kernel<TS, 1, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.wave) norm_bwd_kernel<TS, 2, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.vpt == 1) norm_bwd_kernel<TS, 1, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else norm_bwd_kernel<TS, 2, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  float* dgate = a.gate_kind == MOONEP_GATE_CHANNEL ? (float*)a.dgate : nullptr;
+  if (a.dw_pre || a.dw_post || dgate) {
+    norm_bwd_sum<<<dim3((unsigned)((a.W + 63) / 64), 3), 1024, 0, s>>>(a.part, a.shares, a.W,
+                                                                      a.dw_pre, a.dw_post, dgate);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int32_t dtype, hipStream_t s) {
+  return dtype == MOONEP_F32 ? norm_bwd_as<float>(a, s) : norm_bwd_as<uint16_t>(a, s);
+}
+
+}  // namespace moonep

@@ -419,6 +419,62 @@ moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, in
                                      uint16_t* out, void* ws, int64_t ws_bytes,
                                      hipStream_t stream);
 
+/* A block's end and the next one's start in one pass (the framework-side steps
+ * between combine and the next block): for T rows of W elements, with
+ * rstd(v) = 1 / sqrt(mean(v^2) + eps),
+ *   a  = y + y2                        (y alone if y2 is NULL)
+ *   n  = a rstd(a) w_post              (a if w_post is NULL)
+ *   h' = h + scale gate n         -> h_out [T,W] in the stream's type
+ *   u  = h' rstd(h') w_pre        -> u [T,W] bf16, if w_pre is given
+ * h [T,W]: the residual stream (dtype: MOONEP_F32 or MOONEP_BF16); y, y2 [T,W]
+ * bf16: the block's output, such as moonep_combine's out, and a second one, such
+ * as moonep_shared_ffn's; w_post, w_pre [W] fp32; gate by gate_kind: NULL, [W]
+ * fp32 (CHANNEL), [T] fp32 (TOKEN) or [T,W] bf16 (FULL).  Everything is held in
+ * fp32 between reading and writing: u is of h' before it is rounded.  y may be
+ * NULL (then y2, w_post and gate too, and h_out is not written: u is the norm of
+ * h).  One of y and w_pre is needed; h_out is NULL without y, u without w_pre.
+ * h_out may be h, and u may be y or y2; no other aliasing.  Row arrays and weights are 16-byte
+ * aligned.  0 <= T < 2^31, W a multiple of 8 up to MOONEP_NORM_MAX_W, eps > 0
+ * (MOONEP_ERR_CONFIG for the sizes, MOONEP_ERR_ARG for the rest).  The mean of
+ * squares is taken in fp32: a row whose squares pass 3.4e38 is not normalised
+ * (it gives zeros), and NaN and infinities stay within their row.  The current
+ * device is used; no handle is needed. */
+#define MOONEP_NORM_MAX_W 16384
+enum { MOONEP_GATE_NONE = 0, MOONEP_GATE_CHANNEL, MOONEP_GATE_TOKEN, MOONEP_GATE_FULL };
+moonep_status_t moonep_block_norm(const void* h, int32_t dtype, const uint16_t* y,
+                                  const uint16_t* y2, const void* gate, int32_t gate_kind,
+                                  const float* w_post, const float* w_pre, float scale, float eps,
+                                  int64_t T, int32_t W, void* h_out, uint16_t* u,
+                                  hipStream_t stream);
+
+/* Gradients of moonep_block_norm.  h [T,W] is the stream behind the block (the
+ * forward's h_out; its h where y was NULL), read with w_pre only; dh [T,W] (the
+ * stream's type) is the gradient of h_out or NULL (zero), du [T,W] bf16 that of
+ * u, given iff w_pre is; y, y2, gate, w_post, w_pre, scale and eps as in the
+ * forward.  With s = rstd(h), r = rstd(a), mean over a row:
+ *   v = du w_pre, D = dh + s (v - h s^2 mean(v h))  -> dres [T,W], the stream's type
+ *   dw_pre = sum_t du h s                           -> [W] fp32
+ *   dn = scale gate D, dgate = scale D n, summed over what a gate is shared by,
+ *                                                   -> dgate, shape and type of gate
+ *   v = dn w_post, da = r (v - a r^2 mean(v a))     -> dy [T,W] bf16, of y and of y2 alike
+ *                                   (dn if w_post is NULL)
+ *   dw_post = sum_t dn a r                          -> [W] fp32
+ * dres is needed; dy, dgate, dw_post and dw_pre may each be NULL.  Sums over
+ * tokens are taken in fp32 in an order that T and W fix.  dres may be dh, dy may
+ * be y, y2 or du; no other aliasing.  ws: workspace of at least
+ * moonep_block_norm_bwd_ws bytes, 16-byte aligned, for the sums over tokens
+ * (MOONEP_ERR_SCRATCH if it is too small; NULL if dw_pre, dw_post and a CHANNEL
+ * gate's dgate are not asked for); calls that overlap need one each.  Limits and
+ * alignment as in the forward. */
+int64_t moonep_block_norm_bwd_ws(int64_t T, int32_t W);   /* host only; -1 for bad sizes */
+moonep_status_t moonep_block_norm_bwd(const void* h, int32_t dtype, const void* dh,
+                                      const uint16_t* du, const uint16_t* y, const uint16_t* y2,
+                                      const void* gate, int32_t gate_kind, const float* w_post,
+                                      const float* w_pre, float scale, float eps, int64_t T,
+                                      int32_t W, void* dres, uint16_t* dy, void* dgate,
+                                      float* dw_post, float* dw_pre, void* ws, int64_t ws_bytes,
+                                      hipStream_t stream);
+
 /* ---- Symmetric [E+B,H,Hp] buffers on virtual memory ----
  *
  * The README's contract ("Usage > Integration > Weight buffer", "Gradient
