@@ -40,7 +40,8 @@ from ._abi import MoonepError, lib  # noqa: F401
 
 __all__ = ["Buffer", "Plan", "SymmetricBuffer", "MoonepError", "lib", "vmm_granularity",
            "orthogonalize", "orthogonalize_workspace", "block_norm", "block_norm_bwd",
-           "block_norm_bwd_workspace"]
+           "block_norm_bwd_workspace", "shared_ffn", "shared_ffn_bwd", "shared_ffn_workspace",
+           "shared_ffn_bwd_workspace"]
 
 
 def _stream():
@@ -578,6 +579,113 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
     return out
 
 
+def _ffn_inputs(x, weights, act):
+    """What shared_ffn and its backward check alike: (T, H, Hp, activation, weights' pointers)."""
+    if act not in _abi.ACTS:
+        raise ValueError(f"act: expected one of {sorted(_abi.ACTS)}, got {act!r}")
+    if len(weights) != 3 or any(w.dim() != 2 for w in weights):
+        raise ValueError("three projections (gate, up, down) [H,Hp] expected")
+    if x.dim() == 0:
+        raise ValueError("x: expected [...,H], got a scalar")
+    H, Hp = weights[0].shape
+    _dev_ptr(x, torch.bfloat16, (*x.shape[:-1], H), "x")
+    for name, w in zip(("gate", "up", "down"), weights):
+        _dev_ptr(w, torch.bfloat16, (H, Hp), name)
+        if w.device != x.device:
+            _same_device(x.device, **{name: w})
+    return math.prod(x.shape[:-1]), H, Hp, _abi.ACTS[act], _abi.ptr3(weights)
+
+
+def _workspace(name, nbytes, device):
+    if nbytes < 0:
+        raise MoonepError(_abi.MOONEP_ERR_CONFIG, name)
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def shared_ffn_workspace(T, H, Hp, device="cuda"):
+    """Workspace tensor of `shared_ffn` for T tokens."""
+    return _workspace("moonep_shared_ffn_ws", lib().moonep_shared_ffn_ws(T, H, Hp), device)
+
+
+def shared_ffn_bwd_workspace(T, H, Hp, device="cuda"):
+    """Workspace tensor of `shared_ffn_bwd` for T tokens."""
+    return _workspace("moonep_shared_ffn_bwd_ws", lib().moonep_shared_ffn_bwd_ws(T, H, Hp), device)
+
+
+def shared_ffn(x, weights, act="silu", add=None, out=None, ws=None):
+    """The shared expert (moonep_shared_ffn): (f(x Wg) * (x Wu)) Wd^T (+ add) for
+    x [...,H] bfloat16 and weights = (gate, up, down), each [H,Hp] bfloat16 as the
+    experts' are.  act: "silu" or "gelu_tanh"; add [...,H] bfloat16, such as
+    combine's output, is added before the only rounding.  out may be add.  ws: a
+    workspace of shared_ffn_workspace(T, H, Hp); without one it is allocated per
+    call."""
+    T, H, Hp, kind, w = _ffn_inputs(x, weights, act)
+    dev = x.device
+    p_add = _dev_ptr(add, torch.bfloat16, x.shape, "add", True)
+    if add is not None:
+        _same_device(dev, add=add)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        p = _dev_ptr(out, torch.bfloat16, x.shape, "out")
+        _same_device(dev, out=out)
+        _apart("out", out, x=x, gate=weights[0], up=weights[1], down=weights[2], ws=ws,
+               add=None if p == p_add else add)
+    if ws is None:
+        ws = shared_ffn_workspace(T, H, Hp, device=dev)
+    else:
+        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
+        _same_device(dev, ws=ws)
+        _apart("ws", ws, x=x, gate=weights[0], up=weights[1], down=weights[2], add=add)
+    _launch(dev, "moonep_shared_ffn", x.data_ptr(), w, kind, p_add, T, H, Hp, out.data_ptr(),
+            ws.data_ptr(), ws.numel())
+    return out
+
+
+def shared_ffn_bwd(x, dy, weights, act="silu", need_dx=True, need_dw=True, dx=None, dw=None,
+                   ws=None):
+    """Gradients of shared_ffn (moonep_shared_ffn_bwd): (dx, (dgate, dup, ddown))
+    from dy [...,H] bfloat16 (which is add's gradient too).  dw: three tensors
+    [H,Hp], all bfloat16 (written) or all float32 (added to, like expert_wgrad's
+    grad_home); without it they are bfloat16 and new.  need_dx / need_dw = False
+    leave one out (None).  ws: a workspace of shared_ffn_bwd_workspace(T, H, Hp);
+    without one it is allocated per call."""
+    T, H, Hp, kind, w = _ffn_inputs(x, weights, act)
+    dev = x.device
+    inputs = dict(x=x, dy=dy, gate=weights[0], up=weights[1], down=weights[2])
+    _dev_ptr(dy, torch.bfloat16, x.shape, "dy")
+    _same_device(dev, dy=dy)
+    if (dx is not None and not need_dx) or (dw is not None and not need_dw):
+        raise ValueError("dx or dw given, but need_dx or need_dw is False")
+    if dx is not None:
+        _dev_ptr(dx, torch.bfloat16, x.shape, "dx")
+        _same_device(dev, dx=dx)
+        _apart("dx", dx, ws=ws, **inputs)
+    elif need_dx:
+        dx = torch.empty_like(x)
+    code = _abi.BF16
+    if dw is not None:
+        if len(dw) != 3:
+            raise ValueError("three gradients (gate, up, down) expected")
+        code = _float_type(dw[0], "dw[0]")
+        for i, t in enumerate(dw):
+            _dev_ptr(t, dw[0].dtype, (H, Hp), f"dw[{i}]")
+            _same_device(dev, **{f"dw[{i}]": t})
+            _apart(f"dw[{i}]", t, ws=ws, dx=dx, **inputs,
+                   **{f"dw[{j}]": dw[j] for j in range(i)})
+    elif need_dw:
+        dw = tuple(torch.empty_like(t) for t in weights)
+    if ws is None:
+        ws = shared_ffn_bwd_workspace(T, H, Hp, device=dev)
+    else:
+        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
+        _same_device(dev, ws=ws)
+        _apart("ws", ws, **inputs)
+    _launch(dev, "moonep_shared_ffn_bwd", x.data_ptr(), dy.data_ptr(), w, kind, T, H, Hp, _ptr(dx),
+            None if dw is None else _abi.ptr3(dw), code, ws.data_ptr(), ws.numel())
+    return dx, dw
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -666,10 +774,7 @@ def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0
 
 def block_norm_bwd_workspace(T, W, device="cuda"):
     """Workspace tensor of `block_norm_bwd` for T rows of W elements."""
-    nbytes = int(lib().moonep_block_norm_bwd_ws(T, W))
-    if nbytes < 0:
-        raise MoonepError(_abi.MOONEP_ERR_CONFIG, "moonep_block_norm_bwd_ws")
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    return _workspace("moonep_block_norm_bwd_ws", lib().moonep_block_norm_bwd_ws(T, W), device)
 
 
 def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0,

@@ -79,6 +79,11 @@ def lib():
         "moonep_orthogonalize_tile": (i32, [i32, i32, i32, i32]),
         "moonep_orthogonalize": (i32, [vp, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_float), i32,
                                        ctypes.c_float, vp, vp, i64, vp]),
+        "moonep_shared_ffn_ws": (i64, [i64, i32, i32]),
+        "moonep_shared_ffn": (i32, [vp, P3, i32, vp, i64, i32, i32, vp, vp, i64, vp]),
+        "moonep_shared_ffn_bwd_ws": (i64, [i64, i32, i32]),
+        "moonep_shared_ffn_bwd": (i32, [vp, vp, P3, i32, i64, i32, i32, vp, ctypes.POINTER(vp), i32,
+                                        vp, i64, vp]),
         "moonep_block_norm": (i32, [vp, i32, vp, vp, vp, i32, vp, vp, ctypes.c_float,
                                     ctypes.c_float, i64, i32, vp, vp, vp]),
         "moonep_block_norm_bwd_ws": (i64, [i64, i32]),
@@ -140,6 +145,7 @@ def plan_len(cfg: MoonepConfig, which: int) -> int:
  GRID_COMBINE_BWD) = range(6)
 F32, BF16 = range(2)
 SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"silu": 0, "gelu_tanh": 1}
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = range(4)
 ORTHO_MAX_STEPS, ORTHO_MAX_GAIN = 16, 2048
 ORTHO_PRODUCTS = ORTHO_FIRST, ORTHO_R, ORTHO_TP, ORTHO_A, ORTHO_LAST = tuple(range(5))

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoonep.so")
 SOURCES = ["api.hip", "plan.hip", "plan_noalloc.hip", "move.hip", "gemm.hip", "gemm_bwd.hip",
-           "route.hip", "ortho.hip", "norm.hip", "symbuf.hip"]
+           "route.hip", "ortho.hip", "norm.hip", "shared_ffn.hip",
+           "symbuf.hip"]
 ARCH = "gfx950"
 
 

@@ -340,6 +340,69 @@ moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, in
                                          stream));
 }
 
+static bool views_ok(const uint16_t* const views[3], int p0, int p1) {
+  if (!views) return false;
+  for (int p = p0; p < p1; ++p)
+    if (!views[p] || !aligned(views[p], 16)) return false;
+  return true;
+}
+
+static bool ffn_form_ok(const uint16_t* const w[3], int32_t act) {
+  return w && (act == MOONEP_ACT_SILU || act == MOONEP_ACT_GELU_TANH) && views_ok(w, 0, 3);
+}
+
+int64_t moonep_shared_ffn_ws(int64_t T, int32_t H, int32_t Hp) {
+  return shared_ffn_shape_ok(T, H, Hp) ? shared_ffn_ws_bytes(T, H, Hp) : -1;
+}
+
+moonep_status_t moonep_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,
+                                  const uint16_t* add, int64_t T, int32_t H, int32_t Hp,
+                                  uint16_t* y, void* ws, int64_t ws_bytes, hipStream_t stream) {
+  if (!shared_ffn_shape_ok(T, H, Hp)) return MOONEP_ERR_CONFIG;
+  if (!ffn_form_ok(w, act)) return MOONEP_ERR_ARG;
+  if (T == 0) return MOONEP_OK;
+  if (!x || !y || !ws || !aligned(x, 16) || !aligned(y, 16) || !aligned(add, 16) ||
+      !aligned(ws, 256))
+    return MOONEP_ERR_ARG;
+  const void* in[] = {x, w[0], w[1], w[2], ws};
+  for (const void* p : in)
+    if (p == (const void*)y) return MOONEP_ERR_ARG;
+  if (ws_bytes < shared_ffn_ws_bytes(T, H, Hp)) return MOONEP_ERR_SCRATCH;
+  return hip_status(launch_shared_ffn(x, w, act, add, T, H, Hp, y, (char*)ws, stream));
+}
+
+int64_t moonep_shared_ffn_bwd_ws(int64_t T, int32_t H, int32_t Hp) {
+  return shared_ffn_bwd_shape_ok(T, H, Hp) ? shared_ffn_bwd_ws_bytes(T, H, Hp) : -1;
+}
+
+moonep_status_t moonep_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
+                                      const uint16_t* const w[3], int32_t act, int64_t T,
+                                      int32_t H, int32_t Hp, uint16_t* dx, void* const dw[3],
+                                      int32_t dw_dtype, void* ws, int64_t ws_bytes,
+                                      hipStream_t stream) {
+  if (!shared_ffn_bwd_shape_ok(T, H, Hp)) return MOONEP_ERR_CONFIG;
+  if (!ffn_form_ok(w, act) || (dw_dtype != MOONEP_F32 && dw_dtype != MOONEP_BF16))
+    return MOONEP_ERR_ARG;
+  for (int i = 0; dw && i < 3; ++i)
+    if (!dw[i] || !aligned(dw[i], 16)) return MOONEP_ERR_ARG;
+  if (T > 0) {
+    if (!x || !dy || !ws || !aligned(x, 16) || !aligned(dy, 16) || !aligned(dx, 16) ||
+        !aligned(ws, 256))
+      return MOONEP_ERR_ARG;
+    const void* in[] = {x, dy, w[0], w[1], w[2], ws};
+    const void* out[] = {dx, dw ? dw[0] : nullptr, dw ? dw[1] : nullptr, dw ? dw[2] : nullptr};
+    for (int i = 0; i < 4; ++i) {
+      for (const void* p : in)
+        if (out[i] == p) return MOONEP_ERR_ARG;
+      for (int j = 0; out[i] && j < i; ++j)
+        if (out[i] == out[j]) return MOONEP_ERR_ARG;
+    }
+    if (ws_bytes < shared_ffn_bwd_ws_bytes(T, H, Hp)) return MOONEP_ERR_SCRATCH;
+  }
+  return hip_status(launch_shared_ffn_bwd(x, dy, w, act, T, H, Hp, dx, dw, dw_dtype, (char*)ws,
+                                          stream));
+}
+
 // What the forward and the backward of a block's norms take alike.
 // (arrays of no rows may be NULL).
 static bool norm_form_ok(int64_t T, int32_t dtype, const void* y, const void* y2, const void* gate,
@@ -439,13 +502,6 @@ static bool weights_ok(const Ctx& c, const uint16_t* const home[3],
     if (!home[p] || !aligned(home[p], 16)) return false;
     if (c.d.B > 0 && (!pool[p] || !aligned(pool[p], 16))) return false;
   }
-  return true;
-}
-
-static bool views_ok(const uint16_t* const views[3], int p0, int p1) {
-  if (!views) return false;
-  for (int p = p0; p < p1; ++p)
-    if (!views[p] || !aligned(views[p], 16)) return false;
   return true;
 }
 

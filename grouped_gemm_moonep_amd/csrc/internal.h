@@ -184,6 +184,19 @@ int64_t norm_ws_bytes(int64_t T, int32_t W);
 hipError_t launch_norm(const NormArgs& a, int32_t dtype, hipStream_t s);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int32_t dtype, hipStream_t s);
 
+// The shared expert (shared_ffn.hip).  w: gate, up, down.
+bool shared_ffn_shape_ok(int64_t T, int32_t H, int32_t Hp);
+bool shared_ffn_bwd_shape_ok(int64_t T, int32_t H, int32_t Hp);
+int64_t shared_ffn_ws_bytes(int64_t T, int32_t H, int32_t Hp);
+int64_t shared_ffn_bwd_ws_bytes(int64_t T, int32_t H, int32_t Hp);
+hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,
+                             const uint16_t* add, int64_t T, int32_t H, int32_t Hp, uint16_t* y,
+                             char* ws, hipStream_t s);
+hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
+                                 const uint16_t* const w[3], int32_t act, int64_t T, int32_t H,
+                                 int32_t Hp, uint16_t* dx, void* const dw[3], int32_t dw_type,
+                                 char* ws, hipStream_t s);
+
 hipError_t launch_wgrad(const Ctx& c, const moonep_plan_t& p, int rank,
                         const uint16_t* a, const uint16_t* b, float* gh,
                         float* rb, hipStream_t s);

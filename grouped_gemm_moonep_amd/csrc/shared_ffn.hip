@@ -1,0 +1,995 @@
+// The shared expert on gfx950: a gated feed-forward block that every token
+// passes, dense and in token order, beside the routed experts of the MoonEP
+// path (MoonEP README, "Usage > Integration": the projections are stored
+// [H,H'] like theirs), and its gradients.
+//
+//   Z = bf16(f(X Wg) * (X Wu)),   Y = bf16(Z Wd^T + add),   f(g) = g sigma(c(g))
+//   silu:      c = g
+//   gelu_tanh: c = 2 sqrt(2/pi) (g + 0.044715 g^3)
+// backward, with G = X Wg and U = X Wu taken again:
+//   dZ = dY Wd (kept in fp32),  dU = bf16(dZ f(G)),  dG = bf16(dZ U f'(G)),
+//   f'(g) = s (1 + g (1 - s) c'(g)), s = sigma(c(g))
+//   dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU,  dWd = dY^T Z
+// Products are summed in fp32 on bf16 operands; Z, dG and dU are rounded once,
+// to be operands.
+//
+// Design for CDNA4.  Two kinds of tiles:
+//  - large: the 256-row tiles of gemm_core.h with their hand-scheduled K loop,
+//    one workgroup per CU, where their number fills the GPU;
+//  - small: 128, 64 or 32 rows by 128 columns with a plain ring of LDS-DMA
+//    stages, two workgroups per CU, where it does not.  K is then cut into
+//    splits, so that a few tokens still stream the weights through every CU; the
+//    splits' sums go to the workspace in fp32 and an elementwise kernel adds
+//    them in order (no atomics: results repeat) and finishes.
+#include "gemm_core.h"
+
+namespace moonep {
+namespace {
+
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------- activation
+struct Act {
+  float f, df;       // f(g), f'(g)
+};
+template <int KIND>
+__device__ __forceinline__ Act activate(float g) {
+  float c, dc;
+  if constexpr (KIND == MOONEP_ACT_SILU) {
+    c = g;
+    dc = 1.0f;
+  } else {
+    constexpr float k = 1.5957691216057308f;      // 2 sqrt(2 / pi)
+    // c(g) is far past where sigma is 0 or 1: no overflow of its cube (a NaN
+    // stays in the g outside)
+    const float t = fminf(fmaxf(g, -1e4f), 1e4f);
+    c = k * t * (1.0f + 0.044715f * t * t);
+    dc = k * (1.0f + 3 * 0.044715f * t * t);
+  }
+  // the hardware's reciprocal and exponential: about 1e-7, far below the
+  // rounding to bf16 that follows
+  const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-c));
+  return {g * s, s * (1.0f + g * (1.0f - s) * dc)};
+}
+__device__ __forceinline__ Act activate(int kind, float g) {
+  return kind == MOONEP_ACT_SILU ? activate<MOONEP_ACT_SILU>(g)
+                                 : activate<MOONEP_ACT_GELU_TANH>(g);
+}
+
+__device__ __forceinline__ float bf16_of(unsigned pair, int hi) {
+  return __uint_as_float(hi ? pair & 0xFFFF0000u : pair << 16);
+}
+
+// ------------------------------------------------------------- small tiles
+// Column tile of 128 columns as two regions of 64 (gate and up, or two halves
+// of one matrix): 64 k rows of 128 B each, whole cache lines.  16-byte chunk c
+// of row k sits at c ^ (4 (k / 2 % 2)): a transposing read of 32 lanes takes 64
+// bytes of four rows, two of which share each 256-byte window of the LDS.
+struct ColTile64 {
+  static constexpr bool kRows = false;
+  static constexpr int kLoads = 4;
+  static constexpr int kBytes = 2 * 64 * 128;
+  DmaRsrc rs;           // waves 0, 1: region 0; waves 2, 3: region 1
+  uint32_t voff, ld2, wlds;
+  __device__ __forceinline__ void init(const uint16_t* src0, const uint16_t* src1, int64_t ld,
+                                       int64_t k_total, int nv0, int nv1) {
+    const int w = wave_id(), lane = threadIdx.x & 63, region = w >> 1;
+    rs = make_dma_rsrc(region ? src1 : src0, k_total * ld * 2);
+    ld2 = (uint32_t)(ld * 2);
+    const int k = 32 * (w & 1) + (lane >> 3);          // load i adds 8 i rows
+    const int col = 8 * ((lane & 7) ^ (4 * ((k >> 1) & 1)));
+    voff = col < (region ? nv1 : nv0) ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
+    wlds = (uint32_t)(w * 4 * 1024);
+  }
+  __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
+    const uint32_t ko = valid ? (uint32_t)(k0 * ld2) : kOob;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_lds(rs, tile + wlds + i * 1024, voff + (ko + (uint32_t)(8 * i) * ld2));
+  }
+  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
+    const int lane = threadIdx.x & 63, q = lane & 15, g = (lane >> 4) & 1;
+    const lds_t* region = tile + (nb >> 6) * 8192;
+    const int col = (nb & 63) + 16 * g + 4 * (q & 3);
+    i16x4 h[2];
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int k = 16 * kk + 8 * lh + 4 * hh + (q >> 2);
+      const int off = k * 128 + (((col >> 3) ^ (4 * ((k >> 1) & 1))) << 4) + (col & 7) * 2;
+      h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) i16x4*)(region + off));
+    }
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+template <class T> struct TileBytes;
+template <int NL> struct TileBytes<RowTileT<NL>> { static constexpr int value = NL * 4096; };
+template <int NL> struct TileBytes<RowTile2<NL>> { static constexpr int value = NL * 4096; };
+template <> struct TileBytes<ColTile64> { static constexpr int value = ColTile64::kBytes; };
+
+template <class T>
+__device__ __forceinline__ bf16x8 frag_of(const lds_t* tile, int base, int kk) {
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  if constexpr (T::kRows) return T::frag(tile, base + lr, kk, lh);
+  else return T::frag(tile, base, kk, lh);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// The K loop of the small tiles: DEPTH stages of A and B, loads DEPTH - 1 steps
+// ahead (out-of-range ones past the end keep the wait counts), one barrier a
+// step: it orders the arrival of step j's stage before its reads, and all reads
+// of step j - 1 before the loads into its slot.
+template <int MI, int NJ, int DEPTH, class TA, class TB>
+__device__ __forceinline__ void small_loop(const TA& la, const TB& lb, lds_t* lds, int j0, int j1,
+                                           f32x16 (&acc)[MI][NJ], int arow0, const int (&nrow)[NJ]) {
+  constexpr int kA = TileBytes<TA>::value, kStage = kA + TileBytes<TB>::value;
+  constexpr int kPer = TA::kLoads + TB::kLoads;
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) {
+    const bool v = j0 + d < j1;
+    la.issue(lds + d * kStage, (int64_t)(j0 + d) * BK, v);
+    lb.issue(lds + d * kStage + kA, (int64_t)(j0 + d) * BK, v);
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  int slot = 0;
+  for (int j = j0; j < j1; ++j) {
+    wait_vm<(DEPTH - 2) * kPer>();
+    barrier_reads_done();
+    {
+      const int jn = j + DEPTH - 1;
+      lds_t* to = lds + (slot == 0 ? DEPTH - 1 : slot - 1) * kStage;
+      la.issue(to, (int64_t)jn * BK, jn < j1);
+      lb.issue(to + kA, (int64_t)jn * BK, jn < j1);
+    }
+    const lds_t* A = lds + slot * kStage;
+    const lds_t* Bt = A + kA;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      bf16x8 fa[MI], fb[NJ];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) fa[i] = frag_of<TA>(A, arow0 + 32 * i, kk);
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) fb[i] = frag_of<TB>(Bt, nrow[i], kk);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int n = 0; n < NJ; ++n)
+          acc[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
+    }
+    slot = slot == DEPTH - 1 ? 0 : slot + 1;
+  }
+  wait_vm<0>();                 // nothing in flight when the workgroup ends
+}
+
+// Rows of a small tile by template: waves 2 x 2 with (BM / 64) x 2 blocks each,
+// or, at 32 rows, one block of 32 columns each.
+template <int BM>
+struct Small {
+  static constexpr int MI = BM == 128 ? 2 : 1, NJ = BM == 32 ? 1 : 2;
+  static constexpr int DEPTH = BM == 128 ? 2 : BM == 64 ? 3 : 4;
+  static constexpr int NL = BM / 32;
+  static constexpr int kLds = DEPTH * (BM * 128 + 16384);
+  int arow0;
+  int nrow[NJ];          // the first 32 columns of a pair lie in region 0, the second in region 1
+  __device__ __forceinline__ Small() {
+    const int w = threadIdx.x >> 6;
+    if constexpr (BM == 32) {
+      arow0 = 0;
+      nrow[0] = 32 * w;
+    } else {
+      arow0 = (w >> 1) * 32 * MI;
+      nrow[0] = (w & 1) * 32;
+      nrow[1] = 64 + (w & 1) * 32;
+    }
+  }
+};
+
+struct SmallArgs {
+  // sub-problem p < 3: A [M][K] rows (or [K][M] columns), B; see small_kernel
+  const uint16_t* a[3];
+  const uint16_t* b[3];
+  void* out[3];
+  const uint16_t* add;
+  float* part;
+  int M, N, K;           // of every sub-problem
+  int ntm, ntn, S;       // tiles of all sub-problems together: ntm x ntn, each cut into S splits
+  int act, f32;
+};
+
+enum SmallOp {
+  OP_GATEUP,             // rows X, columns Wg and Wu: 64 of each a tile
+  OP_GRAD,               // the same, then tiles of dZ: rows dY, columns of Wd
+  OP_ROWS,               // rows A, rows B: Z Wd^T
+  OP_ROWS2,              // rows [dG|dU], rows [Wg|Wu]: K = 2 H'
+  OP_WGRAD               // columns A, columns B: three products over the tokens
+};
+template <int OP, int BM> struct SmallTiles { typedef RowTileT<BM / 32> A; typedef ColTile64 B; };
+template <int BM> struct SmallTiles<OP_ROWS, BM> {
+  typedef RowTileT<BM / 32> A; typedef RowTileT<4> B;
+};
+template <int BM> struct SmallTiles<OP_ROWS2, BM> {
+  typedef RowTile2<BM / 32> A; typedef RowTile2<4> B;
+};
+template <int BM> struct SmallTiles<OP_WGRAD, BM> { typedef ColTile64 A; typedef ColTile64 B; };
+
+// One tile, one split.  PART: the sums go to part [S][M][all columns] in fp32
+// (columns: G, U and dZ side by side for OP_GATEUP and OP_GRAD; OP_WGRAD has
+// [S][3][M][N]).  Otherwise the tile is finished here: OP_GATEUP writes Z,
+// OP_ROWS and OP_ROWS2 bf16 (+ add), OP_WGRAD bf16 or adds to fp32.
+template <int OP, int BM, bool PART>
+__global__ __launch_bounds__(kThreads, 2) void small_kernel(SmallArgs a) {
+  typedef Small<BM> G;
+  typedef typename SmallTiles<OP, BM>::A TA;
+  typedef typename SmallTiles<OP, BM>::B TB;
+  constexpr int MI = G::MI, NJ = G::NJ;
+  __shared__ __attribute__((aligned(16))) char smem[G::kLds];
+  const G g;
+  // each XCD takes a run of tiles: M fastest (they share the weights), then N, then the split
+  const int64_t total = (int64_t)a.ntm * a.ntn * a.S, per = (total + kXcds - 1) / kXcds;
+  const int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || l >= total) return;
+  const int tm = (int)(l % a.ntm);
+  int tn = (int)(l / a.ntm % a.ntn);
+  const int sp = (int)(l / ((int64_t)a.ntm * a.ntn));
+  const int m0 = tm * BM;
+  const int mv = a.M - m0 < BM ? a.M - m0 : BM;
+  const int nk = (a.K + BK - 1) / BK;
+  const int j0 = (int)((int64_t)nk * sp / a.S), j1 = (int)((int64_t)nk * (sp + 1) / a.S);
+  int p = 0;                     // sub-problem
+  if constexpr (OP == OP_GRAD) {
+    const int gu = a.N / 64;
+    if (tn >= gu) {
+      p = 2;
+      tn -= gu;
+    }
+  }
+  if constexpr (OP == OP_WGRAD) {
+    const int each = a.ntn / 3;
+    p = tn / each;
+    tn -= p * each;
+  }
+  const bool pair = (OP == OP_GATEUP || OP == OP_GRAD) && p == 0;
+  const int n0 = tn * (pair ? 64 : 128);
+  const int nv = a.N - n0 < (pair ? 64 : 128) ? a.N - n0 : (pair ? 64 : 128);
+  TA la;
+  TB lb;
+  const uint16_t *pa = a.a[p], *pb = a.b[p];
+  if constexpr (OP == OP_GATEUP || OP == OP_GRAD) {
+    la.init(pa + (int64_t)m0 * a.K, a.K, mv);
+    if (pair) lb.init(pb + n0, a.b[1] + n0, a.N, a.K, nv, nv);
+    else lb.init(pb + n0, pb + n0 + 64, a.N, a.K, nv < 64 ? nv : 64, nv < 64 ? 0 : nv - 64);
+  } else if constexpr (OP == OP_ROWS) {
+    la.init(pa + (int64_t)m0 * a.K, a.K, mv);
+    lb.init(pb + (int64_t)n0 * a.K, a.K, nv);
+  } else if constexpr (OP == OP_ROWS2) {
+    const int k1 = a.K / 2;
+    la.init(pa + (int64_t)m0 * k1, a.a[1] + (int64_t)m0 * k1, k1, mv, k1);
+    lb.init(pb + (int64_t)n0 * k1, a.b[1] + (int64_t)n0 * k1, k1, nv, k1);
+  } else {
+    la.init(pa + m0, pa + m0 + 64, a.M, a.K, mv < 64 ? mv : 64, mv < 64 ? 0 : mv - 64);
+    lb.init(pb + n0, pb + n0 + 64, a.N, a.K, nv < 64 ? nv : 64, nv < 64 ? 0 : nv - 64);
+  }
+  f32x16 acc[MI][NJ];
+  small_loop<MI, NJ, G::DEPTH>(la, lb, (lds_t*)smem, j0, j1, acc, g.arow0, g.nrow);
+
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  if constexpr (PART) {
+    const int64_t cols = OP == OP_GATEUP ? 2LL * a.N : OP == OP_GRAD ? 3LL * a.N : a.N;
+    float* out = a.part + (OP == OP_WGRAD ? (int64_t)sp * 3 + p : sp) * a.M * cols;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = g.arow0 + 32 * i + lr;
+      if (m >= mv) continue;
+      float* row = out + (int64_t)(m0 + m) * cols;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          int c = g.nrow[j] + acc_col(q, lh);
+          int64_t col;
+          if (pair) {
+            const int up = c >> 6;
+            c &= 63;
+            col = (int64_t)up * a.N + n0 + c;
+          } else {
+            col = (int64_t)p * (OP == OP_GRAD ? a.N : 0) + n0 + c;
+          }
+          if (c < nv)
+            *(f32x4*)(row + col) = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                         acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = g.arow0 + 32 * i + lr;
+      if (m >= mv) continue;
+#pragma unroll
+      for (int j = 0; j < (OP == OP_GATEUP ? 1 : NJ); ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = g.nrow[j] + acc_col(q, lh);
+          if (c >= nv) continue;
+          const int64_t at = (int64_t)(m0 + m) * a.N + n0 + c;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          if constexpr (OP == OP_GATEUP && NJ == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]).f * acc[i][1][4 * q + e];
+          }
+          if constexpr (OP == OP_ROWS) {
+            if (a.add) {
+              const u32x2 d = *(const u32x2*)(a.add + at);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] += bf16_of(d[e >> 1], e & 1);
+            }
+          }
+          if (OP == OP_WGRAD && a.f32) {
+            f32x4* w = (f32x4*)((float*)a.out[p] + at);
+            f32x4 o = *w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += v[e];
+            *w = o;
+          } else {
+            *(u32x2*)((uint16_t*)a.out[p] + at) = u32x2{pack_bf16x2(v[0], v[1]),
+                                                        pack_bf16x2(v[2], v[3])};
+          }
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------- joins
+// Four neighbouring elements of every split, added in the splits' order.
+__device__ __forceinline__ f32x4 add_splits(const float* p, int S, int64_t slab) {
+  f32x4 v = *(const f32x4*)p;
+  for (int s = 1; s < S; ++s) v += *(const f32x4*)(p + s * slab);
+  return v;
+}
+__device__ __forceinline__ u32x2 pack4(const float v[4]) {
+  return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// z [M,N] from part [S][M][2N]; with dZ (part [S][M][3N]) dg, du and z.
+template <bool GRAD>
+__global__ __launch_bounds__(256) void join_gate(const float* part, int S, int M, int N, int act,
+                                                 uint16_t* z, uint16_t* dg, uint16_t* du) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= (int64_t)M * N) return;
+  const int64_t m = i / N, n = i % N, cols = (GRAD ? 3LL : 2LL) * N, slab = (int64_t)M * cols;
+  const float* p = part + m * cols + n;
+  const f32x4 g = add_splits(p, S, slab), u = add_splits(p + N, S, slab);
+  float zv[4], dgv[4], duv[4];
+  f32x4 dz = {0, 0, 0, 0};
+  if constexpr (GRAD) dz = add_splits(p + 2 * N, S, slab);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const Act t = activate(act, g[e]);
+    zv[e] = t.f * u[e];
+    dgv[e] = dz[e] * u[e] * t.df;
+    duv[e] = dz[e] * t.f;
+  }
+  *(u32x2*)(z + i) = pack4(zv);
+  if constexpr (GRAD) {
+    *(u32x2*)(dg + i) = pack4(dgv);
+    *(u32x2*)(du + i) = pack4(duv);
+  }
+}
+
+// out [n] bf16 from part [S][n] (+ add)
+__global__ __launch_bounds__(256) void join_rows(const float* part, int S, int64_t n,
+                                                 const uint16_t* add, uint16_t* out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const f32x4 s = add_splits(part + i, S, n);
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = s[e];
+  if (add) {
+    const u32x2 d = *(const u32x2*)(add + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += bf16_of(d[e >> 1], e & 1);
+  }
+  *(u32x2*)(out + i) = pack4(v);
+}
+
+// dw_p [n] from part [S][3][n]: bf16, or added to fp32
+struct JoinW {
+  void* out[3];
+};
+__global__ __launch_bounds__(256) void join_wgrad(const float* part, int S, int64_t n, int f32,
+                                                  JoinW w) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int p = blockIdx.y;
+  const f32x4 s = add_splits(part + p * n + i, S, 3 * n);
+  if (f32) {
+    f32x4* o = (f32x4*)((float*)w.out[p] + i);
+    *o += s;
+  } else {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = s[e];
+    *(u32x2*)((uint16_t*)w.out[p] + i) = pack4(v);
+  }
+}
+
+// ------------------------------------------------------------- large tiles
+struct LargeArgs {
+  const uint16_t* x;
+  const uint16_t* dy;
+  const uint16_t* w[3];
+  const uint16_t* add;
+  uint16_t* z;
+  uint16_t* y;
+  float* dz;
+  uint16_t* dg;
+  uint16_t* du;
+  uint16_t* dx;
+  void* dw[3];
+  int T, H, Hp, act, f32;
+  int ntm, ntn;
+};
+
+struct LargeTile {
+  int m0, rows, nt;
+};
+// M-tiles of `height` rows in groups of eight, each group swept over the
+// N-tiles, as in gemm_core.h: what runs together on an XCD shares weight slabs.
+__device__ __forceinline__ bool large_tile(const LargeArgs& a, int height, LargeTile* t) {
+  const int64_t total = (int64_t)a.ntm * a.ntn, per = (total + kXcds - 1) / kXcds;
+  const int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || l >= total) return false;
+  const int group = (int)(l / (8LL * a.ntn));
+  const int gm = a.ntm - 8 * group < 8 ? a.ntm - 8 * group : 8;
+  const int rem = (int)(l - 8LL * group * a.ntn);
+  t->nt = rem / gm;
+  t->m0 = (8 * group + rem % gm) * height;
+  t->rows = a.T - t->m0 < height ? a.T - t->m0 : height;
+  return true;
+}
+
+#define MOONEP_LARGE(name, body)                                                       \
+  template <int MI>                                                                    \
+  __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),           \
+                            amdgpu_waves_per_eu(1, 1))) void name(LargeArgs a) {       \
+    MOONEP_RING(smem);                                                                 \
+    LargeTile t;                                                                       \
+    if (!large_tile(a, 64 * MI, &t)) return;                                           \
+    if (MI == 4 && t.rows <= kHalfTileM) body<2>(a, smem, t);                          \
+    else body<MI>(a, smem, t);                                                         \
+  }
+
+// 32 MI x 2 rows, 128 gate and 128 up columns, K = H.
+template <int MI>
+__device__ __forceinline__ void gateup_product(const LargeArgs& a, const Ring& smem,
+                                               const LargeTile& t, f32x16 (&acc)[MI][4], int wm,
+                                               int wn) {
+  const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
+  const int nrow[4] = {wn * 64, wn * 64 + 32, 128 + wn * 64, 128 + wn * 64 + 32};
+  RowTileT<2 * MI> la;
+  ColTile lb;
+  la.init(a.x + (int64_t)t.m0 * a.H, a.H, t.rows);
+  lb.init(a.w[0] + n0, a.w[1] + n0, a.Hp, a.H, nv, nv);
+  gemm_loop<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
+}
+
+template <int MI>
+__device__ __forceinline__ void large_gateup_tile(const LargeArgs& a, const Ring& smem,
+                                                  const LargeTile& t) {
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
+  f32x16 acc[MI][4];
+  gateup_product<MI>(a, smem, t, acc, wm, wn);
+  typedef Stage<32 * MI, 64> St;
+  lds_t* reg = smem.base + wave * St::kBytes;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          z[e] = activate(a.act, acc[i][j][4 * q + e]).f * acc[i][j + 2][4 * q + e];
+        St::put(reg, i, j, q, pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+      }
+  const Rsrc zs = make_rsrc(a.z + (int64_t)t.m0 * a.Hp + n0, (int64_t)t.rows * a.Hp * 2);
+  St::flush(reg, zs, wm * 32 * MI, a.Hp, wn * 64, nv);
+}
+
+// A tile of 256 bf16 columns from the accumulators, by way of LDS.
+template <int MI>
+__device__ __forceinline__ void store_bf16(const Ring& smem, const f32x16 (&acc)[MI][4],
+                                           uint16_t* out, int64_t ld, int rows, int cols) {
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  typedef Stage<32 * MI, 128> St;
+  lds_t* reg = smem.base + wave * St::kBytes;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        St::put(reg, i, j, q, pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
+  St::flush(reg, make_rsrc(out, (int64_t)rows * ld * 2), wm * 32 * MI, ld, wn * 128, cols);
+}
+
+// Y: 256 columns, K = H'.  What is added is read 16 pieces ahead (two of a
+// wave's columns of blocks): all at once would not fit beside the sums.
+template <int MI>
+__device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& smem,
+                                                const LargeTile& t) {
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
+  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
+  RowTileT<2 * MI> la;
+  RowTile lb;
+  la.init(a.z + (int64_t)t.m0 * a.Hp, a.Hp, t.rows);
+  lb.init(a.w[2] + (int64_t)n0 * a.Hp, a.Hp, cols);
+  f32x16 acc[MI][4];
+  gemm_loop<MI>(la, lb, smem, a.Hp / BK, acc, wm * 32 * MI, nrow);
+  const int64_t at = (int64_t)t.m0 * a.H + n0;
+  if (a.add) {
+    const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = wm * 32 * MI + 32 * i + lr;
+      const uint16_t* row = a.add + at + (int64_t)m * a.H;
+#pragma unroll
+      for (int jj = 0; jj < 4; jj += 2) {
+        u32x2 v[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = nrow[jj + j] + acc_col(q, lh);
+            v[j][q] = u32x2{0, 0};
+            if (m < t.rows && c < cols) v[j][q] = *(const u32x2*)(row + c);
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i][jj + j][4 * q + e] += bf16_of(v[j][q][e >> 1], e & 1);
+      }
+    }
+  }
+  store_bf16<MI>(smem, acc, a.y + at, a.H, t.rows, cols);
+}
+
+// dZ in fp32: 256 columns of H', K = H.
+template <int MI>
+__device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& smem,
+                                              const LargeTile& t) {
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int n0 = t.nt * BN, cols = a.Hp - n0 < BN ? a.Hp - n0 : BN;
+  const int nv0 = cols < 128 ? cols : 128;
+  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
+  RowTileT<2 * MI> la;
+  ColTile lb;
+  la.init(a.dy + (int64_t)t.m0 * a.H, a.H, t.rows);
+  lb.init(a.w[2] + n0, a.w[2] + n0 + 128, a.Hp, a.H, nv0, cols - nv0);
+  f32x16 acc[MI][4];
+  gemm_loop<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = wm * 32 * MI + 32 * i + lr;
+    if (m >= t.rows) continue;
+    float* row = a.dz + (int64_t)(t.m0 + m) * a.Hp + n0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = nrow[j] + acc_col(q, lh);
+        if (c < cols)
+          *(f32x4*)(row + c) = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                     acc[i][j][4 * q + 3]};
+      }
+  }
+}
+
+// dG, dU and Z from the gate/up product and dZ.
+template <int MI>
+__device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& smem,
+                                              const LargeTile& t) {
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
+  f32x16 acc[MI][4];
+  gateup_product<MI>(a, smem, t, acc, wm, wn);
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  typedef Stage<32 * MI, 64> St;
+  lds_t* reg_g = smem.base + wave * (2 * St::kBytes);
+  lds_t* reg_u = reg_g + St::kBytes;
+  const int64_t at = (int64_t)t.m0 * a.Hp + n0, range = (int64_t)t.rows * a.Hp * 2;
+  // Z is kept in the accumulators of U until dG and dU are stored
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    f32x4 dzv[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int m = wm * 32 * MI + i * 32 + lr, n = wn * 64 + j * 32 + acc_col(q, lh);
+        dzv[j][q] = f32x4{0, 0, 0, 0};
+        if (m < t.rows && n < nv) dzv[j][q] = *(const f32x4*)(a.dz + at + (int64_t)m * a.Hp + n);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float dg[4], du[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = acc[i][j + 2][4 * q + e], d = dzv[j][q][e];
+          const Act f = activate(a.act, acc[i][j][4 * q + e]);
+          du[e] = d * f.f;
+          dg[e] = d * u * f.df;
+          acc[i][j + 2][4 * q + e] = f.f * u;
+        }
+        St::put(reg_g, i, j, q, pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
+        St::put(reg_u, i, j, q, pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
+      }
+  }
+  St::flush(reg_g, make_rsrc(a.dg + at, range), wm * 32 * MI, a.Hp, wn * 64, nv);
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        St::put(reg_g, i, j, q,
+                pack_bf16x2(acc[i][j + 2][4 * q], acc[i][j + 2][4 * q + 1]),
+                pack_bf16x2(acc[i][j + 2][4 * q + 2], acc[i][j + 2][4 * q + 3]));
+  St::flush(reg_u, make_rsrc(a.du + at, range), wm * 32 * MI, a.Hp, wn * 64, nv);
+  St::flush(reg_g, make_rsrc(a.z + at, range), wm * 32 * MI, a.Hp, wn * 64, nv);
+}
+
+// dX: 256 columns of H, K = 2 H' over [dG | dU] and [Wg | Wu].
+template <int MI>
+__device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& smem,
+                                              const LargeTile& t) {
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
+  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
+  RowTile2<2 * MI> la;
+  RowTile2<8> lb;
+  const int64_t ab = (int64_t)t.m0 * a.Hp, bb = (int64_t)n0 * a.Hp;
+  la.init(a.dg + ab, a.du + ab, a.Hp, t.rows, a.Hp);
+  lb.init(a.w[0] + bb, a.w[1] + bb, a.Hp, cols, a.Hp);
+  f32x16 acc[MI][4];
+  gemm_loop<MI>(la, lb, smem, 2 * a.Hp / BK, acc, wm * 32 * MI, nrow);
+  store_bf16<MI>(smem, acc, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
+}
+
+MOONEP_LARGE(large_gateup, large_gateup_tile)
+MOONEP_LARGE(large_down, large_down_tile)
+MOONEP_LARGE(large_dz, large_dz_tile)
+MOONEP_LARGE(large_gu, large_gu_tile)
+MOONEP_LARGE(large_dx, large_dx_tile)
+
+// dW of the three projections: 256 x 256 tiles, the sum over the tokens.
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
+                          amdgpu_waves_per_eu(1, 1))) void large_wgrad(LargeArgs a) {
+  MOONEP_RING(smem);
+  const int64_t each = (int64_t)a.ntm * a.ntn, total = 3 * each, per = (total + kXcds - 1) / kXcds;
+  const int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (blockIdx.x / kXcds >= per || l >= total) return;
+  const int p = (int)(l / each), rem = (int)(l % each);
+  const int m0 = rem / a.ntn * BM, n0 = rem % a.ntn * BN;
+  const int mv = a.H - m0 < BM ? a.H - m0 : BM, nv = a.Hp - n0 < BN ? a.Hp - n0 : BN;
+  const int mv0 = mv < 128 ? mv : 128, nv0 = nv < 128 ? nv : 128;
+  const uint16_t* A = (p == 2 ? a.dy : a.x) + m0;
+  const uint16_t* Bm = (p == 0 ? a.dg : p == 1 ? a.du : a.z) + n0;
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
+  ColTile la, lb;
+  la.init(A, A + 128, a.H, a.T, mv0, mv - mv0);
+  lb.init(Bm, Bm + 128, a.Hp, a.T, nv0, nv - nv0);
+  f32x16 acc[4][4];
+  gemm_loop<4>(la, lb, smem, (a.T + BK - 1) / BK, acc, wm * 128, nrow);
+  void* out = p == 0 ? a.dw[0] : p == 1 ? a.dw[1] : a.dw[2];
+  const int64_t at = (int64_t)m0 * a.Hp + n0;
+  if (!a.f32) {
+    store_bf16<4>(smem, acc, (uint16_t*)out + at, a.Hp, mv, nv);
+    return;
+  }
+  // read-modify-write, the 16 reads of a block row before its writes
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = wm * 128 + i * 32 + lr;
+    float* row = (float*)out + at + (int64_t)m * a.Hp;
+    f32x4 v[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = nrow[j] + acc_col(q, lh);
+        if (m < mv && n < nv) v[j][q] = *(const f32x4*)(row + n);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = nrow[j] + acc_col(q, lh);
+        if (m < mv && n < nv) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[j][q][e] += acc[i][j][4 * q + e];
+          *(f32x4*)(row + n) = v[j][q];
+        }
+      }
+  }
+}
+
+// ------------------------------------------------------------- choice
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How one product runs: `rows` of a tile (256 and 128 with large = true), its tiles and splits.
+struct Shape {
+  bool large;
+  int rows, ntm, ntn, S;
+};
+
+// M x N outputs (in tiles of small_n and large_n columns), K in steps of 64.
+Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk) {
+  Shape s;
+  // large tiles where they fill the GPU (one workgroup per CU)
+  const int64_t full = ceil_div(M, 256) * cols_large, half = ceil_div(M, 128) * cols_large;
+  s.large = full >= 192 || half >= 192;
+  if (s.large) {
+    s.rows = full >= 192 ? 256 : 128;
+    s.ntm = (int)ceil_div(M, s.rows);
+    s.ntn = (int)cols_large;
+    s.S = 1;
+    return s;
+  }
+  s.rows = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  s.ntm = (int)ceil_div(M, s.rows);
+  s.ntn = (int)cols_small;
+  const int64_t tiles = (int64_t)s.ntm * s.ntn;
+  int64_t S = ceil_div(512, tiles);
+  if (S > nk / 4) S = nk / 4;
+  s.S = (int)(S < 1 ? 1 : S);
+  return s;
+}
+Shape gateup_shape(int64_t T, int H, int Hp) {
+  return pick(T, Hp / 64, ceil_div(Hp, 128), H / BK);
+}
+Shape down_shape(int64_t T, int H, int Hp) {
+  return pick(T, ceil_div(H, 128), ceil_div(H, 256), Hp / BK);
+}
+Shape dx_shape(int64_t T, int H, int Hp) {
+  return pick(T, ceil_div(H, 128), ceil_div(H, 256), 2 * Hp / BK);
+}
+// dG, dU, Z: tiles of gate and up, and of dZ (in the same launch where they are small)
+Shape grad_shape(int64_t T, int H, int Hp) {
+  return pick(T, Hp / 64 + ceil_div(Hp, 128), ceil_div(Hp, 128), H / BK);
+}
+Shape wgrad_shape(int64_t T, int H, int Hp) {
+  const int nk = (int)ceil_div(T, BK);
+  Shape s;
+  s.S = 1;
+  s.large = 3 * ceil_div(H, 256) * ceil_div(Hp, 256) >= 192;
+  s.rows = s.large ? 256 : 128;
+  s.ntm = (int)ceil_div(H, s.rows);
+  s.ntn = (int)ceil_div(Hp, s.rows);
+  if (!s.large) {
+    s.ntn *= 3;
+    int64_t S = ceil_div(512, (int64_t)s.ntm * s.ntn);
+    if (S > nk / 4) S = nk / 4;
+    s.S = (int)(S < 1 ? 1 : S);
+  }
+  return s;
+}
+
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace: what lies where, in bytes.
+struct FwdWs {
+  int64_t z, part, total;
+};
+FwdWs fwd_ws(int64_t T, int H, int Hp) {
+  FwdWs w;
+  w.z = 0;
+  w.part = round256(T * Hp * 2);
+  const Shape g = gateup_shape(T, H, Hp), d = down_shape(T, H, Hp);
+  int64_t p = 0;
+  if (!g.large) p = (int64_t)g.S * T * 2 * Hp * 4;
+  if (!d.large && d.S > 1 && (int64_t)d.S * T * H * 4 > p) p = (int64_t)d.S * T * H * 4;
+  w.total = w.part + round256(p);
+  return w;
+}
+struct BwdWs {
+  int64_t z, dg, du, dz, part, total;
+};
+BwdWs bwd_ws(int64_t T, int H, int Hp) {
+  BwdWs w;
+  const int64_t one = round256(T * Hp * 2);
+  w.z = 0;
+  w.dg = one;
+  w.du = 2 * one;
+  w.dz = w.part = 3 * one;
+  const Shape g = grad_shape(T, H, Hp), x = dx_shape(T, H, Hp), d = wgrad_shape(T, H, Hp);
+  int64_t p = g.large ? T * Hp * 4 : (int64_t)g.S * T * 3 * Hp * 4;
+  if (!x.large && x.S > 1 && (int64_t)x.S * T * H * 4 > p) p = (int64_t)x.S * T * H * 4;
+  if (!d.large && d.S > 1 && (int64_t)d.S * 3 * H * Hp * 4 > p) p = (int64_t)d.S * 3 * H * Hp * 4;
+  w.total = w.part + round256(p);
+  return w;
+}
+
+unsigned blocks_of(const Shape& s) {
+  return (unsigned)(ceil_div((int64_t)s.ntm * s.ntn * s.S, kXcds) * kXcds);
+}
+unsigned joins(int64_t n) { return (unsigned)ceil_div(n, 1024); }
+
+template <int OP>
+void run_small(const Shape& s, bool part, SmallArgs a, hipStream_t st) {
+  a.ntm = s.ntm;
+  a.ntn = s.ntn;
+  a.S = s.S;
+  const unsigned n = blocks_of(s);
+  if constexpr (OP == OP_WGRAD) {
+    if (part) small_kernel<OP, 128, true><<<n, kThreads, 0, st>>>(a);
+    else small_kernel<OP, 128, false><<<n, kThreads, 0, st>>>(a);
+  } else if (s.rows == 128) {
+    if (part || OP == OP_GRAD) small_kernel<OP, 128, true><<<n, kThreads, 0, st>>>(a);
+    else if constexpr (OP != OP_GRAD) small_kernel<OP, 128, false><<<n, kThreads, 0, st>>>(a);
+  } else if (s.rows == 64) {
+    if (part || OP == OP_GRAD) small_kernel<OP, 64, true><<<n, kThreads, 0, st>>>(a);
+    else if constexpr (OP != OP_GRAD) small_kernel<OP, 64, false><<<n, kThreads, 0, st>>>(a);
+  } else {
+    if (part || OP == OP_GRAD || OP == OP_GATEUP)
+      small_kernel<OP, 32, true><<<n, kThreads, 0, st>>>(a);
+    else if constexpr (OP != OP_GRAD && OP != OP_GATEUP)
+      small_kernel<OP, 32, false><<<n, kThreads, 0, st>>>(a);
+  }
+}
+
+#define MOONEP_RUN_LARGE(kernel, shape, args)                                       \
+  do {                                                                              \
+    LargeArgs la_ = args;                                                           \
+    la_.ntm = (shape).ntm;                                                          \
+    la_.ntn = (shape).ntn;                                                          \
+    if ((shape).rows == 256) kernel<4><<<blocks_of(shape), kThreads, 0, s>>>(la_);  \
+    else kernel<2><<<blocks_of(shape), kThreads, 0, s>>>(la_);                      \
+  } while (0)
+
+}  // namespace
+
+bool shared_ffn_shape_ok(int64_t T, int32_t H, int32_t Hp) {
+  return T >= 0 && T < (int64_t(1) << 31) && H >= 64 && H % 64 == 0 && H <= 65536 && Hp >= 64 &&
+         Hp % 64 == 0 && Hp <= 65536 && (int64_t)H * Hp < (int64_t(1) << 30);
+}
+bool shared_ffn_bwd_shape_ok(int64_t T, int32_t H, int32_t Hp) {
+  return shared_ffn_shape_ok(T, H, Hp) && T * (H > Hp ? H : Hp) < (int64_t(1) << 30);
+}
+int64_t shared_ffn_ws_bytes(int64_t T, int32_t H, int32_t Hp) {
+  return T == 0 ? 0 : fwd_ws(T, H, Hp).total;
+}
+int64_t shared_ffn_bwd_ws_bytes(int64_t T, int32_t H, int32_t Hp) {
+  return T == 0 ? 0 : bwd_ws(T, H, Hp).total;
+}
+
+hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,
+                             const uint16_t* add, int64_t T, int32_t H, int32_t Hp, uint16_t* y,
+                             char* ws, hipStream_t s) {
+  const FwdWs at = fwd_ws(T, H, Hp);
+  const Shape g = gateup_shape(T, H, Hp), d = down_shape(T, H, Hp);
+  uint16_t* z = (uint16_t*)(ws + at.z);
+  float* part = (float*)(ws + at.part);
+  LargeArgs big = {};
+  big.x = x; big.add = add; big.z = z; big.y = y;
+  for (int i = 0; i < 3; ++i) big.w[i] = w[i];
+  big.T = (int)T; big.H = H; big.Hp = Hp; big.act = act;
+  if (g.large) {
+    MOONEP_RUN_LARGE(large_gateup, g, big);
+  } else {
+    SmallArgs a = {};
+    a.a[0] = x; a.b[0] = w[0]; a.b[1] = w[1]; a.out[0] = z;
+    a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
+    const bool p = g.S > 1 || g.rows == 32;
+    run_small<OP_GATEUP>(g, p, a, s);
+    if (p) join_gate<false><<<joins(T * Hp), 256, 0, s>>>(part, g.S, (int)T, Hp, act, z, nullptr,
+                                                         nullptr);
+  }
+  if (d.large) {
+    MOONEP_RUN_LARGE(large_down, d, big);
+  } else {
+    SmallArgs a = {};
+    a.a[0] = z; a.b[0] = w[2]; a.out[0] = y; a.add = add;
+    a.part = part; a.M = (int)T; a.N = H; a.K = Hp;
+    run_small<OP_ROWS>(d, d.S > 1, a, s);
+    if (d.S > 1) join_rows<<<joins(T * H), 256, 0, s>>>(part, d.S, T * H, add, y);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
+                                 const uint16_t* const w[3], int32_t act, int64_t T, int32_t H,
+                                 int32_t Hp, uint16_t* dx, void* const dw[3], int32_t dw_type,
+                                 char* ws, hipStream_t s) {
+  if (T == 0) {                  // sums over no tokens
+    if (dw) {
+      SmallArgs a = {};
+      for (int i = 0; i < 3; ++i) a.out[i] = dw[i];
+      a.M = H; a.N = Hp; a.f32 = dw_type == MOONEP_F32;
+      const Shape z = {false, 128, (int)ceil_div(H, 128), 3 * (int)ceil_div(Hp, 128), 1};
+      run_small<OP_WGRAD>(z, false, a, s);
+    }
+    return hipGetLastError();
+  }
+  const BwdWs at = bwd_ws(T, H, Hp);
+  const Shape g = grad_shape(T, H, Hp), dxs = dx_shape(T, H, Hp), ws_ = wgrad_shape(T, H, Hp);
+  LargeArgs big = {};
+  big.x = x; big.dy = dy; big.dx = dx;
+  big.z = (uint16_t*)(ws + at.z); big.dg = (uint16_t*)(ws + at.dg); big.du = (uint16_t*)(ws + at.du);
+  big.dz = (float*)(ws + at.dz);
+  for (int i = 0; i < 3; ++i) {
+    big.w[i] = w[i];
+    big.dw[i] = dw ? dw[i] : nullptr;
+  }
+  big.T = (int)T; big.H = H; big.Hp = Hp; big.act = act; big.f32 = dw_type == MOONEP_F32;
+  float* part = (float*)(ws + at.part);
+  if (g.large) {
+    Shape z = g;
+    z.ntn = (int)ceil_div(Hp, BN);
+    MOONEP_RUN_LARGE(large_dz, z, big);
+    MOONEP_RUN_LARGE(large_gu, g, big);
+  } else {
+    SmallArgs a = {};
+    a.a[0] = x; a.a[2] = dy; a.b[0] = w[0]; a.b[1] = w[1]; a.b[2] = w[2];
+    a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
+    run_small<OP_GRAD>(g, true, a, s);
+    join_gate<true><<<joins(T * Hp), 256, 0, s>>>(part, g.S, (int)T, Hp, act, big.z, big.dg, big.du);
+  }
+  if (dx) {
+    if (dxs.large) {
+      MOONEP_RUN_LARGE(large_dx, dxs, big);
+    } else {
+      SmallArgs a = {};
+      a.a[0] = big.dg; a.a[1] = big.du; a.b[0] = w[0]; a.b[1] = w[1]; a.out[0] = dx;
+      a.part = part; a.M = (int)T; a.N = H; a.K = 2 * Hp;
+      run_small<OP_ROWS2>(dxs, dxs.S > 1, a, s);
+      if (dxs.S > 1) join_rows<<<joins(T * H), 256, 0, s>>>(part, dxs.S, T * H, nullptr, dx);
+    }
+  }
+  if (dw) {
+    if (ws_.large) {
+      LargeArgs a = big;
+      a.ntm = ws_.ntm;
+      a.ntn = ws_.ntn;
+      large_wgrad<<<(unsigned)(ceil_div(3LL * a.ntm * a.ntn, kXcds) * kXcds), kThreads, 0, s>>>(a);
+    } else {
+      SmallArgs a = {};
+      a.a[0] = a.a[1] = x; a.a[2] = dy;
+      a.b[0] = big.dg; a.b[1] = big.du; a.b[2] = big.z;
+      JoinW j;
+      for (int i = 0; i < 3; ++i) a.out[i] = j.out[i] = dw[i];
+      a.part = part; a.M = H; a.N = Hp; a.K = (int)T; a.f32 = big.f32;
+      run_small<OP_WGRAD>(ws_, ws_.S > 1, a, s);
+      const int64_t n = (int64_t)H * Hp;
+      if (ws_.S > 1)
+        join_wgrad<<<dim3(joins(n), 3), 256, 0, s>>>(part, ws_.S, n, big.f32, j);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moonep

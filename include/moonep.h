@@ -419,6 +419,42 @@ moonep_status_t moonep_orthogonalize(const void* g, int32_t dtype, int32_t n, in
                                      uint16_t* out, void* ws, int64_t ws_bytes,
                                      hipStream_t stream);
 
+/* The shared expert: a gated feed-forward block of every token beside the
+ * routed ones (framework-side on the pages), dense and in token order, with the
+ * projections stored [H,Hp] like the experts' (README "Usage > Integration"):
+ *   Z = bf16_rne(f(X Wg) * (X Wu)),  y = bf16_rne(Z Wd^T + add)
+ * for x [T,H] bf16, HOST array w of 3 device pointers (gate, up, down, each
+ * [H,Hp] bf16), f by act, and add [T,H] bf16 or NULL, such as moonep_combine's
+ * out.  f(g) = g sigma(c(g)) with c = g (SILU) or 2 sqrt(2/pi) (g + 0.044715 g^3)
+ * (GELU_TANH).  Products are summed in fp32.  y [T,H] may be add; no other
+ * aliasing.  ws: workspace of at least moonep_shared_ffn_ws bytes, 256-byte
+ * aligned; its contents need not be kept between calls, and calls that overlap
+ * need one each (MOONEP_ERR_SCRATCH if it is too small).  0 <= T < 2^31, H and Hp
+ * multiples of 64 up to 65536, H Hp < 2^30 (MOONEP_ERR_CONFIG).  Results repeat bit
+ * for bit.  The current device is used; no handle is needed. */
+enum { MOONEP_ACT_SILU = 0, MOONEP_ACT_GELU_TANH = 1 };
+int64_t moonep_shared_ffn_ws(int64_t T, int32_t H, int32_t Hp);   /* host only; -1 for bad sizes */
+moonep_status_t moonep_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,
+                                  const uint16_t* add, int64_t T, int32_t H, int32_t Hp,
+                                  uint16_t* y, void* ws, int64_t ws_bytes, hipStream_t stream);
+
+/* Gradients of moonep_shared_ffn (that of add is dy): for dy [T,H] bf16, with
+ * G = X Wg, U = X Wu and Z taken again and dZ = dy Wd held in fp32,
+ *   dU = bf16_rne(dZ f(G)), dG = bf16_rne(dZ U f'(G)),
+ *   dX = bf16_rne(dG Wg^T + dU Wu^T) -> dx [T,H], or not if dx is NULL;
+ *   dWg = X^T dG, dWu = X^T dU, dWd = dy^T Z -> HOST array dw of 3 device
+ *   pointers [H,Hp], or not if dw is NULL: written as bf16 (dw_dtype MOONEP_BF16), or
+ *   added to what is there (MOONEP_F32, as moonep_expert_wgrad does).
+ * dx and dw[] are apart from each other and from all inputs.  ws as in the
+ * forward, of moonep_shared_ffn_bwd_ws bytes.  Sizes as in the forward, and
+ * T max(H, Hp) < 2^30. */
+int64_t moonep_shared_ffn_bwd_ws(int64_t T, int32_t H, int32_t Hp);  /* host only; -1 for bad sizes */
+moonep_status_t moonep_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
+                                      const uint16_t* const w[3], int32_t act, int64_t T,
+                                      int32_t H, int32_t Hp, uint16_t* dx, void* const dw[3],
+                                      int32_t dw_dtype, void* ws, int64_t ws_bytes,
+                                      hipStream_t stream);
+
 /* A block's end and the next one's start in one pass (the framework-side steps
  * between combine and the next block): for T rows of W elements, with
  * rstd(v) = 1 / sqrt(mean(v^2) + eps),
