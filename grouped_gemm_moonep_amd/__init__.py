@@ -579,27 +579,47 @@ def orthogonalize(g, steps=5, coeffs=MUON_COEFFS, eps=1e-7, out=None, ws=None):
     return out
 
 
-def _ffn_inputs(x, weights, act):
-    """What shared_ffn and its backward check alike: (T, H, Hp, activation, weights' pointers)."""
-    if act not in _abi.ACTS:
-        raise ValueError(f"act: expected one of {sorted(_abi.ACTS)}, got {act!r}")
-    if len(weights) != 3 or any(w.dim() != 2 for w in weights):
-        raise ValueError("three projections (gate, up, down) [H,Hp] expected")
-    if x.dim() == 0:
-        raise ValueError("x: expected [...,H], got a scalar")
-    H, Hp = weights[0].shape
-    _dev_ptr(x, torch.bfloat16, (*x.shape[:-1], H), "x")
-    for name, w in zip(("gate", "up", "down"), weights):
-        _dev_ptr(w, torch.bfloat16, (H, Hp), name)
-        if w.device != x.device:
-            _same_device(x.device, **{name: w})
-    return math.prod(x.shape[:-1]), H, Hp, _abi.ACTS[act], _abi.ptr3(weights)
+def _rows(t, dtype, shape, dev, name):
+    """Pointer of an input of this type and shape on the device `dev`, checked at the least cost."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    p = _dev_ptr(t, dtype, shape, name)
+    _same_device(dev, **{name: t})
+    return p
+
+
+def _maybe(t, dtype, shape, dev, name):
+    return None if t is None else _rows(t, dtype, shape, dev, name)
 
 
 def _workspace(name, nbytes, device):
     if nbytes < 0:
         raise MoonepError(_abi.MOONEP_ERR_CONFIG, name)
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+def _ws_ptr(ws, dev, **inputs):
+    p = _rows(ws, torch.uint8, ws.shape, dev, "ws")
+    _apart("ws", ws, **inputs)
+    return p
+
+
+def _ffn_inputs(x, weights, act):
+    """What shared_ffn and its backward check alike: (T, H, Hp, activation, weights' pointers)."""
+    if act not in _abi.ACTS:
+        raise ValueError(f"act: expected one of {sorted(_abi.ACTS)}, got {act!r}")
+    if len(weights) != 3 or weights[0].dim() != 2:
+        raise ValueError("three projections (gate, up, down) [H,Hp] expected")
+    shape = weights[0].shape
+    H, Hp = shape
+    if x.dim() == 0:
+        raise ValueError("x: expected [...,H], got a scalar")
+    _dev_ptr(x, torch.bfloat16, (*x.shape[:-1], H), "x")
+    dev = x.device
+    w = _abi.PTR3(_rows(weights[0], torch.bfloat16, shape, dev, "gate"),
+                  _rows(weights[1], torch.bfloat16, shape, dev, "up"),
+                  _rows(weights[2], torch.bfloat16, shape, dev, "down"))
+    return x.numel() // H if H else 0, H, Hp, _abi.ACTS[act], w
 
 
 def shared_ffn_workspace(T, H, Hp, device="cuda"):
@@ -621,24 +641,20 @@ def shared_ffn(x, weights, act="silu", add=None, out=None, ws=None):
     call."""
     T, H, Hp, kind, w = _ffn_inputs(x, weights, act)
     dev = x.device
-    p_add = _dev_ptr(add, torch.bfloat16, x.shape, "add", True)
-    if add is not None:
-        _same_device(dev, add=add)
-    if out is None:
-        out = torch.empty_like(x)
-    else:
-        p = _dev_ptr(out, torch.bfloat16, x.shape, "out")
-        _same_device(dev, out=out)
-        _apart("out", out, x=x, gate=weights[0], up=weights[1], down=weights[2], ws=ws,
-               add=None if p == p_add else add)
+    p_add = _maybe(add, torch.bfloat16, x.shape, dev, "add")
     if ws is None:
         ws = shared_ffn_workspace(T, H, Hp, device=dev)
+        p_ws = ws.data_ptr()
     else:
-        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
-        _same_device(dev, ws=ws)
-        _apart("ws", ws, x=x, gate=weights[0], up=weights[1], down=weights[2], add=add)
-    _launch(dev, "moonep_shared_ffn", x.data_ptr(), w, kind, p_add, T, H, Hp, out.data_ptr(),
-            ws.data_ptr(), ws.numel())
+        p_ws = _ws_ptr(ws, dev, x=x, gate=weights[0], up=weights[1], down=weights[2], add=add)
+    if out is None:
+        out = torch.empty_like(x)
+        p = out.data_ptr()
+    else:
+        p = _rows(out, torch.bfloat16, x.shape, dev, "out")
+        _apart("out", out, x=x, gate=weights[0], up=weights[1], down=weights[2], ws=ws,
+               add=None if p == p_add else add)
+    _launch(dev, "moonep_shared_ffn", x.data_ptr(), w, kind, p_add, T, H, Hp, p, p_ws, ws.numel())
     return out
 
 
@@ -653,81 +669,71 @@ def shared_ffn_bwd(x, dy, weights, act="silu", need_dx=True, need_dw=True, dx=No
     T, H, Hp, kind, w = _ffn_inputs(x, weights, act)
     dev = x.device
     inputs = dict(x=x, dy=dy, gate=weights[0], up=weights[1], down=weights[2])
-    _dev_ptr(dy, torch.bfloat16, x.shape, "dy")
-    _same_device(dev, dy=dy)
+    p_dy = _rows(dy, torch.bfloat16, x.shape, dev, "dy")
     if (dx is not None and not need_dx) or (dw is not None and not need_dw):
         raise ValueError("dx or dw given, but need_dx or need_dw is False")
+    if ws is None:
+        ws = shared_ffn_bwd_workspace(T, H, Hp, device=dev)
+        p_ws = ws.data_ptr()
+    else:
+        p_ws = _ws_ptr(ws, dev, **inputs)
+    p_dx = None
     if dx is not None:
-        _dev_ptr(dx, torch.bfloat16, x.shape, "dx")
-        _same_device(dev, dx=dx)
+        p_dx = _rows(dx, torch.bfloat16, x.shape, dev, "dx")
         _apart("dx", dx, ws=ws, **inputs)
     elif need_dx:
         dx = torch.empty_like(x)
-    code = _abi.BF16
+        p_dx = dx.data_ptr()
+    code, p_dw = _abi.BF16, None
     if dw is not None:
         if len(dw) != 3:
             raise ValueError("three gradients (gate, up, down) expected")
         code = _float_type(dw[0], "dw[0]")
         for i, t in enumerate(dw):
-            _dev_ptr(t, dw[0].dtype, (H, Hp), f"dw[{i}]")
-            _same_device(dev, **{f"dw[{i}]": t})
+            _rows(t, dw[0].dtype, (H, Hp), dev, f"dw[{i}]")
             _apart(f"dw[{i}]", t, ws=ws, dx=dx, **inputs,
                    **{f"dw[{j}]": dw[j] for j in range(i)})
+        p_dw = _abi.ptr3(dw)
     elif need_dw:
-        dw = tuple(torch.empty_like(t) for t in weights)
-    if ws is None:
-        ws = shared_ffn_bwd_workspace(T, H, Hp, device=dev)
-    else:
-        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
-        _same_device(dev, ws=ws)
-        _apart("ws", ws, **inputs)
-    _launch(dev, "moonep_shared_ffn_bwd", x.data_ptr(), dy.data_ptr(), w, kind, T, H, Hp, _ptr(dx),
-            None if dw is None else _abi.ptr3(dw), code, ws.data_ptr(), ws.numel())
+        dw = tuple([torch.empty_like(t) for t in weights])
+        p_dw = _abi.PTR3(dw[0].data_ptr(), dw[1].data_ptr(), dw[2].data_ptr())
+    _launch(dev, "moonep_shared_ffn_bwd", x.data_ptr(), p_dy, w, kind, T, H, Hp, p_dx, p_dw, code,
+            p_ws, ws.numel())
     return dx, dw
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _gate(gate, shape):
-    """(kind, the gate as the library takes it) of a gate that broadcasts over `shape`."""
-    if gate is None:
-        return _abi.GATE_NONE
-    W = shape[-1]
-    if gate.dtype == torch.bfloat16:
-        _dev_ptr(gate, torch.bfloat16, shape, "gate")
-        return _abi.GATE_FULL
-    if gate.shape == (W,):
-        _dev_ptr(gate, torch.float32, (W,), "gate")
-        return _abi.GATE_CHANNEL
-    if gate.dtype == torch.float32 and gate.shape != (*shape[:-1], 1):
-        raise ValueError(f"gate: expected shape {(W,)} or {(*shape[:-1], 1)} in float32 or "
-                         f"{tuple(shape)} in bfloat16, got {tuple(gate.shape)}")
-    _dev_ptr(gate, torch.float32, (*shape[:-1], 1), "gate")
-    return _abi.GATE_TOKEN
-
-
 def _norm_inputs(h, y, y2, gate, w_post, w_pre):
-    """What block_norm and its backward check alike: (shape, T, W, gate kind)."""
-    shape = h.shape
+    """What block_norm and its backward check alike: the C call's arguments (h, dtype), (y, y2,
+    gate, kind, w_post, w_pre) and (T, W)."""
+    shape, dev = h.shape, h.device
     if len(shape) == 0:
         raise ValueError("h: expected [...,W], got a scalar")
     W = shape[-1]
-    _dev_ptr(h, h.dtype, shape, "h")
-    _dev_ptr(y, torch.bfloat16, shape, "y", True)
-    _dev_ptr(y2, torch.bfloat16, shape, "y2", True)
-    _dev_ptr(w_post, torch.float32, (W,), "w_post", True)
-    _dev_ptr(w_pre, torch.float32, (W,), "w_pre", True)
-    kind = _gate(gate, shape)
+    p_h, dt = _dev_ptr(h, h.dtype, shape, "h"), _float_type(h, "h")
+    p_gate, kind = None, _abi.GATE_NONE
+    if gate is not None:
+        if gate.dtype is torch.bfloat16:
+            p_gate, kind = _rows(gate, torch.bfloat16, shape, dev, "gate"), _abi.GATE_FULL
+        elif gate.shape == (W,):
+            p_gate, kind = _rows(gate, torch.float32, (W,), dev, "gate"), _abi.GATE_CHANNEL
+        else:
+            token = (*shape[:-1], 1)
+            if gate.dtype is torch.float32 and gate.shape != token:
+                raise ValueError(f"gate: expected shape {(W,)} or {token} in float32 or "
+                                 f"{tuple(shape)} in bfloat16, got {tuple(gate.shape)}")
+            p_gate, kind = _rows(gate, torch.float32, token, dev, "gate"), _abi.GATE_TOKEN
     if y is None:
         for name, t in (("y2", y2), ("gate", gate), ("w_post", w_post)):
             if t is not None:
                 raise ValueError(f"{name} given, but y is None")
         if w_pre is None:
             raise ValueError("one of y and w_pre is needed")
-    _same_device(h.device, y=y, y2=y2, gate=gate, w_post=w_post, w_pre=w_pre)
-    return shape, (math.prod(shape[:-1])), W, kind
+    return ((p_h, dt),
+            (_maybe(y, torch.bfloat16, shape, dev, "y"),
+             _maybe(y2, torch.bfloat16, shape, dev, "y2"), p_gate, kind,
+             _maybe(w_post, torch.float32, (W,), dev, "w_post"),
+             _maybe(w_pre, torch.float32, (W,), dev, "w_pre")),
+            (math.prod(shape[:-1]), W))
 
 
 def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0, eps=1e-6,
@@ -743,32 +749,31 @@ def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0
     [...,W] bfloat16.  Returns (h_out in the stream's type, u in bfloat16 or
     None).  Without y the stream is only normalised and h_out is h.  h_out may
     be h (in place), u may be y or y2."""
-    shape, T, W, kind = _norm_inputs(h, y, y2, gate, w_post, w_pre)
-    dev, dt = h.device, _float_type(h, "h")
+    a0, a1, a2 = _norm_inputs(h, y, y2, gate, w_post, w_pre)
+    shape, dev = h.shape, h.device
+    p_h = p_u = None
     if y is None:
         if h_out is not None and h_out is not h:
             raise ValueError("h_out given, but y is None: the stream stays as it is")
         h_out = h
     elif h_out is None:
         h_out = torch.empty_like(h)
-    elif h_out is not h:
-        p = _dev_ptr(h_out, h.dtype, shape, "h_out")
-        _same_device(dev, h_out=h_out)
-        _apart("h_out", h_out, h=None if p == h.data_ptr() else h, y=y, y2=y2, gate=gate,
+        p_h = h_out.data_ptr()
+    else:
+        p_h = _rows(h_out, h.dtype, shape, dev, "h_out")
+        _apart("h_out", h_out, h=None if p_h == a0[0] else h, y=y, y2=y2, gate=gate,
                w_post=w_post, w_pre=w_pre)
     if w_pre is None:
         if u is not None:
             raise ValueError("u given, but w_pre is None")
     elif u is None:
-        u = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        u = torch.empty_like(h, dtype=torch.bfloat16) if y is None else torch.empty_like(y)
+        p_u = u.data_ptr()
     else:
-        p = _dev_ptr(u, torch.bfloat16, shape, "u")
-        _same_device(dev, u=u)
+        p_u = _rows(u, torch.bfloat16, shape, dev, "u")
         _apart("u", u, h=h, h_out=h_out, gate=gate, w_post=w_post, w_pre=w_pre,
-               y=None if p == _ptr(y) else y, y2=None if p == _ptr(y2) else y2)
-    _launch(dev, "moonep_block_norm", h.data_ptr(), dt, _ptr(y), _ptr(y2), _ptr(gate), kind,
-            _ptr(w_post), _ptr(w_pre), scale, eps, T, W, None if y is None else h_out.data_ptr(),
-            _ptr(u))
+               y=None if p_u == a1[0] else y, y2=None if p_u == a1[1] else y2)
+    _launch(dev, "moonep_block_norm", *a0, *a1, scale, eps, *a2, p_h, p_u)
     return h_out, u
 
 
@@ -788,45 +793,53 @@ def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pr
     where there is no such input.  need_dw=False leaves dgate, dw_post and dw_pre
     out.  dres may be dh, dy may be y, y2 or du.  ws: a workspace of
     block_norm_bwd_workspace(T, W); without one it is allocated per call."""
-    shape, T, W, kind = _norm_inputs(h, y, y2, gate, w_post, w_pre)
-    dev, dt = h.device, _float_type(h, "h")
+    a0, a1, a2 = _norm_inputs(h, y, y2, gate, w_post, w_pre)
+    shape, dev = h.shape, h.device
     if dh is None and du is None:
         raise ValueError("one of dh and du is needed")
     if (du is None) != (w_pre is None):
         raise ValueError("du and w_pre go together")
-    _dev_ptr(dh, h.dtype, shape, "dh", True)
-    _dev_ptr(du, torch.bfloat16, shape, "du", True)
-    _same_device(dev, dh=dh, du=du)
+    p_dh = _maybe(dh, h.dtype, shape, dev, "dh")
+    p_du = _maybe(du, torch.bfloat16, shape, dev, "du")
     if dres is None:
         dres = torch.empty_like(h)
+        p_dres = dres.data_ptr()
     else:
-        p = _dev_ptr(dres, h.dtype, shape, "dres")
-        _same_device(dev, dres=dres)
-        _apart("dres", dres, dh=None if p == _ptr(dh) else dh, h=h, du=du, y=y, y2=y2, gate=gate,
+        p_dres = _rows(dres, h.dtype, shape, dev, "dres")
+        _apart("dres", dres, dh=None if p_dres == p_dh else dh, h=h, du=du, y=y, y2=y2, gate=gate,
                w_post=w_post, w_pre=w_pre, ws=ws)
+    p_dy = None
     if y is None:
         if dy is not None:
             raise ValueError("dy given, but y is None")
     elif dy is None:
-        dy = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        dy = torch.empty_like(y)
+        p_dy = dy.data_ptr()
     else:
-        p = _dev_ptr(dy, torch.bfloat16, shape, "dy")
-        _same_device(dev, dy=dy)
+        p_dy = _rows(dy, torch.bfloat16, shape, dev, "dy")
         _apart("dy", dy, h=h, dh=dh, dres=dres, gate=gate, w_post=w_post, w_pre=w_pre, ws=ws,
-               **{n: None if p == _ptr(t) else t for n, t in (("du", du), ("y", y), ("y2", y2))})
-    new = lambda t: torch.empty_like(t) if need_dw and t is not None else None
-    dgate, dw_post, dw_pre = new(gate), new(w_post), new(w_pre)
+               du=None if p_dy == p_du else du, y=None if p_dy == a1[0] else y,
+               y2=None if p_dy == a1[1] else y2)
+    dgate = dw_post = dw_pre = p_dgate = p_dpost = p_dpre = None
+    if need_dw:
+        if gate is not None:
+            dgate = torch.empty_like(gate)
+            p_dgate = dgate.data_ptr()
+        if w_post is not None:
+            dw_post = torch.empty_like(w_post)
+            p_dpost = dw_post.data_ptr()
+        if w_pre is not None:
+            dw_pre = torch.empty_like(w_pre)
+            p_dpre = dw_pre.data_ptr()
+    p_ws = None
     if ws is not None:
-        _dev_ptr(ws, torch.uint8, ws.shape, "ws")
-        _same_device(dev, ws=ws)
-        _apart("ws", ws, h=h, dh=dh, du=du, y=y, y2=y2, gate=gate, w_post=w_post, w_pre=w_pre)
-    elif dw_post is not None or dw_pre is not None or (dgate is not None and
-                                                       kind == _abi.GATE_CHANNEL):
-        ws = block_norm_bwd_workspace(T, W, device=dev)
-    _launch(dev, "moonep_block_norm_bwd", h.data_ptr(), dt, _ptr(dh), _ptr(du), _ptr(y), _ptr(y2),
-            _ptr(gate), kind, _ptr(w_post), _ptr(w_pre), scale, eps, T, W, dres.data_ptr(),
-            _ptr(dy), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
-            0 if ws is None else ws.numel())
+        p_ws = _ws_ptr(ws, dev, h=h, dh=dh, du=du, y=y, y2=y2, gate=gate, w_post=w_post,
+                       w_pre=w_pre)
+    elif p_dpost or p_dpre or (p_dgate and a1[3] == _abi.GATE_CHANNEL):
+        ws = block_norm_bwd_workspace(*a2, device=dev)
+        p_ws = ws.data_ptr()
+    _launch(dev, "moonep_block_norm_bwd", *a0, p_dh, p_du, *a1, scale, eps, *a2, p_dres, p_dy,
+            p_dgate, p_dpost, p_dpre, p_ws, 0 if ws is None else ws.numel())
     return dres, dy, dgate, dw_post, dw_pre
 
 

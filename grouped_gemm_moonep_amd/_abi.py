@@ -58,7 +58,7 @@ def lib():
         pass
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
-    P3 = ctypes.c_void_p * 3
+    P3 = PTR3
     sig = {
         "moonep_abi_version": (i32, []),
         "moonep_status_string": (ctypes.c_char_p, [i32]),
@@ -155,6 +155,9 @@ TILE_64, TILE_128_DEEP, TILE_128, TILE_128X256, TILE_256 = range(5)
 def launch_grid(cfg: MoonepConfig, which: int, W: int = 0, device_cus: int = 256) -> int:
     """Workgroups a data-movement call would launch (host only)."""
     return int(lib().moonep_launch_grid(ctypes.byref(cfg), which, W, device_cus))
+
+
+PTR3 = ctypes.c_void_p * 3
 
 
 def ptr3(ts):

@@ -26,7 +26,6 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kMaxWaves = 16;      // per workgroup
 constexpr int kVals = 3;           // sums taken together
 
 __device__ __forceinline__ unsigned pack2(float lo, float hi) {
@@ -55,12 +54,22 @@ template <> struct Raw<float> {
   __device__ __forceinline__ void zero() { v[0] = v[1] = f32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ float get(int i) const { return v[i >> 2][i & 3]; }
 };
-__device__ __forceinline__ void store8(uint16_t* p, const float f[8]) {
-  *(u32x4*)p = u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+__device__ __forceinline__ void put8(uint16_t* p, const float f[8], bool past) {
+  const u32x4 v = {pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+  if (past) __builtin_nontemporal_store(v, (u32x4*)p);
+  else *(u32x4*)p = v;
 }
-__device__ __forceinline__ void store8(float* p, const float f[8]) {
-  *(f32x4*)p = f32x4{f[0], f[1], f[2], f[3]};
-  *(f32x4*)(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+__device__ __forceinline__ void put8(float* p, const float f[8], bool past) {
+  const f32x4 v[2] = {{f[0], f[1], f[2], f[3]}, {f[4], f[5], f[6], f[7]}};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (past) __builtin_nontemporal_store(v[i], (f32x4*)p + i);
+    else *((f32x4*)p + i) = v[i];
+  }
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float f[8]) {
+  put8(p, f, false);
 }
 
 // Sum of 16 lanes, the same in each of them.
@@ -137,39 +146,54 @@ __device__ __forceinline__ float rstd(float ss, float inv_w, float eps) {
   return 1.0f / sqrtf(ss * inv_w + eps);
 }
 
-template <class TS, int VPT, bool kWave>
-__global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(NormArgs a) {
+// A row as it is loaded.
+template <class TS, int VPT>
+struct RowIn {
+  Raw<TS> h[VPT];
+  Raw<uint16_t> y[VPT], y2[VPT], g[VPT];
+  float gt;
+  template <bool kWave>
+  __device__ __forceinline__ void load(const NormArgs& a, const Place<kWave>& at, int64_t r) {
+    gt = a.gate_kind == MOONEP_GATE_TOKEN ? ((const float*)a.gate)[r] : 1.0f;
+    const int64_t base = r * a.W;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      h[p].zero();
+      y[p].zero();
+      y2[p].zero();
+      g[p].zero();
+      if (c < a.W) {
+        h[p].load((const TS*)a.h + base + c);
+        if (a.y) y[p].load(a.y + base + c);
+        if (a.y2) y2[p].load(a.y2 + base + c);
+        if (a.gate_kind == MOONEP_GATE_FULL) g[p].load((const uint16_t*)a.gate + base + c);
+      }
+    }
+  }
+};
+
+template <class TS, int VPT, bool kWave, int kMost>
+__global__ __launch_bounds__(kMost) void norm_kernel(NormArgs a) {
   __shared__ float red[2][kVals][16];
   RowSum<kWave> sum{red, 0};
   const Place<kWave> at;
   const int W = a.W;
   const float inv_w = 1.0f / (float)W;
+  // Results that the caches cannot hold are stored past them (32768 rows of 7168 in bf16: 454 ->
+  // 442 us; the backward, stored so, 704 -> 743 us).
+  const bool past = a.T * W > (int64_t(1) << 25);
   for (int64_t r = at.row; r < a.T; r += at.step) {
     const int64_t base = r * W;
-    Raw<TS> hv[VPT];
-    Raw<uint16_t> yv[VPT], y2v[VPT], gv[VPT];
-    const float gt = a.gate_kind == MOONEP_GATE_TOKEN ? ((const float*)a.gate)[r] : 1.0f;
-#pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      const int c = 8 * (at.lane + p * at.lanes);
-      hv[p].zero();
-      yv[p].zero();
-      y2v[p].zero();
-      gv[p].zero();
-      if (c < W) {
-        hv[p].load((const TS*)a.h + base + c);
-        if (a.y) yv[p].load(a.y + base + c);
-        if (a.y2) y2v[p].load(a.y2 + base + c);
-        if (a.gate_kind == MOONEP_GATE_FULL) gv[p].load((const uint16_t*)a.gate + base + c);
-      }
-    }
+    RowIn<TS, VPT> cur;
+    cur.load(a, at, r);
     float h[VPT][8];
     float ss[1] = {0.0f};
 #pragma unroll
     for (int p = 0; p < VPT; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[p][i] = yv[p].get(i) + y2v[p].get(i);
+        h[p][i] = cur.y[p].get(i) + cur.y2[p].get(i);
         ss[0] += h[p][i] * h[p][i];
       }
     float ra = 1.0f;
@@ -177,7 +201,7 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(NormArgs a) {
       sum(ss);
       ra = rstd(ss[0], inv_w, a.eps);
     }
-    const float f = a.scale * gt;
+    const float f = a.scale * cur.gt;
     ss[0] = 0.0f;
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
@@ -192,13 +216,13 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(NormArgs a) {
             float n = h[p][i];
             if (a.w_post) n *= ra * w.get(i);
             if (a.gate_kind == MOONEP_GATE_CHANNEL) n *= g.get(i);
-            if (a.gate_kind == MOONEP_GATE_FULL) n *= gv[p].get(i);
-            h[p][i] = hv[p].get(i) + f * n;
+            if (a.gate_kind == MOONEP_GATE_FULL) n *= cur.g[p].get(i);
+            h[p][i] = cur.h[p].get(i) + f * n;
           }
-          store8((TS*)a.h_out + base + c, h[p]);
+          put8((TS*)a.h_out + base + c, h[p], past);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) h[p][i] = hv[p].get(i);
+          for (int i = 0; i < 8; ++i) h[p][i] = cur.h[p].get(i);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss[0] += h[p][i] * h[p][i];
@@ -215,18 +239,53 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(NormArgs a) {
           w.load(a.w_pre + c);
 #pragma unroll
           for (int i = 0; i < 8; ++i) h[p][i] *= rh * w.get(i);
-          store8(a.u + base + c, h[p]);
+          put8(a.u + base + c, h[p], past);
         }
       }
     }
   }
 }
 
+template <class TS, int VPT>
+struct RowBwdIn {
+  Raw<TS> h[VPT], dh[VPT];
+  Raw<uint16_t> du[VPT], y[VPT], y2[VPT], g[VPT];
+  float gt;
+  template <bool kWave>
+  __device__ __forceinline__ void load(const NormBwdArgs& a, const Place<kWave>& at, int64_t r,
+                                       bool need_a) {
+    gt = a.gate_kind == MOONEP_GATE_TOKEN ? ((const float*)a.gate)[r] : 1.0f;
+    const int64_t base = r * a.W;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      h[p].zero();
+      dh[p].zero();
+      du[p].zero();
+      y[p].zero();
+      y2[p].zero();
+      g[p].zero();
+      if (c < a.W) {
+        if (a.w_pre) {
+          h[p].load((const TS*)a.h + base + c);
+          du[p].load(a.du + base + c);
+        }
+        if (a.dh) dh[p].load((const TS*)a.dh + base + c);
+        if (need_a) {
+          y[p].load(a.y + base + c);
+          if (a.y2) y2[p].load(a.y2 + base + c);
+        }
+        if (a.gate_kind == MOONEP_GATE_FULL) g[p].load((const uint16_t*)a.gate + base + c);
+      }
+    }
+  }
+};
+
 // Sums over tokens stay in a lane's registers, for its columns, over all rows
 // of its wave or workgroup; each then writes its share to part [3][shares][W]
 // and norm_bwd_sum adds the shares, in an order that the launch fixes.
-template <class TS, int VPT, bool kWave>
-__global__ __launch_bounds__(kWave ? 256 : 1024) void norm_bwd_kernel(NormBwdArgs a) {
+template <class TS, int VPT, bool kWave, int kMost>
+__global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][kVals][16];
   RowSum<kWave> sum{red, 0};
   const Place<kWave> at;
@@ -240,31 +299,8 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_bwd_kernel(NormBwdArg
     for (int i = 0; i < 8; ++i) s_pre[p][i] = s_post[p][i] = s_gate[p][i] = 0.0f;
   for (int64_t r = at.row; r < a.T; r += at.step) {
     const int64_t base = r * W;
-    Raw<TS> hv[VPT], dhv[VPT];
-    Raw<uint16_t> duv[VPT], yv[VPT], y2v[VPT], gv[VPT];
-    const float gt = a.gate_kind == MOONEP_GATE_TOKEN ? ((const float*)a.gate)[r] : 1.0f;
-#pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      const int c = 8 * (at.lane + p * at.lanes);
-      hv[p].zero();
-      dhv[p].zero();
-      duv[p].zero();
-      yv[p].zero();
-      y2v[p].zero();
-      gv[p].zero();
-      if (c < W) {
-        if (a.w_pre) {
-          hv[p].load((const TS*)a.h + base + c);
-          duv[p].load(a.du + base + c);
-        }
-        if (a.dh) dhv[p].load((const TS*)a.dh + base + c);
-        if (need_a) {
-          yv[p].load(a.y + base + c);
-          if (a.y2) y2v[p].load(a.y2 + base + c);
-        }
-        if (a.gate_kind == MOONEP_GATE_FULL) gv[p].load((const uint16_t*)a.gate + base + c);
-      }
-    }
+    RowBwdIn<TS, VPT> cur;
+    cur.load(a, at, r, need_a);
     float d[VPT][8], av[VPT][8];
     float s3[3] = {0.0f, 0.0f, 0.0f};       // h'^2, v h', a^2
 #pragma unroll
@@ -275,9 +311,9 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_bwd_kernel(NormBwdArg
       if (a.w_pre && c < W) w.load(a.w_pre + c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h = hv[p].get(i);
-        av[p][i] = yv[p].get(i) + y2v[p].get(i);
-        d[p][i] = duv[p].get(i) * w.get(i);
+        const float h = cur.h[p].get(i);
+        av[p][i] = cur.y[p].get(i) + cur.y2[p].get(i);
+        d[p][i] = cur.du[p].get(i) * w.get(i);
         s3[0] += h * h;
         s3[1] += d[p][i] * h;
         s3[2] += av[p][i] * av[p][i];
@@ -298,9 +334,9 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_bwd_kernel(NormBwdArg
         float dg[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float h = hv[p].get(i);
-          s_pre[p][i] += duv[p].get(i) * (h * rh);
-          d[p][i] = dhv[p].get(i) + rh * (d[p][i] - h * mh);
+          const float h = cur.h[p].get(i);
+          s_pre[p][i] += cur.du[p].get(i) * (h * rh);
+          d[p][i] = cur.dh[p].get(i) + rh * (d[p][i] - h * mh);
         }
         store8((TS*)a.dres + base + c, d[p]);
 #pragma unroll
@@ -312,9 +348,9 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_bwd_kernel(NormBwdArg
           dg[i] = t;
           s_gate[p][i] += t;
           s2[0] += t;
-          float dn = sd * gt;
+          float dn = sd * cur.gt;
           if (a.gate_kind == MOONEP_GATE_CHANNEL) dn *= g.get(i);
-          if (a.gate_kind == MOONEP_GATE_FULL) dn *= gv[p].get(i);
+          if (a.gate_kind == MOONEP_GATE_FULL) dn *= cur.g[p].get(i);
           s_post[p][i] += dn * hat;
           d[p][i] = a.w_post ? dn * w.get(i) : dn;
           s2[1] += d[p][i] * av[p][i];
@@ -378,23 +414,31 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum(const float* part, int shar
   }
 }
 
-// Workgroups of a launch and the lanes of each.
+// Workgroups of a launch and the lanes of each: up to 1024 elements a wave, up to 4096 a workgroup
+// with a vector a lane, beyond two.  Workgroups per CU: as many as give it `waves` waves, one at
+// least.
 struct NormGrid {
   int vpt, threads;
   bool wave;
   int64_t blocks;
 };
-NormGrid norm_grid(int64_t T, int W, int64_t most) {
+NormGrid norm_grid(int64_t T, int W, int waves) {
   NormGrid g;
   const int vecs = W / 8;
   g.wave = vecs <= 128;
-  g.vpt = vecs <= 64 || (vecs > 128 && vecs <= 1024) ? 1 : 2;
+  g.vpt = vecs <= 64 || (vecs > 128 && vecs <= 512) ? 1 : 2;
   g.threads = g.wave ? 256 : (vecs + 64 * g.vpt - 1) / (64 * g.vpt) * 64;
   const int64_t need = g.wave ? (T + 3) / 4 : T;
+  const int per_cu = waves * 64 / g.threads;
+  const int64_t most = 256LL * (per_cu > 1 ? per_cu : 1);
   g.blocks = need < most ? need : most;
   return g;
 }
-constexpr int64_t kNormBlocks = 4096, kNormBwdBlocks = 512;
+// Forward: a row a workgroup as long as the grid is not huge (32768 rows of 7168 in bf16: 454 us,
+// with nine workgroups per CU 485 us; the next row's loads ahead of a row's sums 480 to 490 us).
+// Backward: as few workgroups as keep the CUs busy, for each leaves a share of the sums over tokens
+// (704 us with one per CU, 728 us with three).
+constexpr int kNormWaves = 2048, kNormBwdWaves = 12;
 
 }  // namespace
 
@@ -403,18 +447,19 @@ bool norm_shape_ok(int64_t T, int32_t W) {
 }
 
 int32_t norm_shares(int64_t T, int32_t W) {
-  return (int32_t)(norm_grid(T, W, kNormBwdBlocks).blocks * (W <= 1024 ? 4 : 1));
+  return (int32_t)(norm_grid(T, W, kNormBwdWaves).blocks * (W <= 1024 ? 4 : 1));
 }
 
 int64_t norm_ws_bytes(int64_t T, int32_t W) { return 3LL * norm_shares(T, W) * W * 4; }
 
 template <class TS>
 static hipError_t norm_as(const NormArgs& a, hipStream_t s) {
-  const NormGrid g = norm_grid(a.T, a.W, kNormBlocks);
-  if (g.wave && g.vpt == 1) norm_kernel<TS, 1, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else if (g.wave) norm_kernel<TS, 2, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else if (g.vpt == 1) norm_kernel<TS, 1, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else norm_kernel<TS, 2, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  const NormGrid g = norm_grid(a.T, a.W, kNormWaves);
+  if (g.wave && g.vpt == 1) norm_kernel<TS, 1, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.wave) norm_kernel<TS, 2, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.vpt == 1) norm_kernel<TS, 1, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.threads <= 512) norm_kernel<TS, 2, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else norm_kernel<TS, 2, false, 1024><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -424,12 +469,13 @@ hipError_t launch_norm(const NormArgs& a, int32_t dtype, hipStream_t s) {
 
 template <class TS>
 static hipError_t norm_bwd_as(const NormBwdArgs& a, hipStream_t s) {
-  const NormGrid g = norm_grid(a.T, a.W, kNormBwdBlocks);
+  const NormGrid g = norm_grid(a.T, a.W, kNormBwdWaves);
   if (g.blocks == 0) {}                              // no tokens: the sums below are zeros
-  else if (g.wave && g.vpt == 1) norm_bwd_kernel<TS, 1, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else if (g.wave) norm_bwd_kernel<TS, 2, true><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else if (g.vpt == 1) norm_bwd_kernel<TS, 1, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else norm_bwd_kernel<TS, 2, false><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.wave && g.vpt == 1) norm_bwd_kernel<TS, 1, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.wave) norm_bwd_kernel<TS, 2, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.vpt == 1) norm_bwd_kernel<TS, 1, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.threads <= 512) norm_bwd_kernel<TS, 2, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else norm_bwd_kernel<TS, 2, false, 1024><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   float* dgate = a.gate_kind == MOONEP_GATE_CHANNEL ? (float*)a.dgate : nullptr;
   if (a.dw_pre || a.dw_post || dgate) {
     norm_bwd_sum<<<dim3((unsigned)((a.W + 63) / 64), 3), 1024, 0, s>>>(a.part, a.shares, a.W,

@@ -172,12 +172,12 @@ __device__ __forceinline__ void small_loop(const TA& la, const TB& lb, lds_t* ld
 }
 
 // Rows of a small tile by template: waves 2 x 2 with (BM / 64) x 2 blocks each,
-// or, at 32 rows, one block of 32 columns each.
-template <int BM>
+// or, at 32 rows, one block of 32 columns each.  DEEP: twice the stages, for
+// launches that leave a CU one workgroup.
+template <int BM, bool DEEP>
 struct Small {
   static constexpr int MI = BM == 128 ? 2 : 1, NJ = BM == 32 ? 1 : 2;
-  static constexpr int DEPTH = BM == 128 ? 2 : BM == 64 ? 3 : 4;
-  static constexpr int NL = BM / 32;
+  static constexpr int DEPTH = (BM == 128 ? 2 : BM == 64 ? 3 : 4) * (DEEP ? 2 : 1);
   static constexpr int kLds = DEPTH * (BM * 128 + 16384);
   int arow0;
   int nrow[NJ];          // the first 32 columns of a pair lie in region 0, the second in region 1
@@ -226,18 +226,17 @@ template <int BM> struct SmallTiles<OP_WGRAD, BM> { typedef ColTile64 A; typedef
 // (columns: G, U and dZ side by side for OP_GATEUP and OP_GRAD; OP_WGRAD has
 // [S][3][M][N]).  Otherwise the tile is finished here: OP_GATEUP writes Z,
 // OP_ROWS and OP_ROWS2 bf16 (+ add), OP_WGRAD bf16 or adds to fp32.
-template <int OP, int BM, bool PART>
-__global__ __launch_bounds__(kThreads, 2) void small_kernel(SmallArgs a) {
-  typedef Small<BM> G;
+template <int OP, int BM, bool PART, bool DEEP>
+__device__ __forceinline__ void small_tile(const SmallArgs& a, unsigned block, char* smem) {
+  typedef Small<BM, DEEP> G;
   typedef typename SmallTiles<OP, BM>::A TA;
   typedef typename SmallTiles<OP, BM>::B TB;
   constexpr int MI = G::MI, NJ = G::NJ;
-  __shared__ __attribute__((aligned(16))) char smem[G::kLds];
   const G g;
   // each XCD takes a run of tiles: M fastest (they share the weights), then N, then the split
   const int64_t total = (int64_t)a.ntm * a.ntn * a.S, per = (total + kXcds - 1) / kXcds;
-  const int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  if (blockIdx.x / kXcds >= per || l >= total) return;
+  const int64_t l = (int64_t)(block % kXcds) * per + block / kXcds;
+  if (block / kXcds >= per || l >= total) return;
   const int tm = (int)(l % a.ntm);
   int tn = (int)(l / a.ntm % a.ntn);
   const int sp = (int)(l / ((int64_t)a.ntm * a.ntn));
@@ -350,29 +349,137 @@ __global__ __launch_bounds__(kThreads, 2) void small_kernel(SmallArgs a) {
   }
 }
 
-// ------------------------------------------------------------- joins
-// Four neighbouring elements of every split, added in the splits' order.
-__device__ __forceinline__ f32x4 add_splits(const float* p, int S, int64_t slab) {
-  f32x4 v = *(const f32x4*)p;
-  for (int s = 1; s < S; ++s) v += *(const f32x4*)(p + s * slab);
-  return v;
+template <int OP, int BM, bool PART, bool DEEP>
+__global__ __launch_bounds__(kThreads, DEEP ? 1 : 2) void small_kernel(SmallArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Small<BM, DEEP>::kLds];
+  small_tile<OP, BM, PART, DEEP>(a, blockIdx.x, smem);
 }
+
+// dX and the weight gradients, which both need dG and dU and not each other, in
+// one launch: the first nx workgroups are dX's.
+template <int BM>
+__global__ __launch_bounds__(kThreads, 2) void small_last(SmallArgs x, SmallArgs w, unsigned nx) {
+  constexpr int kX = Small<BM, false>::kLds, kW = Small<128, false>::kLds;
+  __shared__ __attribute__((aligned(16))) char smem[kX > kW ? kX : kW];
+  if (blockIdx.x < nx) small_tile<OP_ROWS2, BM, false, false>(x, blockIdx.x, smem);
+  else small_tile<OP_WGRAD, 128, false, false>(w, blockIdx.x - nx, smem);
+}
+
+// Z Wd^T (+ add) of up to 32 tokens without splits between workgroups: a
+// workgroup takes 32 rows of Wd and its four waves every fourth 64 values of K,
+// each with stages of its own, so that nothing but its own loads holds a wave up
+// until the four sums are added in LDS.
+struct Wave32 {
+  static constexpr int kDepth = 4, kStage = 4 * 8192;        // A and B of each wave
+  static constexpr int kLds = kDepth * kStage;
+};
+__global__ __launch_bounds__(kThreads, 1) void few_rows(SmallArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[Wave32::kLds];
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  const int n0 = blockIdx.x * 32, blocks = a.K / BK, steps = (blocks + 3) / 4;
+  const DmaRsrc ra = make_dma_rsrc(a.a[0], (int64_t)a.M * a.K * 2);
+  const DmaRsrc rb = make_dma_rsrc(a.b[0] + (int64_t)n0 * a.K, 32LL * a.K * 2);
+  // as RowTileT: load i holds rows 8 i .. 8 i + 7
+  const int r = lane >> 3, c = (lane & 7) ^ RowTile::swz(r);
+  const uint32_t voff[2] = {(uint32_t)(r * a.K * 2 + c * 16), (uint32_t)(r * a.K * 2 + (c ^ 4) * 16)};
+  lds_t* mine = (lds_t*)smem + w * 8192;
+  auto issue = [&](int j) {
+    const int b = 4 * j + w;
+    const uint32_t ko = b < blocks ? (uint32_t)(b * BK * 2) : kOob;
+    lds_t* to = mine + (j % Wave32::kDepth) * Wave32::kStage;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = voff[i & 1] + (ko + (uint32_t)(16 * i * a.K));
+      load_lds(ra, to + i * 1024, at);
+      load_lds(rb, to + 4096 + i * 1024, at);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < Wave32::kDepth - 1; ++j) issue(j);
+  f32x16 acc;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+  for (int j = 0; j < steps; ++j) {
+    wait_vm<(Wave32::kDepth - 2) * 8>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // step j - 1 is read
+    issue(j + Wave32::kDepth - 1);
+    const lds_t* A = mine + (j % Wave32::kDepth) * Wave32::kStage;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(RowTile::frag(A + 4096, lr, kk, lh),
+                                                    RowTile::frag(A, lr, kk, lh), acc, 0, 0, 0);
+  }
+  wait_vm<0>();
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  // rows of 32 sums and a gap: 36 words
+  __attribute__((address_space(3))) float* sums = (__attribute__((address_space(3))) float*)mine;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *(__attribute__((address_space(3))) f32x4*)(sums + lr * 36 + acc_col(q, lh)) =
+        f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+  __syncthreads();
+  const int m = threadIdx.x >> 3, col = 4 * (threadIdx.x & 7);
+  if (m >= a.M) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const f32x4 t = *(const __attribute__((address_space(3))) f32x4*)(
+        (const __attribute__((address_space(3))) float*)((lds_t*)smem + s * 8192) + m * 36 + col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += t[e];
+  }
+  const int64_t at = (int64_t)m * a.N + n0 + col;
+  if (a.add) {
+    const u32x2 d = *(const u32x2*)(a.add + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += bf16_of(d[e >> 1], e & 1);
+  }
+  *(u32x2*)((uint16_t*)a.out[0] + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// ------------------------------------------------------------- joins
+// Four neighbouring elements of every split of NP products (at p + i step),
+// added in the splits' order; eight splits' loads are in flight together (one
+// at a time 16 of them took 9 us for 8 tokens).
+template <int NP>
+__device__ __forceinline__ void add_splits(f32x4 (&v)[NP], const float* p, int64_t step, int S,
+                                           int64_t slab) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) v[i] = f32x4{0, 0, 0, 0};
+  for (int s0 = 0; s0 < S; s0 += 8) {
+    f32x4 t[8][NP];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k == 0 || s0 + k < S) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) t[k][i] = *(const f32x4*)(p + (s0 + k) * slab + i * step);
+      }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k == 0 || s0 + k < S) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][e] += t[k][i][e];
+      }
+  }
+}
+constexpr int kJoin = 64;      // threads of a joining workgroup
 __device__ __forceinline__ u32x2 pack4(const float v[4]) {
   return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 // z [M,N] from part [S][M][2N]; with dZ (part [S][M][3N]) dg, du and z.
 template <bool GRAD>
-__global__ __launch_bounds__(256) void join_gate(const float* part, int S, int M, int N, int act,
+__global__ __launch_bounds__(kJoin) void join_gate(const float* part, int S, int M, int N, int act,
                                                  uint16_t* z, uint16_t* dg, uint16_t* du) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t i = ((int64_t)blockIdx.x * kJoin + threadIdx.x) * 4;
   if (i >= (int64_t)M * N) return;
   const int64_t m = i / N, n = i % N, cols = (GRAD ? 3LL : 2LL) * N, slab = (int64_t)M * cols;
-  const float* p = part + m * cols + n;
-  const f32x4 g = add_splits(p, S, slab), u = add_splits(p + N, S, slab);
+  f32x4 v[GRAD ? 3 : 2];
+  add_splits(v, part + m * cols + n, N, S, slab);
+  const f32x4 g = v[0], u = v[1], dz = v[GRAD ? 2 : 0];
   float zv[4], dgv[4], duv[4];
-  f32x4 dz = {0, 0, 0, 0};
-  if constexpr (GRAD) dz = add_splits(p + 2 * N, S, slab);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const Act t = activate(act, g[e]);
@@ -388,14 +495,15 @@ __global__ __launch_bounds__(256) void join_gate(const float* part, int S, int M
 }
 
 // out [n] bf16 from part [S][n] (+ add)
-__global__ __launch_bounds__(256) void join_rows(const float* part, int S, int64_t n,
+__global__ __launch_bounds__(kJoin) void join_rows(const float* part, int S, int64_t n,
                                                  const uint16_t* add, uint16_t* out) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t i = ((int64_t)blockIdx.x * kJoin + threadIdx.x) * 4;
   if (i >= n) return;
-  const f32x4 s = add_splits(part + i, S, n);
+  f32x4 s[1];
+  add_splits(s, part + i, 0, S, n);
   float v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = s[e];
+  for (int e = 0; e < 4; ++e) v[e] = s[0][e];
   if (add) {
     const u32x2 d = *(const u32x2*)(add + i);
 #pragma unroll
@@ -408,19 +516,23 @@ __global__ __launch_bounds__(256) void join_rows(const float* part, int S, int64
 struct JoinW {
   void* out[3];
 };
-__global__ __launch_bounds__(256) void join_wgrad(const float* part, int S, int64_t n, int f32,
+__global__ __launch_bounds__(kJoin) void join_wgrad(const float* part, int S, int64_t n, int f32,
                                                   JoinW w) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t i = ((int64_t)blockIdx.x * kJoin + threadIdx.x) * 4;
   if (i >= n) return;
   const int p = blockIdx.y;
-  const f32x4 s = add_splits(part + p * n + i, S, 3 * n);
+  f32x4 s[1];
+  add_splits(s, part + p * n + i, 0, S, 3 * n);
   if (f32) {
     f32x4* o = (f32x4*)((float*)w.out[p] + i);
-    *o += s;
+    f32x4 t = *o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] += s[0][e];
+    *o = t;
   } else {
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = s[e];
+    for (int e = 0; e < 4; ++e) v[e] = s[0][e];
     *(u32x2*)((uint16_t*)w.out[p] + i) = pack4(v);
   }
 }
@@ -747,6 +859,14 @@ struct Shape {
   int rows, ntm, ntn, S;
 };
 
+// Splits of nk steps for so many tiles: two workgroups per CU, at least four steps each.  Twelve
+// steps are done before another launch could have joined them.
+int splits(int64_t tiles, int nk) {
+  int64_t S = ceil_div(512, tiles);
+  if (S > nk / 4) S = nk / 4;
+  return (int)(S < 1 || nk <= 12 ? 1 : S);
+}
+
 // M x N outputs (in tiles of small_n and large_n columns), K in steps of 64.
 Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk) {
   Shape s;
@@ -763,10 +883,7 @@ Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk) {
   s.rows = M <= 32 ? 32 : M <= 64 ? 64 : 128;
   s.ntm = (int)ceil_div(M, s.rows);
   s.ntn = (int)cols_small;
-  const int64_t tiles = (int64_t)s.ntm * s.ntn;
-  int64_t S = ceil_div(512, tiles);
-  if (S > nk / 4) S = nk / 4;
-  s.S = (int)(S < 1 ? 1 : S);
+  s.S = splits((int64_t)s.ntm * s.ntn, nk);
   return s;
 }
 Shape gateup_shape(int64_t T, int H, int Hp) {
@@ -792,12 +909,13 @@ Shape wgrad_shape(int64_t T, int H, int Hp) {
   s.ntn = (int)ceil_div(Hp, s.rows);
   if (!s.large) {
     s.ntn *= 3;
-    int64_t S = ceil_div(512, (int64_t)s.ntm * s.ntn);
-    if (S > nk / 4) S = nk / 4;
-    s.S = (int)(S < 1 ? 1 : S);
+    s.S = splits((int64_t)s.ntm * s.ntn, nk);
   }
   return s;
 }
+
+// Whether few_rows takes the down product: its 32 rows of Wd a workgroup have to fill the CUs.
+bool few(int64_t T, int H) { return T <= 32 && H / 32 >= 128; }
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -837,28 +955,40 @@ BwdWs bwd_ws(int64_t T, int H, int Hp) {
 unsigned blocks_of(const Shape& s) {
   return (unsigned)(ceil_div((int64_t)s.ntm * s.ntn * s.S, kXcds) * kXcds);
 }
-unsigned joins(int64_t n) { return (unsigned)ceil_div(n, 1024); }
+unsigned joins(int64_t n) { return (unsigned)ceil_div(n, 4 * kJoin); }
 
-template <int OP>
-void run_small(const Shape& s, bool part, SmallArgs a, hipStream_t st) {
+SmallArgs with_shape(SmallArgs a, const Shape& s) {
   a.ntm = s.ntm;
   a.ntn = s.ntn;
   a.S = s.S;
-  const unsigned n = blocks_of(s);
+  return a;
+}
+
+// One workgroup per CU at most: deep rings.
+bool deep(const Shape& s) { return (int64_t)s.ntm * s.ntn * s.S <= 256; }
+
+template <int OP, int BM, bool PART>
+void run_small_as(const Shape& s, const SmallArgs& a, hipStream_t st) {
+  if (deep(s)) small_kernel<OP, BM, PART, true><<<blocks_of(s), kThreads, 0, st>>>(a);
+  else small_kernel<OP, BM, PART, false><<<blocks_of(s), kThreads, 0, st>>>(a);
+}
+template <int OP>
+void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
+  const SmallArgs a = with_shape(in, s);
+  constexpr bool kPart = OP == OP_GRAD;            // always in parts
+  constexpr bool kPart32 = kPart || OP == OP_GATEUP;
   if constexpr (OP == OP_WGRAD) {
-    if (part) small_kernel<OP, 128, true><<<n, kThreads, 0, st>>>(a);
-    else small_kernel<OP, 128, false><<<n, kThreads, 0, st>>>(a);
+    if (part) run_small_as<OP, 128, true>(s, a, st);
+    else run_small_as<OP, 128, false>(s, a, st);
   } else if (s.rows == 128) {
-    if (part || OP == OP_GRAD) small_kernel<OP, 128, true><<<n, kThreads, 0, st>>>(a);
-    else if constexpr (OP != OP_GRAD) small_kernel<OP, 128, false><<<n, kThreads, 0, st>>>(a);
+    if (part || kPart) run_small_as<OP, 128, true>(s, a, st);
+    else run_small_as<OP, 128, kPart>(s, a, st);
   } else if (s.rows == 64) {
-    if (part || OP == OP_GRAD) small_kernel<OP, 64, true><<<n, kThreads, 0, st>>>(a);
-    else if constexpr (OP != OP_GRAD) small_kernel<OP, 64, false><<<n, kThreads, 0, st>>>(a);
+    if (part || kPart) run_small_as<OP, 64, true>(s, a, st);
+    else run_small_as<OP, 64, kPart>(s, a, st);
   } else {
-    if (part || OP == OP_GRAD || OP == OP_GATEUP)
-      small_kernel<OP, 32, true><<<n, kThreads, 0, st>>>(a);
-    else if constexpr (OP != OP_GRAD && OP != OP_GATEUP)
-      small_kernel<OP, 32, false><<<n, kThreads, 0, st>>>(a);
+    if (part || kPart32) run_small_as<OP, 32, true>(s, a, st);
+    else run_small_as<OP, 32, kPart32>(s, a, st);
   }
 }
 
@@ -906,7 +1036,7 @@ hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int3
     a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
     const bool p = g.S > 1 || g.rows == 32;
     run_small<OP_GATEUP>(g, p, a, s);
-    if (p) join_gate<false><<<joins(T * Hp), 256, 0, s>>>(part, g.S, (int)T, Hp, act, z, nullptr,
+    if (p) join_gate<false><<<joins(T * Hp), kJoin, 0, s>>>(part, g.S, (int)T, Hp, act, z, nullptr,
                                                          nullptr);
   }
   if (d.large) {
@@ -915,8 +1045,12 @@ hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int3
     SmallArgs a = {};
     a.a[0] = z; a.b[0] = w[2]; a.out[0] = y; a.add = add;
     a.part = part; a.M = (int)T; a.N = H; a.K = Hp;
+    if (few(T, H)) {
+      few_rows<<<H / 32, kThreads, 0, s>>>(a);
+      return hipGetLastError();
+    }
     run_small<OP_ROWS>(d, d.S > 1, a, s);
-    if (d.S > 1) join_rows<<<joins(T * H), 256, 0, s>>>(part, d.S, T * H, add, y);
+    if (d.S > 1) join_rows<<<joins(T * H), kJoin, 0, s>>>(part, d.S, T * H, add, y);
   }
   return hipGetLastError();
 }
@@ -957,17 +1091,30 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
     a.a[0] = x; a.a[2] = dy; a.b[0] = w[0]; a.b[1] = w[1]; a.b[2] = w[2];
     a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
     run_small<OP_GRAD>(g, true, a, s);
-    join_gate<true><<<joins(T * Hp), 256, 0, s>>>(part, g.S, (int)T, Hp, act, big.z, big.dg, big.du);
+    join_gate<true><<<joins(T * Hp), kJoin, 0, s>>>(part, g.S, (int)T, Hp, act, big.z, big.dg, big.du);
+  }
+  SmallArgs xa = {}, wa = {};
+  xa.a[0] = big.dg; xa.a[1] = big.du; xa.b[0] = w[0]; xa.b[1] = w[1]; xa.out[0] = dx;
+  xa.part = part; xa.M = (int)T; xa.N = H; xa.K = 2 * Hp;
+  wa.a[0] = wa.a[1] = x; wa.a[2] = dy;
+  wa.b[0] = big.dg; wa.b[1] = big.du; wa.b[2] = big.z;
+  wa.part = part; wa.M = H; wa.N = Hp; wa.K = (int)T; wa.f32 = big.f32;
+  JoinW j;
+  for (int i = 0; i < 3; ++i) wa.out[i] = j.out[i] = big.dw[i];
+  if (dx && dw && !dxs.large && dxs.S == 1 && !ws_.large && ws_.S == 1) {
+    const SmallArgs ax = with_shape(xa, dxs), aw = with_shape(wa, ws_);
+    const unsigned nx = blocks_of(dxs), n = nx + blocks_of(ws_);
+    if (dxs.rows == 128) small_last<128><<<n, kThreads, 0, s>>>(ax, aw, nx);
+    else if (dxs.rows == 64) small_last<64><<<n, kThreads, 0, s>>>(ax, aw, nx);
+    else small_last<32><<<n, kThreads, 0, s>>>(ax, aw, nx);
+    return hipGetLastError();
   }
   if (dx) {
     if (dxs.large) {
       MOONEP_RUN_LARGE(large_dx, dxs, big);
     } else {
-      SmallArgs a = {};
-      a.a[0] = big.dg; a.a[1] = big.du; a.b[0] = w[0]; a.b[1] = w[1]; a.out[0] = dx;
-      a.part = part; a.M = (int)T; a.N = H; a.K = 2 * Hp;
-      run_small<OP_ROWS2>(dxs, dxs.S > 1, a, s);
-      if (dxs.S > 1) join_rows<<<joins(T * H), 256, 0, s>>>(part, dxs.S, T * H, nullptr, dx);
+      run_small<OP_ROWS2>(dxs, dxs.S > 1, xa, s);
+      if (dxs.S > 1) join_rows<<<joins(T * H), kJoin, 0, s>>>(part, dxs.S, T * H, nullptr, dx);
     }
   }
   if (dw) {
@@ -977,16 +1124,10 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
       a.ntn = ws_.ntn;
       large_wgrad<<<(unsigned)(ceil_div(3LL * a.ntm * a.ntn, kXcds) * kXcds), kThreads, 0, s>>>(a);
     } else {
-      SmallArgs a = {};
-      a.a[0] = a.a[1] = x; a.a[2] = dy;
-      a.b[0] = big.dg; a.b[1] = big.du; a.b[2] = big.z;
-      JoinW j;
-      for (int i = 0; i < 3; ++i) a.out[i] = j.out[i] = dw[i];
-      a.part = part; a.M = H; a.N = Hp; a.K = (int)T; a.f32 = big.f32;
-      run_small<OP_WGRAD>(ws_, ws_.S > 1, a, s);
+      run_small<OP_WGRAD>(ws_, ws_.S > 1, wa, s);
       const int64_t n = (int64_t)H * Hp;
       if (ws_.S > 1)
-        join_wgrad<<<dim3(joins(n), 3), 256, 0, s>>>(part, ws_.S, n, big.f32, j);
+        join_wgrad<<<dim3(joins(n), 3), kJoin, 0, s>>>(part, ws_.S, n, big.f32, j);
     }
   }
   return hipGetLastError();
