@@ -598,10 +598,16 @@ def _workspace(name, nbytes, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _ws_ptr(ws, dev, **inputs):
-    p = _rows(ws, torch.uint8, ws.shape, dev, "ws")
-    _apart("ws", ws, **inputs)
-    return p
+def _disjoint(outs, ins, instead=()):
+    """Names what overlaps after the library has refused it: every tensor of `outs` has to lie apart
+    from the inputs and the other outputs; `instead`: pairs (output, input) that may start alike."""
+    done = {}
+    for name, t in outs.items():
+        if t is not None:
+            free = {n for o, n in instead if o == name and ins[n] is not None and
+                    ins[n].data_ptr() == t.data_ptr()}
+            _apart(name, t, **{n: i for n, i in ins.items() if n not in free}, **done)
+            done[name] = t
 
 
 def _ffn_inputs(x, weights, act):
@@ -646,15 +652,19 @@ def shared_ffn(x, weights, act="silu", add=None, out=None, ws=None):
         ws = shared_ffn_workspace(T, H, Hp, device=dev)
         p_ws = ws.data_ptr()
     else:
-        p_ws = _ws_ptr(ws, dev, x=x, gate=weights[0], up=weights[1], down=weights[2], add=add)
+        p_ws = _rows(ws, torch.uint8, ws.shape, dev, "ws")
     if out is None:
         out = torch.empty_like(x)
         p = out.data_ptr()
     else:
         p = _rows(out, torch.bfloat16, x.shape, dev, "out")
-        _apart("out", out, x=x, gate=weights[0], up=weights[1], down=weights[2], ws=ws,
-               add=None if p == p_add else add)
-    _launch(dev, "moonep_shared_ffn", x.data_ptr(), w, kind, p_add, T, H, Hp, p, p_ws, ws.numel())
+    try:
+        _launch(dev, "moonep_shared_ffn", x.data_ptr(), w, kind, p_add, T, H, Hp, p, p_ws,
+                ws.numel())
+    except MoonepError:
+        _disjoint(dict(out=out, ws=ws), dict(x=x, gate=weights[0], up=weights[1], down=weights[2],
+                                             add=add), [("out", "add")])
+        raise
     return out
 
 
@@ -668,7 +678,6 @@ def shared_ffn_bwd(x, dy, weights, act="silu", need_dx=True, need_dw=True, dx=No
     without one it is allocated per call."""
     T, H, Hp, kind, w = _ffn_inputs(x, weights, act)
     dev = x.device
-    inputs = dict(x=x, dy=dy, gate=weights[0], up=weights[1], down=weights[2])
     p_dy = _rows(dy, torch.bfloat16, x.shape, dev, "dy")
     if (dx is not None and not need_dx) or (dw is not None and not need_dw):
         raise ValueError("dx or dw given, but need_dx or need_dw is False")
@@ -676,11 +685,10 @@ def shared_ffn_bwd(x, dy, weights, act="silu", need_dx=True, need_dw=True, dx=No
         ws = shared_ffn_bwd_workspace(T, H, Hp, device=dev)
         p_ws = ws.data_ptr()
     else:
-        p_ws = _ws_ptr(ws, dev, **inputs)
+        p_ws = _rows(ws, torch.uint8, ws.shape, dev, "ws")
     p_dx = None
     if dx is not None:
         p_dx = _rows(dx, torch.bfloat16, x.shape, dev, "dx")
-        _apart("dx", dx, ws=ws, **inputs)
     elif need_dx:
         dx = torch.empty_like(x)
         p_dx = dx.data_ptr()
@@ -691,14 +699,17 @@ def shared_ffn_bwd(x, dy, weights, act="silu", need_dx=True, need_dw=True, dx=No
         code = _float_type(dw[0], "dw[0]")
         for i, t in enumerate(dw):
             _rows(t, dw[0].dtype, (H, Hp), dev, f"dw[{i}]")
-            _apart(f"dw[{i}]", t, ws=ws, dx=dx, **inputs,
-                   **{f"dw[{j}]": dw[j] for j in range(i)})
         p_dw = _abi.ptr3(dw)
     elif need_dw:
         dw = tuple([torch.empty_like(t) for t in weights])
         p_dw = _abi.PTR3(dw[0].data_ptr(), dw[1].data_ptr(), dw[2].data_ptr())
-    _launch(dev, "moonep_shared_ffn_bwd", x.data_ptr(), p_dy, w, kind, T, H, Hp, p_dx, p_dw, code,
-            p_ws, ws.numel())
+    try:
+        _launch(dev, "moonep_shared_ffn_bwd", x.data_ptr(), p_dy, w, kind, T, H, Hp, p_dx, p_dw,
+                code, p_ws, ws.numel())
+    except MoonepError:
+        _disjoint({"dx": dx, "ws": ws, **{f"dw[{i}]": t for i, t in enumerate(dw or ())}},
+                  dict(x=x, dy=dy, gate=weights[0], up=weights[1], down=weights[2]))
+        raise
     return dx, dw
 
 
@@ -761,8 +772,6 @@ def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0
         p_h = h_out.data_ptr()
     else:
         p_h = _rows(h_out, h.dtype, shape, dev, "h_out")
-        _apart("h_out", h_out, h=None if p_h == a0[0] else h, y=y, y2=y2, gate=gate,
-               w_post=w_post, w_pre=w_pre)
     if w_pre is None:
         if u is not None:
             raise ValueError("u given, but w_pre is None")
@@ -771,9 +780,13 @@ def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0
         p_u = u.data_ptr()
     else:
         p_u = _rows(u, torch.bfloat16, shape, dev, "u")
-        _apart("u", u, h=h, h_out=h_out, gate=gate, w_post=w_post, w_pre=w_pre,
-               y=None if p_u == a1[0] else y, y2=None if p_u == a1[1] else y2)
-    _launch(dev, "moonep_block_norm", *a0, *a1, scale, eps, *a2, p_h, p_u)
+    try:
+        _launch(dev, "moonep_block_norm", *a0, *a1, scale, eps, *a2, p_h, p_u)
+    except MoonepError:
+        _disjoint(dict(h_out=None if y is None else h_out, u=u),
+                  dict(h=h, y=y, y2=y2, gate=gate, w_post=w_post, w_pre=w_pre),
+                  [("h_out", "h"), ("u", "y"), ("u", "y2")])
+        raise
     return h_out, u
 
 
@@ -806,8 +819,6 @@ def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pr
         p_dres = dres.data_ptr()
     else:
         p_dres = _rows(dres, h.dtype, shape, dev, "dres")
-        _apart("dres", dres, dh=None if p_dres == p_dh else dh, h=h, du=du, y=y, y2=y2, gate=gate,
-               w_post=w_post, w_pre=w_pre, ws=ws)
     p_dy = None
     if y is None:
         if dy is not None:
@@ -817,9 +828,6 @@ def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pr
         p_dy = dy.data_ptr()
     else:
         p_dy = _rows(dy, torch.bfloat16, shape, dev, "dy")
-        _apart("dy", dy, h=h, dh=dh, dres=dres, gate=gate, w_post=w_post, w_pre=w_pre, ws=ws,
-               du=None if p_dy == p_du else du, y=None if p_dy == a1[0] else y,
-               y2=None if p_dy == a1[1] else y2)
     dgate = dw_post = dw_pre = p_dgate = p_dpost = p_dpre = None
     if need_dw:
         if gate is not None:
@@ -833,13 +841,18 @@ def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pr
             p_dpre = dw_pre.data_ptr()
     p_ws = None
     if ws is not None:
-        p_ws = _ws_ptr(ws, dev, h=h, dh=dh, du=du, y=y, y2=y2, gate=gate, w_post=w_post,
-                       w_pre=w_pre)
+        p_ws = _rows(ws, torch.uint8, ws.shape, dev, "ws")
     elif p_dpost or p_dpre or (p_dgate and a1[3] == _abi.GATE_CHANNEL):
         ws = block_norm_bwd_workspace(*a2, device=dev)
         p_ws = ws.data_ptr()
-    _launch(dev, "moonep_block_norm_bwd", *a0, p_dh, p_du, *a1, scale, eps, *a2, p_dres, p_dy,
-            p_dgate, p_dpost, p_dpre, p_ws, 0 if ws is None else ws.numel())
+    try:
+        _launch(dev, "moonep_block_norm_bwd", *a0, p_dh, p_du, *a1, scale, eps, *a2, p_dres, p_dy,
+                p_dgate, p_dpost, p_dpre, p_ws, 0 if ws is None else ws.numel())
+    except MoonepError:
+        _disjoint(dict(ws=ws, dres=dres, dy=dy),
+                  dict(h=h, dh=dh, du=du, y=y, y2=y2, gate=gate, w_post=w_post, w_pre=w_pre),
+                  [("dres", "dh"), ("dy", "du"), ("dy", "y"), ("dy", "y2")])
+        raise
     return dres, dy, dgate, dw_post, dw_pre
 
 

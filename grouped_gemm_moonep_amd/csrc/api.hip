@@ -347,6 +347,28 @@ static bool views_ok(const uint16_t* const views[3], int p0, int p1) {
   return true;
 }
 
+// A range of device memory, for the checks of what must not overlap.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// Every one of `out` lies apart from every one of `in` and from the other outputs (NULLs aside).
+static bool apart(const Span* out, int nout, const Span* in, int nin) {
+  auto clash = [](const Span& a, const Span& b) {
+    const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p;
+    return p && q && p < q + (uintptr_t)b.bytes && q < p + (uintptr_t)a.bytes;
+  };
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (clash(out[i], in[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (clash(out[i], out[j])) return false;
+  }
+  return true;
+}
+// An input that the output at `out` may replace in place: not looked at if it starts there too.
+static const void* unless(const void* in, const void* out) { return in == out ? nullptr : in; }
+
 static bool ffn_form_ok(const uint16_t* const w[3], int32_t act) {
   return w && (act == MOONEP_ACT_SILU || act == MOONEP_ACT_GELU_TANH) && views_ok(w, 0, 3);
 }
@@ -364,10 +386,11 @@ moonep_status_t moonep_shared_ffn(const uint16_t* x, const uint16_t* const w[3],
   if (!x || !y || !ws || !aligned(x, 16) || !aligned(y, 16) || !aligned(add, 16) ||
       !aligned(ws, 256))
     return MOONEP_ERR_ARG;
-  const void* in[] = {x, w[0], w[1], w[2], ws};
-  for (const void* p : in)
-    if (p == (const void*)y) return MOONEP_ERR_ARG;
-  if (ws_bytes < shared_ffn_ws_bytes(T, H, Hp)) return MOONEP_ERR_SCRATCH;
+  const int64_t need = shared_ffn_ws_bytes(T, H, Hp), rows = T * H * 2, wb = (int64_t)H * Hp * 2;
+  if (ws_bytes < need) return MOONEP_ERR_SCRATCH;
+  const Span out[] = {{y, rows}, {ws, need}};
+  const Span in[] = {{x, rows}, {w[0], wb}, {w[1], wb}, {w[2], wb}, {unless(add, y), rows}};
+  if (!apart(out, 2, in, 5)) return MOONEP_ERR_ARG;
   return hip_status(launch_shared_ffn(x, w, act, add, T, H, Hp, y, (char*)ws, stream));
 }
 
@@ -389,15 +412,13 @@ moonep_status_t moonep_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
     if (!x || !dy || !ws || !aligned(x, 16) || !aligned(dy, 16) || !aligned(dx, 16) ||
         !aligned(ws, 256))
       return MOONEP_ERR_ARG;
-    const void* in[] = {x, dy, w[0], w[1], w[2], ws};
-    const void* out[] = {dx, dw ? dw[0] : nullptr, dw ? dw[1] : nullptr, dw ? dw[2] : nullptr};
-    for (int i = 0; i < 4; ++i) {
-      for (const void* p : in)
-        if (out[i] == p) return MOONEP_ERR_ARG;
-      for (int j = 0; out[i] && j < i; ++j)
-        if (out[i] == out[j]) return MOONEP_ERR_ARG;
-    }
-    if (ws_bytes < shared_ffn_bwd_ws_bytes(T, H, Hp)) return MOONEP_ERR_SCRATCH;
+    const int64_t need = shared_ffn_bwd_ws_bytes(T, H, Hp), rows = T * H * 2;
+    const int64_t wb = (int64_t)H * Hp * 2, gb = dw_dtype == MOONEP_F32 ? 2 * wb : wb;
+    if (ws_bytes < need) return MOONEP_ERR_SCRATCH;
+    const Span out[] = {{dx, rows}, {ws, need}, {dw ? dw[0] : nullptr, gb},
+                        {dw ? dw[1] : nullptr, gb}, {dw ? dw[2] : nullptr, gb}};
+    const Span in[] = {{x, rows}, {dy, rows}, {w[0], wb}, {w[1], wb}, {w[2], wb}};
+    if (!apart(out, 5, in, 5)) return MOONEP_ERR_ARG;
   }
   return hip_status(launch_shared_ffn_bwd(x, dy, w, act, T, H, Hp, dx, dw, dw_dtype, (char*)ws,
                                           stream));
@@ -415,6 +436,11 @@ static bool norm_form_ok(int64_t T, int32_t dtype, const void* y, const void* y2
   if ((gate == nullptr) != (gate_kind == MOONEP_GATE_NONE)) return false;
   if (!y && (y2 || gate || w_post)) return false;
   return y || w_pre;
+}
+
+static int64_t gate_bytes(int32_t kind, int64_t T, int64_t W) {
+  return kind == MOONEP_GATE_CHANNEL ? 4 * W : kind == MOONEP_GATE_TOKEN ? 4 * T
+         : kind == MOONEP_GATE_FULL ? 2 * T * W : 0;
 }
 
 static bool all_aligned(const void* const* p, int n, size_t a) {
@@ -437,7 +463,13 @@ moonep_status_t moonep_block_norm(const void* h, int32_t dtype, const uint16_t* 
   const void* p[] = {h, y, y2, gate, w_post, w_pre, h_out, u};
   if (gate_kind == MOONEP_GATE_TOKEN) p[3] = nullptr;      // read a number at a time
   if (!all_aligned(p, 8, 16) || !aligned(gate, 4)) return MOONEP_ERR_ARG;
-  if ((const void*)u == h || (u && (const void*)u == h_out)) return MOONEP_ERR_ARG;
+  const int64_t bf = T * W * 2, stream_b = T * W * (int64_t)type_bytes(dtype);
+  const Span out[] = {{h_out, stream_b}, {u, bf}};
+  const Span in[] = {{gate, gate_bytes(gate_kind, T, W)}, {w_post, 4LL * W}, {w_pre, 4LL * W}};
+  const Span rows_h[] = {{unless(h, h_out), stream_b}, {y, bf}, {y2, bf}};
+  const Span rows_u[] = {{h, stream_b}, {unless(y, u), bf}, {unless(y2, u), bf}};
+  if (!apart(out, 2, in, 3) || !apart(out, 1, rows_h, 3) || !apart(out + 1, 1, rows_u, 3))
+    return MOONEP_ERR_ARG;
   const NormArgs a = {h, y, y2, gate, w_post, w_pre, gate_kind, scale, eps, T, W, h_out, u};
   return hip_status(launch_norm(a, dtype, stream));
 }
@@ -464,10 +496,21 @@ moonep_status_t moonep_block_norm_bwd(const void* h, int32_t dtype, const void* 
   const void* p[] = {h, dh, du, y, y2, gate, w_post, w_pre, dres, dy, dgate, dw_post, dw_pre, ws};
   if (gate_kind == MOONEP_GATE_TOKEN) p[5] = p[10] = nullptr;
   if (!all_aligned(p, 14, 16) || !aligned(gate, 4) || !aligned(dgate, 4)) return MOONEP_ERR_ARG;
-  if (dres && (dres == dy || dres == du || dres == y || dres == h)) return MOONEP_ERR_ARG;
   const bool sums = dw_post || dw_pre || (dgate && gate_kind == MOONEP_GATE_CHANNEL);
   if (sums && T > 0 && !ws) return MOONEP_ERR_ARG;
   if (sums && ws_bytes < norm_ws_bytes(T, W)) return MOONEP_ERR_SCRATCH;
+  const int64_t bf = T * W * 2, stream_b = T * W * (int64_t)type_bytes(dtype);
+  const int64_t gb = gate_bytes(gate_kind, T, W), wb = 4LL * W;
+  const Span out[] = {{dgate, gb}, {dw_post, wb}, {dw_pre, wb},
+                      {sums ? ws : nullptr, norm_ws_bytes(T, W)}, {dres, stream_b}, {dy, bf}};
+  const Span in[] = {{gate, gb}, {w_post, wb}, {w_pre, wb}, {h, stream_b}};
+  const Span rows[] = {{dh, stream_b}, {du, bf}, {y, bf}, {y2, bf}};
+  const Span rows_h[] = {{unless(dh, dres), stream_b}, {du, bf}, {y, bf}, {y2, bf}};
+  const Span rows_y[] = {{dh, stream_b}, {unless(du, dy), bf}, {unless(y, dy), bf},
+                         {unless(y2, dy), bf}};
+  if (!apart(out, 6, in, 4) || !apart(out, 4, rows, 4) || !apart(out + 4, 1, rows_h, 4) ||
+      !apart(out + 5, 1, rows_y, 4))
+    return MOONEP_ERR_ARG;
   const NormBwdArgs a = {h, dh, du, y, y2, gate, w_post, w_pre, gate_kind, scale, eps, T, W,
                          norm_shares(T, W), dres, dy, dgate, dw_post, dw_pre,
                          sums ? (float*)ws : nullptr};

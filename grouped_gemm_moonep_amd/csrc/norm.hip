@@ -282,8 +282,8 @@ struct RowBwdIn {
 };
 
 // Sums over tokens stay in a lane's registers, for its columns, over all rows
-// of its wave or workgroup; each then writes its share to part [3][shares][W]
-// and norm_bwd_sum adds the shares, in an order that the launch fixes.
+// of its wave or workgroup; each workgroup then writes its share to part
+// [3][shares][W] and norm_bwd_sum adds the shares, in an order that T and W fix.
 template <class TS, int VPT, bool kWave, int kMost>
 __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][kVals][16];
@@ -375,16 +375,34 @@ __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
     }
   }
   if (!a.part) return;
-  const int64_t share = kWave ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int64_t slab = (int64_t)a.shares * W;
+  const bool want[3] = {a.dw_pre != nullptr, a.dw_post != nullptr,
+                        a.gate_kind == MOONEP_GATE_CHANNEL && a.dgate};
 #pragma unroll
-  for (int p = 0; p < VPT; ++p) {
-    const int c = 8 * (at.lane + p * at.lanes);
-    if (c < W) {
-      float* q = a.part + share * W + c;
-      if (a.dw_pre) store8(q, s_pre[p]);
-      if (a.dw_post) store8(q + slab, s_post[p]);
-      if (a.gate_kind == MOONEP_GATE_CHANNEL && a.dgate) store8(q + 2 * slab, s_gate[p]);
+  for (int k = 0; k < 3; ++k) {
+    if (!want[k]) continue;
+    float (*v)[8] = k == 0 ? s_pre : k == 1 ? s_post : s_gate;
+    float* q = a.part + ((int64_t)k * a.shares + blockIdx.x) * W;
+    if constexpr (kWave) {
+      // the four waves' sums leave as one share
+      __shared__ __attribute__((aligned(16))) float four[4][64 * 8 * VPT];
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) store8(&four[threadIdx.x >> 6][8 * (at.lane + 64 * p)], v[p]);
+      __syncthreads();
+      for (int c = 4 * threadIdx.x; c < W; c += 1024) {
+        f32x4 t = *(const f32x4*)&four[0][c];
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] += four[w][c + e];
+        *(f32x4*)(q + c) = t;
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+        const int c = 8 * (at.lane + p * at.lanes);
+        if (c < W) store8(q + c, v[p]);
+      }
     }
   }
 }
@@ -447,7 +465,7 @@ bool norm_shape_ok(int64_t T, int32_t W) {
 }
 
 int32_t norm_shares(int64_t T, int32_t W) {
-  return (int32_t)(norm_grid(T, W, kNormBwdWaves).blocks * (W <= 1024 ? 4 : 1));
+  return (int32_t)norm_grid(T, W, kNormBwdWaves).blocks;
 }
 
 int64_t norm_ws_bytes(int64_t T, int32_t W) { return 3LL * norm_shares(T, W) * W * 4; }

@@ -550,19 +550,22 @@ struct LargeArgs {
   uint16_t* du;
   uint16_t* dx;
   void* dw[3];
+  float* part;           // sums of the splits, fp32
   int T, H, Hp, act, f32;
-  int ntm, ntn;
+  int ntm, ntn, S;
 };
 
 struct LargeTile {
-  int m0, rows, nt;
+  int m0, rows, nt, sp;
 };
 // M-tiles of `height` rows in groups of eight, each group swept over the
 // N-tiles, as in gemm_core.h: what runs together on an XCD shares weight slabs.
 __device__ __forceinline__ bool large_tile(const LargeArgs& a, int height, LargeTile* t) {
-  const int64_t total = (int64_t)a.ntm * a.ntn, per = (total + kXcds - 1) / kXcds;
-  const int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  const int64_t each = (int64_t)a.ntm * a.ntn, total = each * a.S, per = (total + kXcds - 1) / kXcds;
+  int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
   if (blockIdx.x / kXcds >= per || l >= total) return false;
+  t->sp = (int)(l / each);
+  l -= t->sp * each;
   const int group = (int)(l / (8LL * a.ntn));
   const int gm = a.ntm - 8 * group < 8 ? a.ntm - 8 * group : 8;
   const int rem = (int)(l - 8LL * group * a.ntn);
@@ -572,38 +575,87 @@ __device__ __forceinline__ bool large_tile(const LargeArgs& a, int height, Large
   return true;
 }
 
+// PART: one of S splits of K, whose sums go to a.part [S][T][columns] in fp32.
 #define MOONEP_LARGE(name, body)                                                       \
-  template <int MI>                                                                    \
+  template <int MI, bool PART>                                                         \
   __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),           \
                             amdgpu_waves_per_eu(1, 1))) void name(LargeArgs a) {       \
     MOONEP_RING(smem);                                                                 \
     LargeTile t;                                                                       \
     if (!large_tile(a, 64 * MI, &t)) return;                                           \
-    if (MI == 4 && t.rows <= kHalfTileM) body<2>(a, smem, t);                          \
-    else body<MI>(a, smem, t);                                                         \
+    if (MI == 4 && t.rows <= kHalfTileM) body<2, PART>(a, smem, t);                    \
+    else body<MI, PART>(a, smem, t);                                                   \
   }
 
-// 32 MI x 2 rows, 128 gate and 128 up columns, K = H.
+// Steps [j0, j0 + n) of K of a split.
+struct Steps {
+  int j0, n;
+};
+template <bool PART>
+__device__ __forceinline__ Steps steps_of(const LargeArgs& a, const LargeTile& t, int nk) {
+  if constexpr (!PART) return {0, nk};
+  const int j0 = (int)((int64_t)nk * t.sp / a.S);
+  return {j0, (int)((int64_t)nk * (t.sp + 1) / a.S) - j0};
+}
+
+// The accumulators to fp32 rows: block j of this lane's row lies at row + col[j].
 template <int MI>
+__device__ __forceinline__ void store_f32(const f32x16 (&acc)[MI][4], float* out, int64_t ld,
+                                          int rows, const int64_t (&col)[4], const int (&left)[4]) {
+  const int wm = threadIdx.x >> 7, lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = wm * 32 * MI + 32 * i + lr;
+    if (m >= rows) continue;
+    float* row = out + (int64_t)m * ld;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = acc_col(q, lh);
+        if (c < left[j])
+          *(f32x4*)(row + col[j] + c) = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                              acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      }
+  }
+}
+
+// 32 MI x 2 rows, 128 gate and 128 up columns, K = H.
+template <int MI, bool PART>
 __device__ __forceinline__ void gateup_product(const LargeArgs& a, const Ring& smem,
                                                const LargeTile& t, f32x16 (&acc)[MI][4], int wm,
                                                int wn) {
   const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
   const int nrow[4] = {wn * 64, wn * 64 + 32, 128 + wn * 64, 128 + wn * 64 + 32};
+  const Steps k = steps_of<PART>(a, t, a.H / BK);
+  const int64_t k0 = (int64_t)k.j0 * BK;
   RowTileT<2 * MI> la;
   ColTile lb;
-  la.init(a.x + (int64_t)t.m0 * a.H, a.H, t.rows);
-  lb.init(a.w[0] + n0, a.w[1] + n0, a.Hp, a.H, nv, nv);
-  gemm_loop<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
+  la.init(a.x + (int64_t)t.m0 * a.H + k0, a.H, t.rows);
+  lb.init(a.w[0] + k0 * a.Hp + n0, a.w[1] + k0 * a.Hp + n0, a.Hp, a.H - k0, nv, nv);
+  gemm_loop<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
 }
 
-template <int MI>
+template <int MI, bool PART>
 __device__ __forceinline__ void large_gateup_tile(const LargeArgs& a, const Ring& smem,
                                                   const LargeTile& t) {
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
   f32x16 acc[MI][4];
-  gateup_product<MI>(a, smem, t, acc, wm, wn);
+  gateup_product<MI, PART>(a, smem, t, acc, wm, wn);
+  if constexpr (PART) {
+    int64_t col[4];
+    int left[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = wn * 64 + 32 * (j & 1);
+      col[j] = (j >> 1) * (int64_t)a.Hp + n0 + c;
+      left[j] = nv - c;
+    }
+    store_f32<MI>(acc, a.part + ((int64_t)t.sp * a.T + t.m0) * 2 * a.Hp, 2LL * a.Hp, t.rows, col,
+                  left);
+    return;
+  }
   typedef Stage<32 * MI, 64> St;
   lds_t* reg = smem.base + wave * St::kBytes;
 #pragma unroll
@@ -640,53 +692,100 @@ __device__ __forceinline__ void store_bf16(const Ring& smem, const f32x16 (&acc)
   St::flush(reg, make_rsrc(out, (int64_t)rows * ld * 2), wm * 32 * MI, ld, wn * 128, cols);
 }
 
-// Y: 256 columns, K = H'.  What is added is read 16 pieces ahead (two of a
-// wave's columns of blocks): all at once would not fit beside the sums.
-template <int MI>
+// What is added to 32 rows of a wave's 128 columns, as it is stored: lane l has
+// eight columns of row 4 t + l / 16 in piece t.
+struct Added {
+  u32x4 v[8];
+  __device__ __forceinline__ void load(const uint16_t* add, int64_t ld, int m0, int rows, int c0,
+                                       int cols) {
+    const int lane = threadIdx.x & 63, c = c0 + 8 * (lane & 15);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int m = m0 + 4 * t + (lane >> 4);
+      v[t] = u32x4{0, 0, 0, 0};
+      if (m < rows && c < cols) v[t] = *(const u32x4*)(add + (int64_t)m * ld + c);
+    }
+  }
+};
+
+// Y: 256 columns, K = H'.  What is added is read along whole rows, so the sums
+// go through LDS in fp32, 32 rows at a time, to meet it (read at the
+// accumulators' places, 8 bytes a lane and row, it cost 150 us of 32768 tokens'
+// 990); each 32 rows' loads are issued before the 32 rows in front are
+// finished.
+template <int MI, bool PART>
 __device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& smem,
                                                 const LargeTile& t) {
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
   const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
+  const Steps k = steps_of<PART>(a, t, a.Hp / BK);
+  const int64_t k0 = (int64_t)k.j0 * BK, at = (int64_t)t.m0 * a.H + n0;
   RowTileT<2 * MI> la;
   RowTile lb;
-  la.init(a.z + (int64_t)t.m0 * a.Hp, a.Hp, t.rows);
-  lb.init(a.w[2] + (int64_t)n0 * a.Hp, a.Hp, cols);
+  la.init(a.z + (int64_t)t.m0 * a.Hp + k0, a.Hp, t.rows);
+  lb.init(a.w[2] + (int64_t)n0 * a.Hp + k0, a.Hp, cols);
   f32x16 acc[MI][4];
-  gemm_loop<MI>(la, lb, smem, a.Hp / BK, acc, wm * 32 * MI, nrow);
-  const int64_t at = (int64_t)t.m0 * a.H + n0;
-  if (a.add) {
-    const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  const bool add = !PART && a.add;
+  gemm_loop<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
+  if constexpr (PART) {
+    int64_t col[4];
+    int left[4];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int m = wm * 32 * MI + 32 * i + lr;
-      const uint16_t* row = a.add + at + (int64_t)m * a.H;
+    for (int j = 0; j < 4; ++j) {
+      col[j] = n0 + nrow[j];
+      left[j] = cols - nrow[j];
+    }
+    store_f32<MI>(acc, a.part + ((int64_t)t.sp * a.T + t.m0) * a.H, a.H, t.rows, col, left);
+    return;
+  }
+  if (!add) {
+    store_bf16<MI>(smem, acc, a.y + at, a.H, t.rows, cols);
+    return;
+  }
+  typedef __attribute__((address_space(3))) float lds_f;
+  constexpr int kRow = 132;                       // floats: 32 rows' pieces on distinct banks
+  lds_f* reg = (lds_f*)(smem.base + wave * (32 * kRow * 4));
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  const Rsrc ys = make_rsrc(a.y + at, (int64_t)t.rows * a.H * 2);
+  Added next;
+  next.load(a.add + at, a.H, wm * 32 * MI, t.rows, wn * 128, cols);
 #pragma unroll
-      for (int jj = 0; jj < 4; jj += 2) {
-        u32x2 v[2][4];
+  for (int i = 0; i < MI; ++i) {
+    const Added now = next;
+    if (i + 1 < MI)
+      next.load(a.add + at, a.H, wm * 32 * MI + 32 * (i + 1), t.rows, wn * 128, cols);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = nrow[jj + j] + acc_col(q, lh);
-            v[j][q] = u32x2{0, 0};
-            if (m < t.rows && c < cols) v[j][q] = *(const u32x2*)(row + c);
-          }
+      for (int q = 0; q < 4; ++q)
+        *(__attribute__((address_space(3))) f32x4*)(reg + lr * kRow + 32 * j + acc_col(q, lh)) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                  acc[i][j][4 * q + 3]};
+    const int c = 8 * (lane & 15);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+    for (int p = 0; p < 8; ++p) {
+      const int r = 4 * p + (lane >> 4);
+      const lds_f* from = reg + r * kRow + c;
+      const f32x4 s0 = *(const __attribute__((address_space(3))) f32x4*)from;
+      const f32x4 s1 = *(const __attribute__((address_space(3))) f32x4*)(from + 4);
+      u32x4 o;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[i][jj + j][4 * q + e] += bf16_of(v[j][q][e >> 1], e & 1);
+      for (int e = 0; e < 4; ++e) {
+        const float lo = e < 2 ? s0[2 * (e & 1)] : s1[2 * (e & 1)];
+        const float hi = e < 2 ? s0[2 * (e & 1) + 1] : s1[2 * (e & 1) + 1];
+        o[e] = pack_bf16x2(lo + bf16_of(now.v[p][e], 0), hi + bf16_of(now.v[p][e], 1));
       }
+      const int m = wm * 32 * MI + 32 * i + r;
+      const uint32_t off = wn * 128 + c < cols
+                               ? (uint32_t)(((int64_t)m * a.H + wn * 128 + c) * 2) : kOob;
+      __builtin_amdgcn_raw_buffer_store_b128(o, ys, off, 0, 0);
     }
   }
-  store_bf16<MI>(smem, acc, a.y + at, a.H, t.rows, cols);
 }
 
 // dZ in fp32: 256 columns of H', K = H.
-template <int MI>
+template <int MI, bool PART>
 __device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
@@ -699,32 +798,24 @@ __device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& sm
   lb.init(a.w[2] + n0, a.w[2] + n0 + 128, a.Hp, a.H, nv0, cols - nv0);
   f32x16 acc[MI][4];
   gemm_loop<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  int64_t col[4];
+  int left[4];
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = wm * 32 * MI + 32 * i + lr;
-    if (m >= t.rows) continue;
-    float* row = a.dz + (int64_t)(t.m0 + m) * a.Hp + n0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = nrow[j] + acc_col(q, lh);
-        if (c < cols)
-          *(f32x4*)(row + c) = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                     acc[i][j][4 * q + 3]};
-      }
+  for (int j = 0; j < 4; ++j) {
+    col[j] = n0 + nrow[j];
+    left[j] = cols - nrow[j];
   }
+  store_f32<MI>(acc, a.dz + (int64_t)t.m0 * a.Hp, a.Hp, t.rows, col, left);
 }
 
 // dG, dU and Z from the gate/up product and dZ.
-template <int MI>
+template <int MI, bool PART>
 __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
   const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
   f32x16 acc[MI][4];
-  gateup_product<MI>(a, smem, t, acc, wm, wn);
+  gateup_product<MI, false>(a, smem, t, acc, wm, wn);
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
   typedef Stage<32 * MI, 64> St;
   lds_t* reg_g = smem.base + wave * (2 * St::kBytes);
@@ -774,7 +865,7 @@ __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& sm
 }
 
 // dX: 256 columns of H, K = 2 H' over [dG | dU] and [Wg | Wu].
-template <int MI>
+template <int MI, bool PART>
 __device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
   const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
@@ -868,16 +959,19 @@ int splits(int64_t tiles, int nk) {
 }
 
 // M x N outputs (in tiles of small_n and large_n columns), K in steps of 64.
-Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk) {
+constexpr int kLargeSteps = 16;
+Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk, bool large_splits) {
   Shape s;
   // large tiles where they fill the GPU (one workgroup per CU)
   const int64_t full = ceil_div(M, 256) * cols_large, half = ceil_div(M, 128) * cols_large;
-  s.large = full >= 192 || half >= 192;
+  int64_t S = half > 0 ? 256 / half : 1;
+  if (S < 1) S = 1;
+  s.large = full >= 192 || half >= 192 || (large_splits && half * S >= 192 && nk / S >= kLargeSteps);
   if (s.large) {
     s.rows = full >= 192 ? 256 : 128;
     s.ntm = (int)ceil_div(M, s.rows);
     s.ntn = (int)cols_large;
-    s.S = 1;
+    s.S = s.rows == 256 || half >= 192 ? 1 : (int)S;
     return s;
   }
   s.rows = M <= 32 ? 32 : M <= 64 ? 64 : 128;
@@ -887,17 +981,17 @@ Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk) {
   return s;
 }
 Shape gateup_shape(int64_t T, int H, int Hp) {
-  return pick(T, Hp / 64, ceil_div(Hp, 128), H / BK);
+  return pick(T, Hp / 64, ceil_div(Hp, 128), H / BK, true);
 }
 Shape down_shape(int64_t T, int H, int Hp) {
-  return pick(T, ceil_div(H, 128), ceil_div(H, 256), Hp / BK);
+  return pick(T, ceil_div(H, 128), ceil_div(H, 256), Hp / BK, true);
 }
 Shape dx_shape(int64_t T, int H, int Hp) {
-  return pick(T, ceil_div(H, 128), ceil_div(H, 256), 2 * Hp / BK);
+  return pick(T, ceil_div(H, 128), ceil_div(H, 256), 2 * Hp / BK, false);
 }
 // dG, dU, Z: tiles of gate and up, and of dZ (in the same launch where they are small)
 Shape grad_shape(int64_t T, int H, int Hp) {
-  return pick(T, Hp / 64 + ceil_div(Hp, 128), ceil_div(Hp, 128), H / BK);
+  return pick(T, Hp / 64 + ceil_div(Hp, 128), ceil_div(Hp, 128), H / BK, false);
 }
 Shape wgrad_shape(int64_t T, int H, int Hp) {
   const int nk = (int)ceil_div(T, BK);
@@ -929,8 +1023,8 @@ FwdWs fwd_ws(int64_t T, int H, int Hp) {
   w.part = round256(T * Hp * 2);
   const Shape g = gateup_shape(T, H, Hp), d = down_shape(T, H, Hp);
   int64_t p = 0;
-  if (!g.large) p = (int64_t)g.S * T * 2 * Hp * 4;
-  if (!d.large && d.S > 1 && (int64_t)d.S * T * H * 4 > p) p = (int64_t)d.S * T * H * 4;
+  if (!g.large || g.S > 1) p = (int64_t)g.S * T * 2 * Hp * 4;
+  if (d.S > 1 && (int64_t)d.S * T * H * 4 > p) p = (int64_t)d.S * T * H * 4;
   w.total = w.part + round256(p);
   return w;
 }
@@ -992,13 +1086,23 @@ void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
   }
 }
 
-#define MOONEP_RUN_LARGE(kernel, shape, args)                                       \
-  do {                                                                              \
-    LargeArgs la_ = args;                                                           \
-    la_.ntm = (shape).ntm;                                                          \
-    la_.ntn = (shape).ntn;                                                          \
-    if ((shape).rows == 256) kernel<4><<<blocks_of(shape), kThreads, 0, s>>>(la_);  \
-    else kernel<2><<<blocks_of(shape), kThreads, 0, s>>>(la_);                      \
+LargeArgs with_shape(LargeArgs a, const Shape& s) {
+  a.ntm = s.ntm;
+  a.ntn = s.ntn;
+  a.S = s.S;
+  return a;
+}
+#define MOONEP_RUN_LARGE(kernel, shape, args)                                                      \
+  do {                                                                                             \
+    const LargeArgs la_ = with_shape(args, shape);                                                 \
+    if ((shape).rows == 256) kernel<4, false><<<blocks_of(shape), kThreads, 0, s>>>(la_);          \
+    else kernel<2, false><<<blocks_of(shape), kThreads, 0, s>>>(la_);                              \
+  } while (0)
+// the same, or splits of 128-row tiles
+#define MOONEP_RUN_LARGE_SPLITS(kernel, shape, args)                                               \
+  do {                                                                                             \
+    if ((shape).S == 1) MOONEP_RUN_LARGE(kernel, shape, args);                                     \
+    else kernel<2, true><<<blocks_of(shape), kThreads, 0, s>>>(with_shape(args, shape));           \
   } while (0)
 
 }  // namespace
@@ -1027,31 +1131,36 @@ hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int3
   LargeArgs big = {};
   big.x = x; big.add = add; big.z = z; big.y = y;
   for (int i = 0; i < 3; ++i) big.w[i] = w[i];
-  big.T = (int)T; big.H = H; big.Hp = Hp; big.act = act;
+  big.part = part; big.T = (int)T; big.H = H; big.Hp = Hp; big.act = act;
+  bool parts = g.S > 1;
   if (g.large) {
-    MOONEP_RUN_LARGE(large_gateup, g, big);
+    MOONEP_RUN_LARGE_SPLITS(large_gateup, g, big);
   } else {
     SmallArgs a = {};
     a.a[0] = x; a.b[0] = w[0]; a.b[1] = w[1]; a.out[0] = z;
     a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
-    const bool p = g.S > 1 || g.rows == 32;
-    run_small<OP_GATEUP>(g, p, a, s);
-    if (p) join_gate<false><<<joins(T * Hp), kJoin, 0, s>>>(part, g.S, (int)T, Hp, act, z, nullptr,
-                                                         nullptr);
+    parts = parts || g.rows == 32;
+    run_small<OP_GATEUP>(g, parts, a, s);
+  }
+  if (parts)
+    join_gate<false><<<joins(T * Hp), kJoin, 0, s>>>(part, g.S, (int)T, Hp, act, z, nullptr,
+                                                     nullptr);
+  if (few(T, H)) {
+    SmallArgs a = {};
+    a.a[0] = z; a.b[0] = w[2]; a.out[0] = y; a.add = add;
+    a.M = (int)T; a.N = H; a.K = Hp;
+    few_rows<<<H / 32, kThreads, 0, s>>>(a);
+    return hipGetLastError();
   }
   if (d.large) {
-    MOONEP_RUN_LARGE(large_down, d, big);
+    MOONEP_RUN_LARGE_SPLITS(large_down, d, big);
   } else {
     SmallArgs a = {};
     a.a[0] = z; a.b[0] = w[2]; a.out[0] = y; a.add = add;
     a.part = part; a.M = (int)T; a.N = H; a.K = Hp;
-    if (few(T, H)) {
-      few_rows<<<H / 32, kThreads, 0, s>>>(a);
-      return hipGetLastError();
-    }
     run_small<OP_ROWS>(d, d.S > 1, a, s);
-    if (d.S > 1) join_rows<<<joins(T * H), kJoin, 0, s>>>(part, d.S, T * H, add, y);
   }
+  if (d.S > 1) join_rows<<<joins(T * H), kJoin, 0, s>>>(part, d.S, T * H, add, y);
   return hipGetLastError();
 }
 

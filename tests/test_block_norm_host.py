@@ -58,6 +58,23 @@ def test_backward_refuses(bad, status):
     assert backward(**bad) == status
 
 
+@pytest.mark.parametrize("bad", [
+    dict(h_out=A[0] + 16), dict(h_out=A[1]), dict(h_out=A[2]), dict(u=A[0] + 512), dict(u=A[1] + 16),
+    dict(u=A[3]), dict(u=A[4] + 1008), dict(y2=A[6], h_out=A[6]), dict(kind=1, gate=A[4] + 64),
+    dict(kind=3, gate=A[7], u=A[7]), dict(kind=2, gate=A[5] + 4)])
+def test_forward_refuses_overlaps(bad):
+    assert forward(**bad) == ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dres=A[1] + 16), dict(dres=A[2] + 496), dict(dy=A[6] + 1008), dict(dy=A[0]),
+    dict(dy=A[3] + 16), dict(dw_post=A[9]), dict(dw_pre=A[5]), dict(ws=A[0] + 256), dict(dw_post=A[10]),
+    dict(kind=1, gate=A[11], dgate=A[11]), dict(kind=2, gate=A[11], dgate=A[7] + 500),
+    dict(y2=A[12], dres=A[12] + 256)])
+def test_backward_refuses_overlaps(bad):
+    assert backward(**bad) == ARG
+
+
 def test_no_rows_need_no_pointers():
     assert forward(T=0, h=None, h_out=None, u=None) == OK
 

@@ -55,6 +55,21 @@ def test_backward_refuses(bad):
     assert backward(**bad) == ARG
 
 
+@pytest.mark.parametrize("bad", [
+    dict(y=A[0] + 496), dict(y=A[10] + 64 * 256 - 16), dict(add=A[1] + 16), dict(ws=A[0] - 256),
+    dict(ws=A[12] + 256)])
+def test_forward_refuses_overlaps(bad):
+    assert forward(**bad) == ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dx=A[0] + 16), dict(dx=A[1] - 496), dict(dw=(A[3], A[3] + 64 * 256 - 16, A[5])),
+    dict(dw=(A[3], A[3] + 64 * 256, A[5]), dtype=_abi.F32), dict(dw=(A[10] + 16, A[4], A[5])),
+    dict(ws=A[1]), dict(ws=A[5] - 256), dict(dw=(A[2] + 496, A[4], A[5]))])
+def test_backward_refuses_overlaps(bad):
+    assert backward(**bad) == ARG
+
+
 def test_too_many_tokens_for_the_weight_gradients():
     """The backward addresses the tokens' columns with 31-bit offsets; the forward does not."""
     lib = _abi.lib()
