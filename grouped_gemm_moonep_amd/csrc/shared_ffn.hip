@@ -538,6 +538,74 @@ __global__ __launch_bounds__(kJoin) void join_wgrad(const float* part, int S, in
 }
 
 // ------------------------------------------------------------- large tiles
+// K loop of the 128-row tiles (128 x 256, four waves of 64 x 128).  A step has
+// half the MFMAs of a 256-row one, so a load one step ahead, as gemm_loop's A
+// tiles are, arrives too late; the smaller A tile leaves room for three whole
+// stages of 48 KiB in place of five slots: all loads are two steps ahead.  Step j's
+// barrier comes when its last fragments are read, so the loads of step j + 3
+// may go to its stage from then on.
+constexpr int kMidA = 16384, kMidStage = kMidA + kSlotBytes;
+template <int J, class TA, class TB>
+__device__ __forceinline__ void mid_step(const TA& la, const TB& lb, lds_t* base, int j, int nk,
+                                         Frags<2>& f0, Frags<2>& f1, f32x16 (&acc)[2][4], int arow0,
+                                         const int (&nrow)[4]) {
+  static_assert(TA::kLoads == 4 && TB::kLoads == 8, "the wait counts a stage's loads");
+  constexpr int P = 32, SUB = 8, NF = 6, BAR = 23;
+  const lds_t* A = base + J * kMidStage;
+  const lds_t* An = base + (J + 1) % 3 * kMidStage;
+  lds_t* to = base + (J + 2) % 3 * kMidStage;
+  const uint32_t koa = j + 2 < nk ? la.koff((int64_t)(j + 2) * BK) : kOob;
+  const uint32_t kob = j + 2 < nk ? lb.koff((int64_t)(j + 2) * BK) : kOob;
+  MOONEP_PIN();
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int sub = p / SUB, idx = p % SUB;
+    mma1<2>(acc, (sub & 1) ? f1 : f0, idx);
+    if (sub < 3 && idx < NF)
+      read_frag<2, TA, TB>((sub & 1) ? f0 : f1, idx, A, A + kMidA, sub + 1, arow0, nrow);
+    if (p & 1) {
+      if (p / 2 < 4) la.issue1(to, p / 2, koa);
+      else if (p / 2 < 12) lb.issue1(to + kMidA, p / 2 - 4, kob);
+    }
+    if (p == BAR) {
+      MOONEP_PIN();
+      wait_vm<12>();
+      barrier_reads_done();
+    }
+    if (p > BAR && p - BAR - 1 < NF)
+      read_frag<2, TA, TB>(f0, p - BAR - 1, An, An + kMidA, 0, arow0, nrow);
+    MOONEP_PIN();
+  }
+}
+template <class TA, class TB>
+__device__ __forceinline__ void mid_loop(const TA& la, const TB& lb, lds_t* base, int nk,
+                                         f32x16 (&acc)[2][4], int arow0, const int (&nrow)[4]) {
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    la.issue(base + d * kMidStage, d * BK, d < nk);
+    lb.issue(base + d * kMidStage + kMidA, d * BK, d < nk);
+  }
+  zero_acc<2>(acc);
+  wait_vm<12>();
+  barrier_reads_done();
+  Frags<2> f0, f1;
+#pragma unroll
+  for (int q = 0; q < 6; ++q) read_frag<2, TA, TB>(f0, q, base, base + kMidA, 0, arow0, nrow);
+  for (int j = 0; j < nk; j += 3) {
+    mid_step<0>(la, lb, base, j, nk, f0, f1, acc, arow0, nrow);
+    if (j + 1 < nk) mid_step<1>(la, lb, base, j + 1, nk, f0, f1, acc, arow0, nrow);
+    if (j + 2 < nk) mid_step<2>(la, lb, base, j + 2, nk, f0, f1, acc, arow0, nrow);
+  }
+  wait_vm<0>();
+  __syncthreads();               // the ring may be reused
+}
+template <int MI, class TA, class TB>
+__device__ __forceinline__ void product(const TA& la, const TB& lb, const Ring& ring, int nk,
+                                        f32x16 (&acc)[MI][4], int arow0, const int (&nrow)[4]) {
+  if constexpr (MI == 2) mid_loop(la, lb, ring.base, nk, acc, arow0, nrow);
+  else gemm_loop<MI>(la, lb, ring, nk, acc, arow0, nrow);
+}
+
 struct LargeArgs {
   const uint16_t* x;
   const uint16_t* dy;
@@ -633,7 +701,7 @@ __device__ __forceinline__ void gateup_product(const LargeArgs& a, const Ring& s
   ColTile lb;
   la.init(a.x + (int64_t)t.m0 * a.H + k0, a.H, t.rows);
   lb.init(a.w[0] + k0 * a.Hp + n0, a.w[1] + k0 * a.Hp + n0, a.Hp, a.H - k0, nv, nv);
-  gemm_loop<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
+  product<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
 }
 
 template <int MI, bool PART>
@@ -727,7 +795,7 @@ __device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& 
   lb.init(a.w[2] + (int64_t)n0 * a.Hp + k0, a.Hp, cols);
   f32x16 acc[MI][4];
   const bool add = !PART && a.add;
-  gemm_loop<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
+  product<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
   if constexpr (PART) {
     int64_t col[4];
     int left[4];
@@ -797,7 +865,7 @@ __device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& sm
   la.init(a.dy + (int64_t)t.m0 * a.H, a.H, t.rows);
   lb.init(a.w[2] + n0, a.w[2] + n0 + 128, a.Hp, a.H, nv0, cols - nv0);
   f32x16 acc[MI][4];
-  gemm_loop<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
+  product<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
   int64_t col[4];
   int left[4];
 #pragma unroll
@@ -877,8 +945,41 @@ __device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& sm
   la.init(a.dg + ab, a.du + ab, a.Hp, t.rows, a.Hp);
   lb.init(a.w[0] + bb, a.w[1] + bb, a.Hp, cols, a.Hp);
   f32x16 acc[MI][4];
-  gemm_loop<MI>(la, lb, smem, 2 * a.Hp / BK, acc, wm * 32 * MI, nrow);
+  product<MI>(la, lb, smem, 2 * a.Hp / BK, acc, wm * 32 * MI, nrow);
   store_bf16<MI>(smem, acc, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
+}
+
+// G, U and dZ of a middling number of tokens in one launch, in splits: tiles of
+// gate and up columns, then tiles of 256 columns of dZ, as two regions of 128
+// like the others.
+__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
+                          amdgpu_waves_per_eu(1, 1))) void large_grad(LargeArgs a) {
+  MOONEP_RING(smem);
+  LargeTile t;
+  if (!large_tile(a, 128, &t)) return;
+  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1, gu = (a.Hp + 127) / 128;
+  const bool dz = t.nt >= gu;
+  const int n0 = dz ? (t.nt - gu) * 256 : t.nt * 128, rest = a.Hp - n0;
+  const int nv0 = rest < 128 ? rest : 128;
+  const int nv1 = !dz ? nv0 : rest < 256 ? rest - nv0 : 128;
+  const int nrow[4] = {wn * 64, wn * 64 + 32, 128 + wn * 64, 128 + wn * 64 + 32};
+  const Steps k = steps_of<true>(a, t, a.H / BK);
+  const int64_t k0 = (int64_t)k.j0 * BK, at = k0 * a.Hp + n0;
+  RowTileT<4> la;
+  ColTile lb;
+  la.init((dz ? a.dy : a.x) + (int64_t)t.m0 * a.H + k0, a.H, t.rows);
+  lb.init(a.w[dz ? 2 : 0] + at, dz ? a.w[2] + at + 128 : a.w[1] + at, a.Hp, a.H - k0, nv0, nv1);
+  f32x16 acc[2][4];
+  product<2>(la, lb, smem, k.n, acc, wm * 64, nrow);
+  int64_t col[4];
+  int left[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = wn * 64 + 32 * (j & 1);
+    col[j] = dz ? 2LL * a.Hp + n0 + (j >> 1) * 128 + c : (j >> 1) * (int64_t)a.Hp + n0 + c;
+    left[j] = ((j >> 1) ? nv1 : nv0) - c;
+  }
+  store_f32<2>(acc, a.part + ((int64_t)t.sp * a.T + t.m0) * 3 * a.Hp, 3LL * a.Hp, t.rows, col, left);
 }
 
 MOONEP_LARGE(large_gateup, large_gateup_tile)
@@ -950,34 +1051,43 @@ struct Shape {
   int rows, ntm, ntn, S;
 };
 
-// Splits of nk steps for so many tiles: two workgroups per CU, at least four steps each.  Twelve
-// steps are done before another launch could have joined them.
+// Splits of nk steps for so many small tiles: a workgroup per CU (with deep rings), or two where
+// one would leave a quarter of them idle; at least four steps each.  Twelve steps are done before
+// another launch could have joined them.  (Two workgroups per CU throughout: 64 tokens of 7168 x
+// 2048 39.8 us, 256 tokens 72 us; this 34.5 and 53 us: half the splits leave half the sums.)
 int splits(int64_t tiles, int nk) {
-  int64_t S = ceil_div(512, tiles);
+  int64_t S = 256 / tiles;
+  if (tiles * S < 192) S = 512 / tiles;
   if (S > nk / 4) S = nk / 4;
   return (int)(S < 1 || nk <= 12 ? 1 : S);
 }
 
-// M x N outputs (in tiles of small_n and large_n columns), K in steps of 64.
-constexpr int kLargeSteps = 16;
-Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk, bool large_splits) {
+// Splits of 128-row large tiles that fill the GPU with at least 16 steps each, or 0.
+int large_splits(int64_t tiles, int nk) {
+  if (tiles < 1 || tiles > 256) return 0;
+  const int64_t S = 256 / tiles;
+  return tiles * S >= 192 && nk / S >= 16 ? (int)S : 0;
+}
+
+// A product of M rows in tiles of so many columns, K in nk steps of 64.  `half`: 128-row large
+// tiles may be cut into splits.
+Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk, bool half) {
   Shape s;
+  s.S = 1;
   // large tiles where they fill the GPU (one workgroup per CU)
-  const int64_t full = ceil_div(M, 256) * cols_large, half = ceil_div(M, 128) * cols_large;
-  int64_t S = half > 0 ? 256 / half : 1;
-  if (S < 1) S = 1;
-  s.large = full >= 192 || half >= 192 || (large_splits && half * S >= 192 && nk / S >= kLargeSteps);
+  const int64_t n256 = ceil_div(M, 256) * cols_large, n128 = ceil_div(M, 128) * cols_large;
+  const int S = half && n128 < 192 ? large_splits(n128, nk) : 0;
+  s.large = n128 >= 192 || S > 0;
   if (s.large) {
-    s.rows = full >= 192 ? 256 : 128;
-    s.ntm = (int)ceil_div(M, s.rows);
+    s.rows = n256 >= 192 ? 256 : 128;
     s.ntn = (int)cols_large;
-    s.S = s.rows == 256 || half >= 192 ? 1 : (int)S;
-    return s;
+    if (S > 0) s.S = S;
+  } else {
+    s.rows = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    s.ntn = (int)cols_small;
   }
-  s.rows = M <= 32 ? 32 : M <= 64 ? 64 : 128;
   s.ntm = (int)ceil_div(M, s.rows);
-  s.ntn = (int)cols_small;
-  s.S = splits((int64_t)s.ntm * s.ntn, nk);
+  if (!s.large) s.S = splits((int64_t)s.ntm * s.ntn, nk);
   return s;
 }
 Shape gateup_shape(int64_t T, int H, int Hp) {
@@ -989,9 +1099,20 @@ Shape down_shape(int64_t T, int H, int Hp) {
 Shape dx_shape(int64_t T, int H, int Hp) {
   return pick(T, ceil_div(H, 128), ceil_div(H, 256), 2 * Hp / BK, false);
 }
-// dG, dU, Z: tiles of gate and up, and of dZ (in the same launch where they are small)
-Shape grad_shape(int64_t T, int H, int Hp) {
-  return pick(T, Hp / 64 + ceil_div(Hp, 128), ceil_div(Hp, 128), H / BK, false);
+// dG, dU, Z: tiles of gate and up; small ones, and 128-row large ones in splits (`parts`), with
+// those of dZ in the same launch.
+struct GradShape {
+  Shape s;
+  bool parts;
+};
+GradShape grad_shape(int64_t T, int H, int Hp) {
+  GradShape g;
+  const int64_t gu = ceil_div(Hp, 128), all = gu + ceil_div(Hp, 256), m = ceil_div(T, 128);
+  const int S = m * gu < 192 ? large_splits(m * all, H / BK) : 0;
+  g.s = pick(T, Hp / 64 + gu, gu, H / BK, false);
+  g.parts = S > 0 || !g.s.large;
+  if (S > 0) g.s = {true, 128, (int)m, (int)all, S};
+  return g;
 }
 Shape wgrad_shape(int64_t T, int H, int Hp) {
   const int nk = (int)ceil_div(T, BK);
@@ -1038,8 +1159,9 @@ BwdWs bwd_ws(int64_t T, int H, int Hp) {
   w.dg = one;
   w.du = 2 * one;
   w.dz = w.part = 3 * one;
-  const Shape g = grad_shape(T, H, Hp), x = dx_shape(T, H, Hp), d = wgrad_shape(T, H, Hp);
-  int64_t p = g.large ? T * Hp * 4 : (int64_t)g.S * T * 3 * Hp * 4;
+  const GradShape g = grad_shape(T, H, Hp);
+  const Shape x = dx_shape(T, H, Hp), d = wgrad_shape(T, H, Hp);
+  int64_t p = g.parts ? (int64_t)g.s.S * T * 3 * Hp * 4 : T * Hp * 4;
   if (!x.large && x.S > 1 && (int64_t)x.S * T * H * 4 > p) p = (int64_t)x.S * T * H * 4;
   if (!d.large && d.S > 1 && (int64_t)d.S * 3 * H * Hp * 4 > p) p = (int64_t)d.S * 3 * H * Hp * 4;
   w.total = w.part + round256(p);
@@ -1179,7 +1301,8 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
     return hipGetLastError();
   }
   const BwdWs at = bwd_ws(T, H, Hp);
-  const Shape g = grad_shape(T, H, Hp), dxs = dx_shape(T, H, Hp), ws_ = wgrad_shape(T, H, Hp);
+  const GradShape g = grad_shape(T, H, Hp);
+  const Shape dxs = dx_shape(T, H, Hp), ws_ = wgrad_shape(T, H, Hp);
   LargeArgs big = {};
   big.x = x; big.dy = dy; big.dx = dx;
   big.z = (uint16_t*)(ws + at.z); big.dg = (uint16_t*)(ws + at.dg); big.du = (uint16_t*)(ws + at.du);
@@ -1190,18 +1313,23 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
   }
   big.T = (int)T; big.H = H; big.Hp = Hp; big.act = act; big.f32 = dw_type == MOONEP_F32;
   float* part = (float*)(ws + at.part);
-  if (g.large) {
-    Shape z = g;
+  big.part = part;
+  if (!g.parts) {
+    Shape z = g.s;
     z.ntn = (int)ceil_div(Hp, BN);
     MOONEP_RUN_LARGE(large_dz, z, big);
-    MOONEP_RUN_LARGE(large_gu, g, big);
+    MOONEP_RUN_LARGE(large_gu, g.s, big);
+  } else if (g.s.large) {
+    large_grad<<<blocks_of(g.s), kThreads, 0, s>>>(with_shape(big, g.s));
   } else {
     SmallArgs a = {};
     a.a[0] = x; a.a[2] = dy; a.b[0] = w[0]; a.b[1] = w[1]; a.b[2] = w[2];
     a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
-    run_small<OP_GRAD>(g, true, a, s);
-    join_gate<true><<<joins(T * Hp), kJoin, 0, s>>>(part, g.S, (int)T, Hp, act, big.z, big.dg, big.du);
+    run_small<OP_GRAD>(g.s, true, a, s);
   }
+  if (g.parts)
+    join_gate<true><<<joins(T * Hp), kJoin, 0, s>>>(part, g.s.S, (int)T, Hp, act, big.z, big.dg,
+                                                    big.du);
   SmallArgs xa = {}, wa = {};
   xa.a[0] = big.dg; xa.a[1] = big.du; xa.b[0] = w[0]; xa.b[1] = w[1]; xa.out[0] = dx;
   xa.part = part; xa.M = (int)T; xa.N = H; xa.K = 2 * Hp;
