@@ -433,31 +433,29 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum(const float* part, int shar
 }
 
 // Workgroups of a launch and the lanes of each: up to 1024 elements a wave, up to 4096 a workgroup
-// with a vector a lane, beyond two.  Workgroups per CU: as many as give it `waves` waves, one at
-// least.
+// with a vector a lane, beyond two.  Workgroups per CU: as many as have `waves` waves, one at least.
+// Forward: a row a workgroup nearly always (32768 rows of 7168 in bf16: 448 us, with nine workgroups
+// per CU 485 us; the next row's loads ahead of a row's sums 480 to 490 us).  Backward: as few
+// workgroups as keep the CUs busy, for each leaves a share of the sums over tokens (702 us with one
+// per CU, 728 us with three; 16384 rows of 4096 208 us with two per CU, 235 us with one).
 struct NormGrid {
   int vpt, threads;
   bool wave;
   int64_t blocks;
 };
-NormGrid norm_grid(int64_t T, int W, int waves) {
+NormGrid norm_grid(int64_t T, int W, bool bwd) {
   NormGrid g;
   const int vecs = W / 8;
   g.wave = vecs <= 128;
   g.vpt = vecs <= 64 || (vecs > 128 && vecs <= 512) ? 1 : 2;
   g.threads = g.wave ? 256 : (vecs + 64 * g.vpt - 1) / (64 * g.vpt) * 64;
   const int64_t need = g.wave ? (T + 3) / 4 : T;
+  const int waves = !bwd ? 512 : g.vpt == 1 ? 16 : 12;
   const int per_cu = waves * 64 / g.threads;
   const int64_t most = 256LL * (per_cu > 1 ? per_cu : 1);
   g.blocks = need < most ? need : most;
   return g;
 }
-// Forward: a row a workgroup as long as the grid is not huge (32768 rows of 7168 in bf16: 454 us,
-// with nine workgroups per CU 485 us; the next row's loads ahead of a row's sums 480 to 490 us).
-// Backward: as few workgroups as keep the CUs busy, for each leaves a share of the sums over tokens
-// (704 us with one per CU, 728 us with three).
-constexpr int kNormWaves = 2048, kNormBwdWaves = 12;
-
 }  // namespace
 
 bool norm_shape_ok(int64_t T, int32_t W) {
@@ -465,14 +463,14 @@ bool norm_shape_ok(int64_t T, int32_t W) {
 }
 
 int32_t norm_shares(int64_t T, int32_t W) {
-  return (int32_t)norm_grid(T, W, kNormBwdWaves).blocks;
+  return (int32_t)norm_grid(T, W, true).blocks;
 }
 
 int64_t norm_ws_bytes(int64_t T, int32_t W) { return 3LL * norm_shares(T, W) * W * 4; }
 
 template <class TS>
 static hipError_t norm_as(const NormArgs& a, hipStream_t s) {
-  const NormGrid g = norm_grid(a.T, a.W, kNormWaves);
+  const NormGrid g = norm_grid(a.T, a.W, false);
   if (g.wave && g.vpt == 1) norm_kernel<TS, 1, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   else if (g.wave) norm_kernel<TS, 2, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   else if (g.vpt == 1) norm_kernel<TS, 1, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
@@ -487,7 +485,7 @@ hipError_t launch_norm(const NormArgs& a, int32_t dtype, hipStream_t s) {
 
 template <class TS>
 static hipError_t norm_bwd_as(const NormBwdArgs& a, hipStream_t s) {
-  const NormGrid g = norm_grid(a.T, a.W, kNormBwdWaves);
+  const NormGrid g = norm_grid(a.T, a.W, true);
   if (g.blocks == 0) {}                              // no tokens: the sums below are zeros
   else if (g.wave && g.vpt == 1) norm_bwd_kernel<TS, 1, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   else if (g.wave) norm_bwd_kernel<TS, 2, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);

@@ -308,6 +308,32 @@ __device__ __forceinline__ void small_tile(const SmallArgs& a, unsigned block, c
                                          acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         }
     }
+  } else if constexpr (OP == OP_GATEUP && BM == 32) {
+    // waves 0, 1 hold the gate's columns, 2, 3 the up's: these go by way of LDS
+    typedef __attribute__((address_space(3))) f32x4 lds_f4;
+    constexpr int kRow = 36;                       // floats
+    const int w = threadIdx.x >> 6;
+    lds_t* at = (lds_t*)smem + ((w & 1) * 32 + lr) * kRow * 4;
+    __syncthreads();                               // every wave has read its last stage
+    if (w >= 2) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(lds_f4*)(at + acc_col(q, lh) * 4) = f32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1],
+                                                    acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+    }
+    __syncthreads();
+    if (w >= 2 || lr >= mv) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = 32 * w + acc_col(q, lh);
+      if (c >= nv) continue;
+      const f32x4 u = *(const lds_f4*)(at + acc_col(q, lh) * 4);
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = activate(a.act, acc[0][0][4 * q + e]).f * u[e];
+      *(u32x2*)((uint16_t*)a.out[0] + (int64_t)(m0 + lr) * a.N + n0 + c) =
+          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -323,7 +349,7 @@ __device__ __forceinline__ void small_tile(const SmallArgs& a, unsigned block, c
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-          if constexpr (OP == OP_GATEUP && NJ == 2) {
+          if constexpr (OP == OP_GATEUP) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]).f * acc[i][1][4 * q + e];
           }
@@ -1129,8 +1155,9 @@ Shape wgrad_shape(int64_t T, int H, int Hp) {
   return s;
 }
 
-// Whether few_rows takes the down product: its 32 rows of Wd a workgroup have to fill the CUs.
-bool few(int64_t T, int H) { return T <= 32 && H / 32 >= 128; }
+// Whether few_rows takes the down product: with 32 rows of Wd a workgroup either fills the CUs or is
+// done in 16 steps.
+bool few(int64_t T, int H, int Hp) { return T <= 32 && (H / 32 >= 128 || Hp <= 4096); }
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -1144,8 +1171,8 @@ FwdWs fwd_ws(int64_t T, int H, int Hp) {
   w.part = round256(T * Hp * 2);
   const Shape g = gateup_shape(T, H, Hp), d = down_shape(T, H, Hp);
   int64_t p = 0;
-  if (!g.large || g.S > 1) p = (int64_t)g.S * T * 2 * Hp * 4;
-  if (d.S > 1 && (int64_t)d.S * T * H * 4 > p) p = (int64_t)d.S * T * H * 4;
+  if (g.S > 1) p = (int64_t)g.S * T * 2 * Hp * 4;
+  if (d.S > 1 && !few(T, H, Hp) && (int64_t)d.S * T * H * 4 > p) p = (int64_t)d.S * T * H * 4;
   w.total = w.part + round256(p);
   return w;
 }
@@ -1192,7 +1219,6 @@ template <int OP>
 void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
   const SmallArgs a = with_shape(in, s);
   constexpr bool kPart = OP == OP_GRAD;            // always in parts
-  constexpr bool kPart32 = kPart || OP == OP_GATEUP;
   if constexpr (OP == OP_WGRAD) {
     if (part) run_small_as<OP, 128, true>(s, a, st);
     else run_small_as<OP, 128, false>(s, a, st);
@@ -1203,8 +1229,8 @@ void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
     if (part || kPart) run_small_as<OP, 64, true>(s, a, st);
     else run_small_as<OP, 64, kPart>(s, a, st);
   } else {
-    if (part || kPart32) run_small_as<OP, 32, true>(s, a, st);
-    else run_small_as<OP, 32, kPart32>(s, a, st);
+    if (part || kPart) run_small_as<OP, 32, true>(s, a, st);
+    else run_small_as<OP, 32, kPart>(s, a, st);
   }
 }
 
@@ -1254,20 +1280,18 @@ hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int3
   big.x = x; big.add = add; big.z = z; big.y = y;
   for (int i = 0; i < 3; ++i) big.w[i] = w[i];
   big.part = part; big.T = (int)T; big.H = H; big.Hp = Hp; big.act = act;
-  bool parts = g.S > 1;
   if (g.large) {
     MOONEP_RUN_LARGE_SPLITS(large_gateup, g, big);
   } else {
     SmallArgs a = {};
     a.a[0] = x; a.b[0] = w[0]; a.b[1] = w[1]; a.out[0] = z;
     a.part = part; a.M = (int)T; a.N = Hp; a.K = H; a.act = act;
-    parts = parts || g.rows == 32;
-    run_small<OP_GATEUP>(g, parts, a, s);
+    run_small<OP_GATEUP>(g, g.S > 1, a, s);
   }
-  if (parts)
+  if (g.S > 1)
     join_gate<false><<<joins(T * Hp), kJoin, 0, s>>>(part, g.S, (int)T, Hp, act, z, nullptr,
                                                      nullptr);
-  if (few(T, H)) {
+  if (few(T, H, Hp)) {
     SmallArgs a = {};
     a.a[0] = z; a.b[0] = w[2]; a.out[0] = y; a.add = add;
     a.M = (int)T; a.N = H; a.K = Hp;
