@@ -564,19 +564,86 @@ __global__ __launch_bounds__(kJoin) void join_wgrad(const float* part, int S, in
 }
 
 // ------------------------------------------------------------- large tiles
-// K loop of the 128-row tiles (128 x 256, four waves of 64 x 128).  A step has
-// half the MFMAs of a 256-row one, so a load one step ahead, as gemm_loop's A
-// tiles are, arrives too late; the smaller A tile leaves room for three whole
-// stages of 48 KiB in place of five slots: all loads are two steps ahead.  Step j's
-// barrier comes when its last fragments are read, so the loads of step j + 3
-// may go to its stage from then on.
+// A 256-row tile is four waves of 128 x 128 on gemm_core.h's loop.  A 128-row
+// one (128 x 256) is eight waves of 64 x 64, two to a SIMD: a step has half the
+// MFMAs, and one wave's waits for the barrier and for LDS are then filled by the
+// other (against four waves of 64 x 128 in as many stages: 4000 tokens of 512 x
+// 768 26.5 -> 24.3 us; the same at 1024 tokens of 7168 x 2048, where either way
+// the tiles' bytes, 48 KiB a step and CU, arrive at 27 bytes a clock, like the 64
+// KiB of the 256-row tiles).
+struct Four {
+  static constexpr int kWaves = 4, NJ = 4;
+  template <int MI> struct Tiles {
+    typedef RowTileT<2 * MI> A;
+    typedef RowTile2<2 * MI> A2;
+    typedef RowTile B;
+    typedef RowTile2<8> B2;
+    typedef ColTile Col;
+  };
+};
+
+// gemm_core.h's column tile loaded by eight waves.
+struct ColTile8 {
+  static constexpr bool kRows = false;
+  static constexpr int kLoads = 4;
+  DmaRsrc rs;           // waves 0..3: region 0; waves 4..7: region 1
+  uint32_t voff, ld2, wlds;
+  __device__ __forceinline__ void init(const uint16_t* src0, const uint16_t* src1, int64_t ld,
+                                       int64_t k_total, int nv0, int nv1) {
+    const int w = wave_id(), lane = threadIdx.x & 63, region = w >> 2;
+    rs = make_dma_rsrc(region ? src1 : src0, k_total * ld * 2);
+    ld2 = (uint32_t)(ld * 2);
+    const int k = 16 * (w & 3) + (lane >> 4);        // load i adds 4 i rows
+    const int col = 8 * ((lane & 15) ^ (4 * (k & 3)));
+    voff = col < (region ? nv1 : nv0) ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
+    wlds = (uint32_t)(w * 4 * 1024);
+  }
+  __device__ __forceinline__ uint32_t koff(int64_t k0) const { return (uint32_t)(k0 * ld2); }
+  __device__ __forceinline__ void issue1(lds_t* tile, int i, uint32_t ko) const {
+    load_lds(rs, tile + wlds + i * 1024, voff + (ko + (uint32_t)(4 * i) * ld2));
+  }
+  __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
+    const uint32_t ko = valid ? koff(k0) : kOob;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) issue1(tile, i, ko);
+  }
+  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
+    return ColTile::frag(tile, nb, kk, lh);
+  }
+};
+struct Eight {
+  static constexpr int kWaves = 8, NJ = 2;
+  template <int MI> struct Tiles {
+    typedef RowTileT<2> A;
+    typedef RowTile2<2> A2;
+    typedef RowTileT<4> B;
+    typedef RowTile2<4> B2;
+    typedef ColTile8 Col;
+  };
+};
+
+// K loop of eight waves: three whole stages of 48 KiB (A 16, B 32), all loads
+// two steps ahead.  Step j = 16 MFMAs a wave in four sub-steps; a sub-step reads
+// the next one's four fragments, the loads go out after every second MFMA, and
+// the barrier comes when the step's last fragments are read: it orders the
+// arrival of step j + 1's stage before its reads, and all reads of step j before
+// the loads of step j + 3 into its stage.
 constexpr int kMidA = 16384, kMidStage = kMidA + kSlotBytes;
+struct Frags8 {
+  bf16x8 a[2], b[2];
+};
+template <class TA, class TB>
+__device__ __forceinline__ void read_frag8(Frags8& f, int q, const lds_t* A, int kk, int arow0,
+                                           const int (&nrow)[2]) {
+  if (q == 0 || q == 3) f.a[q / 3] = frag_of<TA>(A, arow0 + 32 * (q / 3), kk);
+  else f.b[q - 1] = frag_of<TB>(A + kMidA, nrow[q - 1], kk);
+}
 template <int J, class TA, class TB>
-__device__ __forceinline__ void mid_step(const TA& la, const TB& lb, lds_t* base, int j, int nk,
-                                         Frags<2>& f0, Frags<2>& f1, f32x16 (&acc)[2][4], int arow0,
-                                         const int (&nrow)[4]) {
-  static_assert(TA::kLoads == 4 && TB::kLoads == 8, "the wait counts a stage's loads");
-  constexpr int P = 32, SUB = 8, NF = 6, BAR = 23;
+__device__ __forceinline__ void eight_step(const TA& la, const TB& lb, lds_t* base, int j, int nk,
+                                           Frags8& f0, Frags8& f1, f32x16 (&acc)[2][2], int arow0,
+                                           const int (&nrow)[2]) {
+  static_assert(TA::kLoads == 2 && TB::kLoads == 4, "the wait counts a stage's loads");
+  constexpr int P = 16, BAR = 11;
   const lds_t* A = base + J * kMidStage;
   const lds_t* An = base + (J + 1) % 3 * kMidStage;
   lds_t* to = base + (J + 2) % 3 * kMidStage;
@@ -585,51 +652,57 @@ __device__ __forceinline__ void mid_step(const TA& la, const TB& lb, lds_t* base
   MOONEP_PIN();
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int sub = p / SUB, idx = p % SUB;
-    mma1<2>(acc, (sub & 1) ? f1 : f0, idx);
-    if (sub < 3 && idx < NF)
-      read_frag<2, TA, TB>((sub & 1) ? f0 : f1, idx, A, A + kMidA, sub + 1, arow0, nrow);
+    const int sub = p / 4, idx = p % 4;
+    Frags8& f = (sub & 1) ? f1 : f0;
+    acc[idx >> 1][idx & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        f.b[idx & 1], f.a[idx >> 1], acc[idx >> 1][idx & 1], 0, 0, 0);
+    if (sub < 3) read_frag8<TA, TB>((sub & 1) ? f0 : f1, idx, A, sub + 1, arow0, nrow);
     if (p & 1) {
-      if (p / 2 < 4) la.issue1(to, p / 2, koa);
-      else if (p / 2 < 12) lb.issue1(to + kMidA, p / 2 - 4, kob);
+      if (p / 2 < 2) la.issue1(to, p / 2, koa);
+      else if (p / 2 < 6) lb.issue1(to + kMidA, p / 2 - 2, kob);
     }
     if (p == BAR) {
       MOONEP_PIN();
-      wait_vm<12>();
+      wait_vm<6>();
       barrier_reads_done();
     }
-    if (p > BAR && p - BAR - 1 < NF)
-      read_frag<2, TA, TB>(f0, p - BAR - 1, An, An + kMidA, 0, arow0, nrow);
+    if (p > BAR) read_frag8<TA, TB>(f0, p - BAR - 1, An, 0, arow0, nrow);
     MOONEP_PIN();
   }
 }
-template <class TA, class TB>
-__device__ __forceinline__ void mid_loop(const TA& la, const TB& lb, lds_t* base, int nk,
-                                         f32x16 (&acc)[2][4], int arow0, const int (&nrow)[4]) {
-#pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    la.issue(base + d * kMidStage, d * BK, d < nk);
-    lb.issue(base + d * kMidStage + kMidA, d * BK, d < nk);
-  }
-  zero_acc<2>(acc);
-  wait_vm<12>();
-  barrier_reads_done();
-  Frags<2> f0, f1;
-#pragma unroll
-  for (int q = 0; q < 6; ++q) read_frag<2, TA, TB>(f0, q, base, base + kMidA, 0, arow0, nrow);
-  for (int j = 0; j < nk; j += 3) {
-    mid_step<0>(la, lb, base, j, nk, f0, f1, acc, arow0, nrow);
-    if (j + 1 < nk) mid_step<1>(la, lb, base, j + 1, nk, f0, f1, acc, arow0, nrow);
-    if (j + 2 < nk) mid_step<2>(la, lb, base, j + 2, nk, f0, f1, acc, arow0, nrow);
-  }
-  wait_vm<0>();
-  __syncthreads();               // the ring may be reused
-}
-template <int MI, class TA, class TB>
+
+template <class G, int MI, class TA, class TB>
 __device__ __forceinline__ void product(const TA& la, const TB& lb, const Ring& ring, int nk,
-                                        f32x16 (&acc)[MI][4], int arow0, const int (&nrow)[4]) {
-  if constexpr (MI == 2) mid_loop(la, lb, ring.base, nk, acc, arow0, nrow);
-  else gemm_loop<MI>(la, lb, ring, nk, acc, arow0, nrow);
+                                        f32x16 (&acc)[MI][G::NJ], int arow0,
+                                        const int (&nrow)[G::NJ]) {
+  if constexpr (G::kWaves == 4) {
+    gemm_loop<MI>(la, lb, ring, nk, acc, arow0, nrow);
+  } else {
+    lds_t* base = ring.base;
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      la.issue(base + d * kMidStage, d * BK, d < nk);
+      lb.issue(base + d * kMidStage + kMidA, d * BK, d < nk);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    wait_vm<6>();
+    barrier_reads_done();
+    Frags8 f0, f1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) read_frag8<TA, TB>(f0, q, base, 0, arow0, nrow);
+    for (int j = 0; j < nk; j += 3) {
+      eight_step<0>(la, lb, base, j, nk, f0, f1, acc, arow0, nrow);
+      if (j + 1 < nk) eight_step<1>(la, lb, base, j + 1, nk, f0, f1, acc, arow0, nrow);
+      if (j + 2 < nk) eight_step<2>(la, lb, base, j + 2, nk, f0, f1, acc, arow0, nrow);
+    }
+    wait_vm<0>();
+    __syncthreads();               // the stages may be reused
+  }
 }
 
 struct LargeArgs {
@@ -669,16 +742,46 @@ __device__ __forceinline__ bool large_tile(const LargeArgs& a, int height, Large
   return true;
 }
 
+// Where a wave's blocks lie in a tile: rows m0 + 32 i; columns of block j at
+// col(j), or, of a pair of 128-column regions (gate and up), with the first half
+// of its blocks in the one and the other half at the same columns of the other.
+template <class G, int MI>
+struct Waves {
+  static constexpr int NJ = G::NJ, kHalf = NJ / 2, kAcross = G::kWaves / 2;
+  int w, m0, n;                            // wave, its first row, its place along N
+  int nrow[NJ], pair[NJ];
+  __device__ __forceinline__ Waves() {
+    w = threadIdx.x >> 6;
+    n = w % kAcross;
+    m0 = w / kAcross * 32 * MI;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      nrow[j] = 32 * (NJ * n + j);
+      pair[j] = 128 * (j / kHalf) + 32 * (kHalf * n + j % kHalf);
+    }
+  }
+};
+
+// 256 rows in tiles of four waves (a last one of up to 128 rows with half the
+// blocks), 128 rows in tiles of eight.
+#define MOONEP_LARGE(name, body)                                                           \
+  __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),                         \
+                            amdgpu_waves_per_eu(1, 1))) void name##_256(LargeArgs a) {     \
+    MOONEP_RING(smem);                                                                     \
+    LargeTile t;                                                                           \
+    if (!large_tile(a, 256, &t)) return;                                                   \
+    if (t.rows <= kHalfTileM) body<Four, 2, false>(a, smem, t);                            \
+    else body<Four, 4, false>(a, smem, t);                                                 \
+  }                                                                                        \
+  MOONEP_LARGE_128(name##_128, body, false)
 // PART: one of S splits of K, whose sums go to a.part [S][T][columns] in fp32.
-#define MOONEP_LARGE(name, body)                                                       \
-  template <int MI, bool PART>                                                         \
-  __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),           \
-                            amdgpu_waves_per_eu(1, 1))) void name(LargeArgs a) {       \
-    MOONEP_RING(smem);                                                                 \
-    LargeTile t;                                                                       \
-    if (!large_tile(a, 64 * MI, &t)) return;                                           \
-    if (MI == 4 && t.rows <= kHalfTileM) body<2, PART>(a, smem, t);                    \
-    else body<MI, PART>(a, smem, t);                                                   \
+#define MOONEP_LARGE_128(name, body, PART)                                                 \
+  __global__ __attribute__((amdgpu_flat_work_group_size(512, 512),                         \
+                            amdgpu_waves_per_eu(2, 2))) void name(LargeArgs a) {           \
+    MOONEP_RING(smem);                                                                     \
+    LargeTile t;                                                                           \
+    if (!large_tile(a, 128, &t)) return;                                                   \
+    body<Eight, 2, PART>(a, smem, t);                                                      \
   }
 
 // Steps [j0, j0 + n) of K of a split.
@@ -693,17 +796,18 @@ __device__ __forceinline__ Steps steps_of(const LargeArgs& a, const LargeTile& t
 }
 
 // The accumulators to fp32 rows: block j of this lane's row lies at row + col[j].
-template <int MI>
-__device__ __forceinline__ void store_f32(const f32x16 (&acc)[MI][4], float* out, int64_t ld,
-                                          int rows, const int64_t (&col)[4], const int (&left)[4]) {
-  const int wm = threadIdx.x >> 7, lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+template <class G, int MI>
+__device__ __forceinline__ void store_f32(const f32x16 (&acc)[MI][G::NJ], const Waves<G, MI>& at,
+                                          float* out, int64_t ld, int rows,
+                                          const int64_t (&col)[G::NJ], const int (&left)[G::NJ]) {
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int m = wm * 32 * MI + 32 * i + lr;
+    const int m = at.m0 + 32 * i + lr;
     if (m >= rows) continue;
     float* row = out + (int64_t)m * ld;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int c = acc_col(q, lh);
@@ -714,88 +818,90 @@ __device__ __forceinline__ void store_f32(const f32x16 (&acc)[MI][4], float* out
   }
 }
 
-// 32 MI x 2 rows, 128 gate and 128 up columns, K = H.
-template <int MI, bool PART>
+// 128 gate and 128 up columns, K = H.
+template <class G, int MI, bool PART>
 __device__ __forceinline__ void gateup_product(const LargeArgs& a, const Ring& smem,
-                                               const LargeTile& t, f32x16 (&acc)[MI][4], int wm,
-                                               int wn) {
+                                               const LargeTile& t, f32x16 (&acc)[MI][G::NJ],
+                                               const Waves<G, MI>& at) {
   const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
-  const int nrow[4] = {wn * 64, wn * 64 + 32, 128 + wn * 64, 128 + wn * 64 + 32};
   const Steps k = steps_of<PART>(a, t, a.H / BK);
   const int64_t k0 = (int64_t)k.j0 * BK;
-  RowTileT<2 * MI> la;
-  ColTile lb;
+  typename G::template Tiles<MI>::A la;
+  typename G::template Tiles<MI>::Col lb;
   la.init(a.x + (int64_t)t.m0 * a.H + k0, a.H, t.rows);
   lb.init(a.w[0] + k0 * a.Hp + n0, a.w[1] + k0 * a.Hp + n0, a.Hp, a.H - k0, nv, nv);
-  product<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
+  product<G, MI>(la, lb, smem, k.n, acc, at.m0, at.pair);
 }
 
-template <int MI, bool PART>
+template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_gateup_tile(const LargeArgs& a, const Ring& smem,
                                                   const LargeTile& t) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  typedef Waves<G, MI> Wv;
+  const Wv at;
   const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
-  f32x16 acc[MI][4];
-  gateup_product<MI, PART>(a, smem, t, acc, wm, wn);
+  f32x16 acc[MI][G::NJ];
+  gateup_product<G, MI, PART>(a, smem, t, acc, at);
   if constexpr (PART) {
-    int64_t col[4];
-    int left[4];
+    int64_t col[G::NJ];
+    int left[G::NJ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = wn * 64 + 32 * (j & 1);
-      col[j] = (j >> 1) * (int64_t)a.Hp + n0 + c;
+    for (int j = 0; j < G::NJ; ++j) {
+      const int c = at.pair[j] & 127;
+      col[j] = (at.pair[j] >> 7) * (int64_t)a.Hp + n0 + c;
       left[j] = nv - c;
     }
-    store_f32<MI>(acc, a.part + ((int64_t)t.sp * a.T + t.m0) * 2 * a.Hp, 2LL * a.Hp, t.rows, col,
-                  left);
+    store_f32<G, MI>(acc, at, a.part + ((int64_t)t.sp * a.T + t.m0) * 2 * a.Hp, 2LL * a.Hp, t.rows,
+                     col, left);
     return;
   }
-  typedef Stage<32 * MI, 64> St;
-  lds_t* reg = smem.base + wave * St::kBytes;
+  typedef Stage<32 * MI, 32 * Wv::kHalf> St;
+  lds_t* reg = smem.base + at.w * St::kBytes;
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < Wv::kHalf; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float z[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          z[e] = activate(a.act, acc[i][j][4 * q + e]).f * acc[i][j + 2][4 * q + e];
+          z[e] = activate(a.act, acc[i][j][4 * q + e]).f * acc[i][j + Wv::kHalf][4 * q + e];
         St::put(reg, i, j, q, pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
       }
   const Rsrc zs = make_rsrc(a.z + (int64_t)t.m0 * a.Hp + n0, (int64_t)t.rows * a.Hp * 2);
-  St::flush(reg, zs, wm * 32 * MI, a.Hp, wn * 64, nv);
+  St::flush(reg, zs, at.m0, a.Hp, at.pair[0], nv);
 }
 
 // A tile of 256 bf16 columns from the accumulators, by way of LDS.
-template <int MI>
-__device__ __forceinline__ void store_bf16(const Ring& smem, const f32x16 (&acc)[MI][4],
-                                           uint16_t* out, int64_t ld, int rows, int cols) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
-  typedef Stage<32 * MI, 128> St;
-  lds_t* reg = smem.base + wave * St::kBytes;
+template <class G, int MI>
+__device__ __forceinline__ void store_bf16(const Ring& smem, const f32x16 (&acc)[MI][G::NJ],
+                                           const Waves<G, MI>& at, uint16_t* out, int64_t ld,
+                                           int rows, int cols) {
+  typedef Stage<32 * MI, 32 * G::NJ> St;
+  lds_t* reg = smem.base + at.w * St::kBytes;
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         St::put(reg, i, j, q, pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
                 pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
-  St::flush(reg, make_rsrc(out, (int64_t)rows * ld * 2), wm * 32 * MI, ld, wn * 128, cols);
+  St::flush(reg, make_rsrc(out, (int64_t)rows * ld * 2), at.m0, ld, at.nrow[0], cols);
 }
 
-// What is added to 32 rows of a wave's 128 columns, as it is stored: lane l has
-// eight columns of row 4 t + l / 16 in piece t.
+// What is added to 32 rows of a wave's 32 NJ columns, as it is stored: lane l has
+// eight columns of one of an access's 64 / kLanes rows.
+template <int NJ>
 struct Added {
-  u32x4 v[8];
+  static constexpr int kLanes = 4 * NJ, kRows = 64 / kLanes, kPieces = 32 / kRows;
+  u32x4 v[kPieces];
   __device__ __forceinline__ void load(const uint16_t* add, int64_t ld, int m0, int rows, int c0,
                                        int cols) {
-    const int lane = threadIdx.x & 63, c = c0 + 8 * (lane & 15);
+    const int lane = threadIdx.x & 63, c = c0 + 8 * (lane % kLanes);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int m = m0 + 4 * t + (lane >> 4);
+    for (int t = 0; t < kPieces; ++t) {
+      const int m = m0 + kRows * t + lane / kLanes;
       v[t] = u32x4{0, 0, 0, 0};
       if (m < rows && c < cols) v[t] = *(const u32x4*)(add + (int64_t)m * ld + c);
     }
@@ -807,59 +913,59 @@ struct Added {
 // accumulators' places, 8 bytes a lane and row, it cost 150 us of 32768 tokens'
 // 990); each 32 rows' loads are issued before the 32 rows in front are
 // finished.
-template <int MI, bool PART>
+template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& smem,
                                                 const LargeTile& t) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  typedef Waves<G, MI> Wv;
+  constexpr int NJ = G::NJ;
+  const Wv wv;
   const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
-  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
   const Steps k = steps_of<PART>(a, t, a.Hp / BK);
   const int64_t k0 = (int64_t)k.j0 * BK, at = (int64_t)t.m0 * a.H + n0;
-  RowTileT<2 * MI> la;
-  RowTile lb;
+  typename G::template Tiles<MI>::A la;
+  typename G::template Tiles<MI>::B lb;
   la.init(a.z + (int64_t)t.m0 * a.Hp + k0, a.Hp, t.rows);
   lb.init(a.w[2] + (int64_t)n0 * a.Hp + k0, a.Hp, cols);
-  f32x16 acc[MI][4];
-  const bool add = !PART && a.add;
-  product<MI>(la, lb, smem, k.n, acc, wm * 32 * MI, nrow);
+  f32x16 acc[MI][NJ];
+  product<G, MI>(la, lb, smem, k.n, acc, wv.m0, wv.nrow);
   if constexpr (PART) {
-    int64_t col[4];
-    int left[4];
+    int64_t col[NJ];
+    int left[NJ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      col[j] = n0 + nrow[j];
-      left[j] = cols - nrow[j];
+    for (int j = 0; j < NJ; ++j) {
+      col[j] = n0 + wv.nrow[j];
+      left[j] = cols - wv.nrow[j];
     }
-    store_f32<MI>(acc, a.part + ((int64_t)t.sp * a.T + t.m0) * a.H, a.H, t.rows, col, left);
+    store_f32<G, MI>(acc, wv, a.part + ((int64_t)t.sp * a.T + t.m0) * a.H, a.H, t.rows, col, left);
     return;
   }
-  if (!add) {
-    store_bf16<MI>(smem, acc, a.y + at, a.H, t.rows, cols);
+  if (!a.add) {
+    store_bf16<G, MI>(smem, acc, wv, a.y + at, a.H, t.rows, cols);
     return;
   }
   typedef __attribute__((address_space(3))) float lds_f;
-  constexpr int kRow = 132;                       // floats: 32 rows' pieces on distinct banks
-  lds_f* reg = (lds_f*)(smem.base + wave * (32 * kRow * 4));
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  typedef Added<NJ> Ad;
+  constexpr int kRow = 32 * NJ + 4;               // floats: 32 rows' pieces on distinct banks
+  lds_f* reg = (lds_f*)(smem.base + wv.w * (32 * kRow * 4));
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5, c0 = wv.nrow[0];
   const Rsrc ys = make_rsrc(a.y + at, (int64_t)t.rows * a.H * 2);
-  Added next;
-  next.load(a.add + at, a.H, wm * 32 * MI, t.rows, wn * 128, cols);
+  Ad next;
+  next.load(a.add + at, a.H, wv.m0, t.rows, c0, cols);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const Added now = next;
-    if (i + 1 < MI)
-      next.load(a.add + at, a.H, wm * 32 * MI + 32 * (i + 1), t.rows, wn * 128, cols);
+    const Ad now = next;
+    if (i + 1 < MI) next.load(a.add + at, a.H, wv.m0 + 32 * (i + 1), t.rows, c0, cols);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *(__attribute__((address_space(3))) f32x4*)(reg + lr * kRow + 32 * j + acc_col(q, lh)) =
             f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                   acc[i][j][4 * q + 3]};
-    const int c = 8 * (lane & 15);
+    const int c = 8 * (lane % Ad::kLanes);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int r = 4 * p + (lane >> 4);
+    for (int p = 0; p < Ad::kPieces; ++p) {
+      const int r = Ad::kRows * p + lane / Ad::kLanes;
       const lds_f* from = reg + r * kRow + c;
       const f32x4 s0 = *(const __attribute__((address_space(3))) f32x4*)from;
       const f32x4 s1 = *(const __attribute__((address_space(3))) f32x4*)(from + 4);
@@ -870,149 +976,150 @@ __device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& 
         const float hi = e < 2 ? s0[2 * (e & 1) + 1] : s1[2 * (e & 1) + 1];
         o[e] = pack_bf16x2(lo + bf16_of(now.v[p][e], 0), hi + bf16_of(now.v[p][e], 1));
       }
-      const int m = wm * 32 * MI + 32 * i + r;
-      const uint32_t off = wn * 128 + c < cols
-                               ? (uint32_t)(((int64_t)m * a.H + wn * 128 + c) * 2) : kOob;
+      const int m = wv.m0 + 32 * i + r;
+      const uint32_t off = c0 + c < cols ? (uint32_t)(((int64_t)m * a.H + c0 + c) * 2) : kOob;
       __builtin_amdgcn_raw_buffer_store_b128(o, ys, off, 0, 0);
     }
   }
 }
 
 // dZ in fp32: 256 columns of H', K = H.
-template <int MI, bool PART>
+template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const Waves<G, MI> at;
   const int n0 = t.nt * BN, cols = a.Hp - n0 < BN ? a.Hp - n0 : BN;
   const int nv0 = cols < 128 ? cols : 128;
-  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
-  RowTileT<2 * MI> la;
-  ColTile lb;
+  typename G::template Tiles<MI>::A la;
+  typename G::template Tiles<MI>::Col lb;
   la.init(a.dy + (int64_t)t.m0 * a.H, a.H, t.rows);
   lb.init(a.w[2] + n0, a.w[2] + n0 + 128, a.Hp, a.H, nv0, cols - nv0);
-  f32x16 acc[MI][4];
-  product<MI>(la, lb, smem, a.H / BK, acc, wm * 32 * MI, nrow);
-  int64_t col[4];
-  int left[4];
+  f32x16 acc[MI][G::NJ];
+  product<G, MI>(la, lb, smem, a.H / BK, acc, at.m0, at.nrow);
+  int64_t col[G::NJ];
+  int left[G::NJ];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    col[j] = n0 + nrow[j];
-    left[j] = cols - nrow[j];
+  for (int j = 0; j < G::NJ; ++j) {
+    col[j] = n0 + at.nrow[j];
+    left[j] = cols - at.nrow[j];
   }
-  store_f32<MI>(acc, a.dz + (int64_t)t.m0 * a.Hp, a.Hp, t.rows, col, left);
+  store_f32<G, MI>(acc, at, a.dz + (int64_t)t.m0 * a.Hp, a.Hp, t.rows, col, left);
 }
 
 // dG, dU and Z from the gate/up product and dZ.
-template <int MI, bool PART>
+template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  typedef Waves<G, MI> Wv;
+  constexpr int kHalf = Wv::kHalf;
+  const Wv wv;
   const int n0 = t.nt * 128, nv = a.Hp - n0 < 128 ? a.Hp - n0 : 128;
-  f32x16 acc[MI][4];
-  gateup_product<MI, false>(a, smem, t, acc, wm, wn);
+  f32x16 acc[MI][G::NJ];
+  gateup_product<G, MI, false>(a, smem, t, acc, wv);
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  typedef Stage<32 * MI, 64> St;
-  lds_t* reg_g = smem.base + wave * (2 * St::kBytes);
+  typedef Stage<32 * MI, 32 * kHalf> St;
+  lds_t* reg_g = smem.base + wv.w * (2 * St::kBytes);
   lds_t* reg_u = reg_g + St::kBytes;
   const int64_t at = (int64_t)t.m0 * a.Hp + n0, range = (int64_t)t.rows * a.Hp * 2;
   // Z is kept in the accumulators of U until dG and dU are stored
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    f32x4 dzv[2][4];
+    f32x4 dzv[kHalf][4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < kHalf; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int m = wm * 32 * MI + i * 32 + lr, n = wn * 64 + j * 32 + acc_col(q, lh);
+        const int m = wv.m0 + i * 32 + lr, n = wv.pair[j] + acc_col(q, lh);
         dzv[j][q] = f32x4{0, 0, 0, 0};
         if (m < t.rows && n < nv) dzv[j][q] = *(const f32x4*)(a.dz + at + (int64_t)m * a.Hp + n);
       }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < kHalf; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float dg[4], du[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float u = acc[i][j + 2][4 * q + e], d = dzv[j][q][e];
+          const float u = acc[i][j + kHalf][4 * q + e], d = dzv[j][q][e];
           const Act f = activate(a.act, acc[i][j][4 * q + e]);
           du[e] = d * f.f;
           dg[e] = d * u * f.df;
-          acc[i][j + 2][4 * q + e] = f.f * u;
+          acc[i][j + kHalf][4 * q + e] = f.f * u;
         }
         St::put(reg_g, i, j, q, pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
         St::put(reg_u, i, j, q, pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
       }
   }
-  St::flush(reg_g, make_rsrc(a.dg + at, range), wm * 32 * MI, a.Hp, wn * 64, nv);
+  St::flush(reg_g, make_rsrc(a.dg + at, range), wv.m0, a.Hp, wv.pair[0], nv);
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < kHalf; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         St::put(reg_g, i, j, q,
-                pack_bf16x2(acc[i][j + 2][4 * q], acc[i][j + 2][4 * q + 1]),
-                pack_bf16x2(acc[i][j + 2][4 * q + 2], acc[i][j + 2][4 * q + 3]));
-  St::flush(reg_u, make_rsrc(a.du + at, range), wm * 32 * MI, a.Hp, wn * 64, nv);
-  St::flush(reg_g, make_rsrc(a.z + at, range), wm * 32 * MI, a.Hp, wn * 64, nv);
+                pack_bf16x2(acc[i][j + kHalf][4 * q], acc[i][j + kHalf][4 * q + 1]),
+                pack_bf16x2(acc[i][j + kHalf][4 * q + 2], acc[i][j + kHalf][4 * q + 3]));
+  St::flush(reg_u, make_rsrc(a.du + at, range), wv.m0, a.Hp, wv.pair[0], nv);
+  St::flush(reg_g, make_rsrc(a.z + at, range), wv.m0, a.Hp, wv.pair[0], nv);
 }
 
 // dX: 256 columns of H, K = 2 H' over [dG | dU] and [Wg | Wu].
-template <int MI, bool PART>
+template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const Waves<G, MI> at;
   const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
-  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
-  RowTile2<2 * MI> la;
-  RowTile2<8> lb;
+  typename G::template Tiles<MI>::A2 la;
+  typename G::template Tiles<MI>::B2 lb;
   const int64_t ab = (int64_t)t.m0 * a.Hp, bb = (int64_t)n0 * a.Hp;
   la.init(a.dg + ab, a.du + ab, a.Hp, t.rows, a.Hp);
   lb.init(a.w[0] + bb, a.w[1] + bb, a.Hp, cols, a.Hp);
-  f32x16 acc[MI][4];
-  product<MI>(la, lb, smem, 2 * a.Hp / BK, acc, wm * 32 * MI, nrow);
-  store_bf16<MI>(smem, acc, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
+  f32x16 acc[MI][G::NJ];
+  product<G, MI>(la, lb, smem, 2 * a.Hp / BK, acc, at.m0, at.nrow);
+  store_bf16<G, MI>(smem, acc, at, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
 }
 
 // G, U and dZ of a middling number of tokens in one launch, in splits: tiles of
 // gate and up columns, then tiles of 256 columns of dZ, as two regions of 128
 // like the others.
-__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1))) void large_grad(LargeArgs a) {
-  MOONEP_RING(smem);
-  LargeTile t;
-  if (!large_tile(a, 128, &t)) return;
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1, gu = (a.Hp + 127) / 128;
+template <class G, int MI, bool PART>
+__device__ __forceinline__ void large_grad_tile(const LargeArgs& a, const Ring& smem,
+                                                const LargeTile& t) {
+  const Waves<G, MI> wv;
+  const int gu = (a.Hp + 127) / 128;
   const bool dz = t.nt >= gu;
   const int n0 = dz ? (t.nt - gu) * 256 : t.nt * 128, rest = a.Hp - n0;
   const int nv0 = rest < 128 ? rest : 128;
   const int nv1 = !dz ? nv0 : rest < 256 ? rest - nv0 : 128;
-  const int nrow[4] = {wn * 64, wn * 64 + 32, 128 + wn * 64, 128 + wn * 64 + 32};
-  const Steps k = steps_of<true>(a, t, a.H / BK);
+  const Steps k = steps_of<PART>(a, t, a.H / BK);
   const int64_t k0 = (int64_t)k.j0 * BK, at = k0 * a.Hp + n0;
-  RowTileT<4> la;
-  ColTile lb;
+  typename G::template Tiles<MI>::A la;
+  typename G::template Tiles<MI>::Col lb;
   la.init((dz ? a.dy : a.x) + (int64_t)t.m0 * a.H + k0, a.H, t.rows);
   lb.init(a.w[dz ? 2 : 0] + at, dz ? a.w[2] + at + 128 : a.w[1] + at, a.Hp, a.H - k0, nv0, nv1);
-  f32x16 acc[2][4];
-  product<2>(la, lb, smem, k.n, acc, wm * 64, nrow);
-  int64_t col[4];
-  int left[4];
+  f32x16 acc[MI][G::NJ];
+  product<G, MI>(la, lb, smem, k.n, acc, wv.m0, wv.pair);
+  int64_t col[G::NJ];
+  int left[G::NJ];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = wn * 64 + 32 * (j & 1);
-    col[j] = dz ? 2LL * a.Hp + n0 + (j >> 1) * 128 + c : (j >> 1) * (int64_t)a.Hp + n0 + c;
-    left[j] = ((j >> 1) ? nv1 : nv0) - c;
+  for (int j = 0; j < G::NJ; ++j) {
+    const int region = wv.pair[j] >> 7, c = wv.pair[j] & 127;
+    col[j] = (dz ? 2LL * a.Hp + region * 128 : region * (int64_t)a.Hp) + n0 + c;
+    left[j] = (region ? nv1 : nv0) - c;
   }
-  store_f32<2>(acc, a.part + ((int64_t)t.sp * a.T + t.m0) * 3 * a.Hp, 3LL * a.Hp, t.rows, col, left);
+  store_f32<G, MI>(acc, wv, a.part + ((int64_t)t.sp * a.T + t.m0) * 3 * a.Hp, 3LL * a.Hp, t.rows,
+                   col, left);
 }
 
 MOONEP_LARGE(large_gateup, large_gateup_tile)
+MOONEP_LARGE_128(large_gateup_splits, large_gateup_tile, true)
 MOONEP_LARGE(large_down, large_down_tile)
+MOONEP_LARGE_128(large_down_splits, large_down_tile, true)
 MOONEP_LARGE(large_dz, large_dz_tile)
 MOONEP_LARGE(large_gu, large_gu_tile)
 MOONEP_LARGE(large_dx, large_dx_tile)
+MOONEP_LARGE_128(large_grad_splits, large_grad_tile, true)
 
 // dW of the three projections: 256 x 256 tiles, the sum over the tokens.
 __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
@@ -1037,7 +1144,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
   void* out = p == 0 ? a.dw[0] : p == 1 ? a.dw[1] : a.dw[2];
   const int64_t at = (int64_t)m0 * a.Hp + n0;
   if (!a.f32) {
-    store_bf16<4>(smem, acc, (uint16_t*)out + at, a.Hp, mv, nv);
+    store_bf16<Four, 4>(smem, acc, Waves<Four, 4>(), (uint16_t*)out + at, a.Hp, mv, nv);
     return;
   }
   // read-modify-write, the 16 reads of a block row before its writes
@@ -1240,17 +1347,17 @@ LargeArgs with_shape(LargeArgs a, const Shape& s) {
   a.S = s.S;
   return a;
 }
-#define MOONEP_RUN_LARGE(kernel, shape, args)                                                      \
-  do {                                                                                             \
-    const LargeArgs la_ = with_shape(args, shape);                                                 \
-    if ((shape).rows == 256) kernel<4, false><<<blocks_of(shape), kThreads, 0, s>>>(la_);          \
-    else kernel<2, false><<<blocks_of(shape), kThreads, 0, s>>>(la_);                              \
+#define MOONEP_RUN_LARGE(kernel, shape, args)                                              \
+  do {                                                                                     \
+    const LargeArgs la_ = with_shape(args, shape);                                         \
+    if ((shape).rows == 256) kernel##_256<<<blocks_of(shape), 256, 0, s>>>(la_);           \
+    else kernel##_128<<<blocks_of(shape), 512, 0, s>>>(la_);                               \
   } while (0)
 // the same, or splits of 128-row tiles
-#define MOONEP_RUN_LARGE_SPLITS(kernel, shape, args)                                               \
-  do {                                                                                             \
-    if ((shape).S == 1) MOONEP_RUN_LARGE(kernel, shape, args);                                     \
-    else kernel<2, true><<<blocks_of(shape), kThreads, 0, s>>>(with_shape(args, shape));           \
+#define MOONEP_RUN_LARGE_SPLITS(kernel, shape, args)                                       \
+  do {                                                                                     \
+    if ((shape).S == 1) MOONEP_RUN_LARGE(kernel, shape, args);                             \
+    else kernel##_splits<<<blocks_of(shape), 512, 0, s>>>(with_shape(args, shape));        \
   } while (0)
 
 }  // namespace
@@ -1344,7 +1451,7 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
     MOONEP_RUN_LARGE(large_dz, z, big);
     MOONEP_RUN_LARGE(large_gu, g.s, big);
   } else if (g.s.large) {
-    large_grad<<<blocks_of(g.s), kThreads, 0, s>>>(with_shape(big, g.s));
+    large_grad_splits<<<blocks_of(g.s), 512, 0, s>>>(with_shape(big, g.s));
   } else {
     SmallArgs a = {};
     a.a[0] = x; a.a[2] = dy; a.b[0] = w[0]; a.b[1] = w[1]; a.b[2] = w[2];
