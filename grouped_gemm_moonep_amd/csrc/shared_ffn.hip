@@ -1064,18 +1064,56 @@ __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& sm
   St::flush(reg_g, make_rsrc(a.z + at, range), wv.m0, a.Hp, wv.pair[0], nv);
 }
 
+// A tile whose K range starts at k0 of another's (for splits of two matrices one after the other,
+// whose base cannot be moved).
+template <class T>
+struct From {
+  static constexpr bool kRows = T::kRows;
+  static constexpr int kLoads = T::kLoads;
+  T t;
+  int64_t k0;
+  __device__ __forceinline__ uint32_t koff(int64_t k) const { return t.koff(k0 + k); }
+  __device__ __forceinline__ void issue1(lds_t* tile, int i, uint32_t ko) const {
+    t.issue1(tile, i, ko);
+  }
+  __device__ __forceinline__ void issue(lds_t* tile, int64_t k, bool valid) const {
+    t.issue(tile, k0 + k, valid);
+  }
+  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int row, int kk, int lh) {
+    return T::frag(tile, row, kk, lh);
+  }
+};
+
 // dX: 256 columns of H, K = 2 H' over [dG | dU] and [Wg | Wu].
 template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
   const Waves<G, MI> at;
   const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
+  const int64_t ab = (int64_t)t.m0 * a.Hp, bb = (int64_t)n0 * a.Hp;
+  f32x16 acc[MI][G::NJ];
+  if constexpr (PART) {
+    const Steps k = steps_of<PART>(a, t, 2 * a.Hp / BK);
+    From<typename G::template Tiles<MI>::A2> la;
+    From<typename G::template Tiles<MI>::B2> lb;
+    la.k0 = lb.k0 = (int64_t)k.j0 * BK;
+    la.t.init(a.dg + ab, a.du + ab, a.Hp, t.rows, a.Hp);
+    lb.t.init(a.w[0] + bb, a.w[1] + bb, a.Hp, cols, a.Hp);
+    product<G, MI>(la, lb, smem, k.n, acc, at.m0, at.nrow);
+    int64_t col[G::NJ];
+    int left[G::NJ];
+#pragma unroll
+    for (int j = 0; j < G::NJ; ++j) {
+      col[j] = n0 + at.nrow[j];
+      left[j] = cols - at.nrow[j];
+    }
+    store_f32<G, MI>(acc, at, a.part + ((int64_t)t.sp * a.T + t.m0) * a.H, a.H, t.rows, col, left);
+    return;
+  }
   typename G::template Tiles<MI>::A2 la;
   typename G::template Tiles<MI>::B2 lb;
-  const int64_t ab = (int64_t)t.m0 * a.Hp, bb = (int64_t)n0 * a.Hp;
   la.init(a.dg + ab, a.du + ab, a.Hp, t.rows, a.Hp);
   lb.init(a.w[0] + bb, a.w[1] + bb, a.Hp, cols, a.Hp);
-  f32x16 acc[MI][G::NJ];
   product<G, MI>(la, lb, smem, 2 * a.Hp / BK, acc, at.m0, at.nrow);
   store_bf16<G, MI>(smem, acc, at, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
 }
@@ -1119,53 +1157,108 @@ MOONEP_LARGE_128(large_down_splits, large_down_tile, true)
 MOONEP_LARGE(large_dz, large_dz_tile)
 MOONEP_LARGE(large_gu, large_gu_tile)
 MOONEP_LARGE(large_dx, large_dx_tile)
+MOONEP_LARGE_128(large_dx_splits, large_dx_tile, true)
 MOONEP_LARGE_128(large_grad_splits, large_grad_tile, true)
 
-// dW of the three projections: 256 x 256 tiles, the sum over the tokens.
-__global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
-                          amdgpu_waves_per_eu(1, 1))) void large_wgrad(LargeArgs a) {
-  MOONEP_RING(smem);
-  const int64_t each = (int64_t)a.ntm * a.ntn, total = 3 * each, per = (total + kXcds - 1) / kXcds;
-  const int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+// dW of the three projections, the sum over the tokens: tiles of 256 columns of
+// H' and 256 rows of H by four waves, or 128 by eight.
+struct ColTileA8 {       // 128 columns loaded by eight waves, laid out as a region of ColTile
+  static constexpr bool kRows = false;
+  static constexpr int kLoads = 2;
+  DmaRsrc rs;
+  uint32_t voff, ld2, wlds;
+  __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t k_total, int nv) {
+    const int w = wave_id(), lane = threadIdx.x & 63;
+    rs = make_dma_rsrc(src, k_total * ld * 2);
+    ld2 = (uint32_t)(ld * 2);
+    const int k = 8 * w + (lane >> 4);               // load i adds 4 i rows
+    const int col = 8 * ((lane & 15) ^ (4 * (k & 3)));
+    voff = col < nv ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
+    wlds = (uint32_t)(w * 2 * 1024);
+  }
+  __device__ __forceinline__ uint32_t koff(int64_t k0) const { return (uint32_t)(k0 * ld2); }
+  __device__ __forceinline__ void issue1(lds_t* tile, int i, uint32_t ko) const {
+    load_lds(rs, tile + wlds + i * 1024, voff + (ko + (uint32_t)(4 * i) * ld2));
+  }
+  __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
+    const uint32_t ko = valid ? koff(k0) : kOob;
+    issue1(tile, 0, ko);
+    issue1(tile, 1, ko);
+  }
+  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
+    return ColTile::frag(tile, nb, kk, lh);
+  }
+};
+
+template <class G, int MI, bool PART>
+__device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem) {
+  constexpr int kM = G::kWaves == 4 ? 256 : 128, NJ = G::NJ;
+  const int64_t each = (int64_t)a.ntm * a.ntn, total = 3 * each * a.S;
+  const int64_t per = (total + kXcds - 1) / kXcds;
+  int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
   if (blockIdx.x / kXcds >= per || l >= total) return;
+  LargeTile t;
+  t.sp = (int)(l / (3 * each));
+  l -= t.sp * 3 * each;
   const int p = (int)(l / each), rem = (int)(l % each);
-  const int m0 = rem / a.ntn * BM, n0 = rem % a.ntn * BN;
-  const int mv = a.H - m0 < BM ? a.H - m0 : BM, nv = a.Hp - n0 < BN ? a.Hp - n0 : BN;
-  const int mv0 = mv < 128 ? mv : 128, nv0 = nv < 128 ? nv : 128;
-  const uint16_t* A = (p == 2 ? a.dy : a.x) + m0;
-  const uint16_t* Bm = (p == 0 ? a.dg : p == 1 ? a.du : a.z) + n0;
-  const int wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
-  const int nrow[4] = {wn * 128, wn * 128 + 32, wn * 128 + 64, wn * 128 + 96};
-  ColTile la, lb;
-  la.init(A, A + 128, a.H, a.T, mv0, mv - mv0);
-  lb.init(Bm, Bm + 128, a.Hp, a.T, nv0, nv - nv0);
-  f32x16 acc[4][4];
-  gemm_loop<4>(la, lb, smem, (a.T + BK - 1) / BK, acc, wm * 128, nrow);
-  void* out = p == 0 ? a.dw[0] : p == 1 ? a.dw[1] : a.dw[2];
+  const int m0 = rem / a.ntn * kM, n0 = rem % a.ntn * BN;
+  const int mv = a.H - m0 < kM ? a.H - m0 : kM, nv = a.Hp - n0 < BN ? a.Hp - n0 : BN;
+  const int nv0 = nv < 128 ? nv : 128;
+  const Steps k = steps_of<PART>(a, t, (a.T + BK - 1) / BK);
+  const int64_t k0 = (int64_t)k.j0 * BK;
+  const uint16_t* A = (p == 2 ? a.dy : a.x) + k0 * a.H + m0;
+  const uint16_t* Bm = (p == 0 ? a.dg : p == 1 ? a.du : a.z) + k0 * a.Hp + n0;
+  const Waves<G, MI> wv;
+  typename G::template Tiles<MI>::Col lb;
+  lb.init(Bm, Bm + 128, a.Hp, a.T - k0, nv0, nv - nv0);
+  f32x16 acc[MI][NJ];
+  if constexpr (G::kWaves == 4) {
+    const int mv0 = mv < 128 ? mv : 128;
+    ColTile la;
+    la.init(A, A + 128, a.H, a.T - k0, mv0, mv - mv0);
+    product<G, MI>(la, lb, smem, k.n, acc, wv.m0, wv.nrow);
+  } else {
+    ColTileA8 la;
+    la.init(A, a.H, a.T - k0, mv);
+    product<G, MI>(la, lb, smem, k.n, acc, wv.m0, wv.nrow);
+  }
   const int64_t at = (int64_t)m0 * a.Hp + n0;
-  if (!a.f32) {
-    store_bf16<Four, 4>(smem, acc, Waves<Four, 4>(), (uint16_t*)out + at, a.Hp, mv, nv);
+  if constexpr (PART) {
+    int64_t col[NJ];
+    int left[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      col[j] = wv.nrow[j];
+      left[j] = nv - wv.nrow[j];
+    }
+    float* out = a.part + ((int64_t)t.sp * 3 + p) * a.H * a.Hp + at;
+    store_f32<G, MI>(acc, wv, out, a.Hp, mv, col, left);
     return;
   }
-  // read-modify-write, the 16 reads of a block row before its writes
+  void* out = p == 0 ? a.dw[0] : p == 1 ? a.dw[1] : a.dw[2];
+  if (!a.f32) {
+    store_bf16<G, MI>(smem, acc, wv, (uint16_t*)out + at, a.Hp, mv, nv);
+    return;
+  }
+  // read-modify-write, the reads of a block row before its writes
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = wm * 128 + i * 32 + lr;
+  for (int i = 0; i < MI; ++i) {
+    const int m = wv.m0 + i * 32 + lr;
     float* row = (float*)out + at + (int64_t)m * a.Hp;
-    f32x4 v[4][4];
+    f32x4 v[NJ][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n = nrow[j] + acc_col(q, lh);
+        const int n = wv.nrow[j] + acc_col(q, lh);
         if (m < mv && n < nv) v[j][q] = *(const f32x4*)(row + n);
       }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n = nrow[j] + acc_col(q, lh);
+        const int n = wv.nrow[j] + acc_col(q, lh);
         if (m < mv && n < nv) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[j][q][e] += acc[i][j][4 * q + e];
@@ -1173,6 +1266,21 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kThreads, kThreads),
         }
       }
   }
+}
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
+                          amdgpu_waves_per_eu(1, 1))) void large_wgrad_256(LargeArgs a) {
+  MOONEP_RING(smem);
+  wgrad_tile<Four, 4, false>(a, smem);
+}
+__global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
+                          amdgpu_waves_per_eu(2, 2))) void large_wgrad_128(LargeArgs a) {
+  MOONEP_RING(smem);
+  wgrad_tile<Eight, 2, false>(a, smem);
+}
+__global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
+                          amdgpu_waves_per_eu(2, 2))) void large_wgrad_splits(LargeArgs a) {
+  MOONEP_RING(smem);
+  wgrad_tile<Eight, 2, true>(a, smem);
 }
 
 // ------------------------------------------------------------- choice
@@ -1202,6 +1310,12 @@ int large_splits(int64_t tiles, int nk) {
   return tiles * S >= 192 && nk / S >= 16 ? (int)S : 0;
 }
 
+// Microseconds of so many large tiles, a round of one per CU after the other: about what the two
+// kinds took for 20000 tokens of H or H' 64 to 2560 and 2560, and for 32768 of 7168 x 2048.  A
+// 128-row tile's start and end cost less, and its rounds are finer; many steps favour 256 rows.
+double cost256(int64_t tiles, int nk) { return ceil_div(tiles, 256) * (12.0 + 1.45 * nk); }
+double cost128(int64_t tiles, int nk) { return ceil_div(tiles, 256) * (5.0 + 0.85 * nk); }
+
 // A product of M rows in tiles of so many columns, K in nk steps of 64.  `half`: 128-row large
 // tiles may be cut into splits.
 Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk, bool half) {
@@ -1212,7 +1326,7 @@ Shape pick(int64_t M, int64_t cols_small, int64_t cols_large, int nk, bool half)
   const int S = half && n128 < 192 ? large_splits(n128, nk) : 0;
   s.large = n128 >= 192 || S > 0;
   if (s.large) {
-    s.rows = n256 >= 192 ? 256 : 128;
+    s.rows = S == 0 && cost256(n256, nk) < cost128(n128, nk) ? 256 : 128;
     s.ntn = (int)cols_large;
     if (S > 0) s.S = S;
   } else {
@@ -1230,7 +1344,7 @@ Shape down_shape(int64_t T, int H, int Hp) {
   return pick(T, ceil_div(H, 128), ceil_div(H, 256), Hp / BK, true);
 }
 Shape dx_shape(int64_t T, int H, int Hp) {
-  return pick(T, ceil_div(H, 128), ceil_div(H, 256), 2 * Hp / BK, false);
+  return pick(T, ceil_div(H, 128), ceil_div(H, 256), 2 * Hp / BK, true);
 }
 // dG, dU, Z: tiles of gate and up; small ones, and 128-row large ones in splits (`parts`), with
 // those of dZ in the same launch.
@@ -1249,16 +1363,17 @@ GradShape grad_shape(int64_t T, int H, int Hp) {
 }
 Shape wgrad_shape(int64_t T, int H, int Hp) {
   const int nk = (int)ceil_div(T, BK);
-  Shape s;
-  s.S = 1;
-  s.large = 3 * ceil_div(H, 256) * ceil_div(Hp, 256) >= 192;
-  s.rows = s.large ? 256 : 128;
-  s.ntm = (int)ceil_div(H, s.rows);
-  s.ntn = (int)ceil_div(Hp, s.rows);
-  if (!s.large) {
-    s.ntn *= 3;
-    s.S = splits((int64_t)s.ntm * s.ntn, nk);
+  const int cols = (int)ceil_div(Hp, 256), m256 = (int)ceil_div(H, 256), m128 = (int)ceil_div(H, 128);
+  const int64_t n256 = 3LL * m256 * cols, n128 = 3LL * m128 * cols;
+  const int S = n128 < 192 ? large_splits(n128, nk) : 1;
+  if (S > 0) {
+    // near a tie the larger tiles' whole rows store faster (512 tokens of 7168 x 2048: the whole
+    // backward 179 us, with 128-row ones 185 us)
+    if (S == 1 && cost256(n256, nk) < 1.05 * cost128(n128, nk)) return {true, 256, m256, cols, 1};
+    return {true, 128, m128, cols, S};
   }
+  Shape s = {false, 128, m128, 3 * (int)ceil_div(Hp, 128), 1};
+  s.S = splits((int64_t)s.ntm * s.ntn, nk);
   return s;
 }
 
@@ -1296,8 +1411,8 @@ BwdWs bwd_ws(int64_t T, int H, int Hp) {
   const GradShape g = grad_shape(T, H, Hp);
   const Shape x = dx_shape(T, H, Hp), d = wgrad_shape(T, H, Hp);
   int64_t p = g.parts ? (int64_t)g.s.S * T * 3 * Hp * 4 : T * Hp * 4;
-  if (!x.large && x.S > 1 && (int64_t)x.S * T * H * 4 > p) p = (int64_t)x.S * T * H * 4;
-  if (!d.large && d.S > 1 && (int64_t)d.S * 3 * H * Hp * 4 > p) p = (int64_t)d.S * 3 * H * Hp * 4;
+  if (x.S > 1 && (int64_t)x.S * T * H * 4 > p) p = (int64_t)x.S * T * H * 4;
+  if (d.S > 1 && (int64_t)d.S * 3 * H * Hp * 4 > p) p = (int64_t)d.S * 3 * H * Hp * 4;
   w.total = w.part + round256(p);
   return w;
 }
@@ -1479,24 +1594,24 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
   }
   if (dx) {
     if (dxs.large) {
-      MOONEP_RUN_LARGE(large_dx, dxs, big);
+      MOONEP_RUN_LARGE_SPLITS(large_dx, dxs, big);
     } else {
       run_small<OP_ROWS2>(dxs, dxs.S > 1, xa, s);
-      if (dxs.S > 1) join_rows<<<joins(T * H), kJoin, 0, s>>>(part, dxs.S, T * H, nullptr, dx);
     }
+    if (dxs.S > 1) join_rows<<<joins(T * H), kJoin, 0, s>>>(part, dxs.S, T * H, nullptr, dx);
   }
   if (dw) {
     if (ws_.large) {
-      LargeArgs a = big;
-      a.ntm = ws_.ntm;
-      a.ntn = ws_.ntn;
-      large_wgrad<<<(unsigned)(ceil_div(3LL * a.ntm * a.ntn, kXcds) * kXcds), kThreads, 0, s>>>(a);
+      const LargeArgs a = with_shape(big, ws_);
+      const unsigned n = (unsigned)(ceil_div(3LL * a.ntm * a.ntn * a.S, kXcds) * kXcds);
+      if (ws_.rows == 256) large_wgrad_256<<<n, 256, 0, s>>>(a);
+      else if (ws_.S == 1) large_wgrad_128<<<n, 512, 0, s>>>(a);
+      else large_wgrad_splits<<<n, 512, 0, s>>>(a);
     } else {
       run_small<OP_WGRAD>(ws_, ws_.S > 1, wa, s);
-      const int64_t n = (int64_t)H * Hp;
-      if (ws_.S > 1)
-        join_wgrad<<<dim3(joins(n), 3), kJoin, 0, s>>>(part, ws_.S, n, big.f32, j);
     }
+    const int64_t n = (int64_t)H * Hp;
+    if (ws_.S > 1) join_wgrad<<<dim3(joins(n), 3), kJoin, 0, s>>>(part, ws_.S, n, big.f32, j);
   }
   return hipGetLastError();
 }
