@@ -81,6 +81,7 @@ def lib():
                                        ctypes.c_float, vp, vp, i64, vp]),
         "moonep_shared_ffn_ws": (i64, [i64, i32, i32]),
         "moonep_shared_ffn": (i32, [vp, P3, i32, vp, i64, i32, i32, vp, vp, i64, vp]),
+        "moonep_shared_ffn_tile": (i32, [i64, i32, i32, i32, ctypes.POINTER(i32)]),
         "moonep_shared_ffn_bwd_ws": (i64, [i64, i32, i32]),
         "moonep_shared_ffn_bwd": (i32, [vp, vp, P3, i32, i64, i32, i32, vp, ctypes.POINTER(vp), i32,
                                         vp, i64, vp]),
@@ -145,6 +146,10 @@ def plan_len(cfg: MoonepConfig, which: int) -> int:
  GRID_COMBINE_BWD) = range(6)
 F32, BF16 = range(2)
 SCORES = {"softmax": 0, "sigmoid": 1}
+FFN_PRODUCTS = FFN_GATEUP, FFN_DOWN, FFN_GRAD, FFN_DX, FFN_WGRAD = tuple(range(5))
+(FFN_TILE_32, FFN_TILE_64, FFN_TILE_128, FFN_TILE_128X256, FFN_TILE_256X256,
+ FFN_TILE_FEW) = range(6)
+FFN_TILE_DEEP = 8
 ACTS = {"silu": 0, "gelu_tanh": 1}
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = range(4)
 ORTHO_MAX_STEPS, ORTHO_MAX_GAIN = 16, 2048
@@ -158,6 +163,12 @@ def launch_grid(cfg: MoonepConfig, which: int, W: int = 0, device_cus: int = 256
 
 
 PTR3 = ctypes.c_void_p * 3
+
+
+def shared_ffn_tile(T: int, H: int, Hp: int, product: int):
+    """(tile, splits) of a product of the shared expert (host only)."""
+    splits = ctypes.c_int32()
+    return int(lib().moonep_shared_ffn_tile(T, H, Hp, product, ctypes.byref(splits))), splits.value
 
 
 def ptr3(ts):

@@ -394,6 +394,14 @@ moonep_status_t moonep_shared_ffn(const uint16_t* x, const uint16_t* const w[3],
   return hip_status(launch_shared_ffn(x, w, act, add, T, H, Hp, y, (char*)ws, stream));
 }
 
+int32_t moonep_shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product,
+                               int32_t* splits) {
+  const bool fwd = product == MOONEP_FFN_GATEUP || product == MOONEP_FFN_DOWN;
+  if (!splits || T < 1 || !(fwd ? shared_ffn_shape_ok : shared_ffn_bwd_shape_ok)(T, H, Hp))
+    return -1;
+  return shared_ffn_tile(T, H, Hp, product, splits);
+}
+
 int64_t moonep_shared_ffn_bwd_ws(int64_t T, int32_t H, int32_t Hp) {
   return shared_ffn_bwd_shape_ok(T, H, Hp) ? shared_ffn_bwd_ws_bytes(T, H, Hp) : -1;
 }

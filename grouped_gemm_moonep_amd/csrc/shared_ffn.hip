@@ -1450,6 +1450,8 @@ void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
   } else if (s.rows == 64) {
     if (part || kPart) run_small_as<OP, 64, true>(s, a, st);
     else run_small_as<OP, 64, kPart>(s, a, st);
+  } else if constexpr (OP == OP_ROWS) {            // what few() leaves: long sums, few columns
+    small_kernel<OP, 32, true, true><<<blocks_of(s), kThreads, 0, st>>>(a);
   } else {
     if (part || kPart) run_small_as<OP, 32, true>(s, a, st);
     else run_small_as<OP, 32, kPart>(s, a, st);
@@ -1489,6 +1491,27 @@ int64_t shared_ffn_ws_bytes(int64_t T, int32_t H, int32_t Hp) {
 }
 int64_t shared_ffn_bwd_ws_bytes(int64_t T, int32_t H, int32_t Hp) {
   return T == 0 ? 0 : bwd_ws(T, H, Hp).total;
+}
+
+int32_t shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product, int32_t* splits) {
+  Shape s;
+  switch (product) {
+    case MOONEP_FFN_GATEUP: s = gateup_shape(T, H, Hp); break;
+    case MOONEP_FFN_DOWN: s = down_shape(T, H, Hp); break;
+    case MOONEP_FFN_GRAD: s = grad_shape(T, H, Hp).s; break;
+    case MOONEP_FFN_DX: s = dx_shape(T, H, Hp); break;
+    case MOONEP_FFN_WGRAD: s = wgrad_shape(T, H, Hp); break;
+    default: return -1;
+  }
+  *splits = s.S;
+  if (product == MOONEP_FFN_DOWN && few(T, H, Hp)) {
+    *splits = 1;
+    return MOONEP_FFN_TILE_FEW;
+  }
+  if (s.large) return s.rows == 256 ? MOONEP_FFN_TILE_256X256 : MOONEP_FFN_TILE_128X256;
+  const int32_t t = s.rows == 32 ? MOONEP_FFN_TILE_32 : s.rows == 64 ? MOONEP_FFN_TILE_64
+                                                                     : MOONEP_FFN_TILE_128;
+  return t + (deep(s) ? MOONEP_FFN_TILE_DEEP : 0);
 }
 
 hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,

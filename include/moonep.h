@@ -455,6 +455,23 @@ moonep_status_t moonep_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
                                       int32_t dw_dtype, void* ws, int64_t ws_bytes,
                                       hipStream_t stream);
 
+/* Tile (MOONEP_FFN_TILE_*) that a product (MOONEP_FFN_*) of T >= 1 tokens is
+ * computed in, and into how many splits its sums are cut (host only): GATEUP and
+ * DOWN of the forward; of the backward GRAD (G, U and dZ), DX and WGRAD.  The
+ * small tiles are 32, 64 or 128 rows by 128 columns, plus MOONEP_FFN_TILE_DEEP
+ * where their loads run further ahead.  -1 for sizes or a product that there is
+ * not, or a NULL splits. */
+enum {
+  MOONEP_FFN_GATEUP = 0, MOONEP_FFN_DOWN, MOONEP_FFN_GRAD, MOONEP_FFN_DX, MOONEP_FFN_WGRAD
+};
+enum {
+  MOONEP_FFN_TILE_32 = 0, MOONEP_FFN_TILE_64, MOONEP_FFN_TILE_128,
+  MOONEP_FFN_TILE_128X256, MOONEP_FFN_TILE_256X256,
+  MOONEP_FFN_TILE_FEW,         /* up to 32 tokens, K shared by a workgroup's waves */
+  MOONEP_FFN_TILE_DEEP = 8
+};
+int32_t moonep_shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product, int32_t* splits);
+
 /* A block's end and the next one's start in one pass (the framework-side steps
  * between combine and the next block): for T rows of W elements, with
  * rstd(v) = 1 / sqrt(mean(v^2) + eps),

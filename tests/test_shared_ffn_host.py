@@ -1,12 +1,15 @@
 """Host-only checks of shared_ffn and its backward (no GPU needed): what they
 refuse before anything is enqueued, and workspace sizes."""
 import ctypes
+import math
+import random
 
 import pytest
 import torch
 
 import grouped_gemm_moonep_amd as moonep
 from grouped_gemm_moonep_amd import _abi
+from shared_ffn_cases import CASES, taken
 
 ARG, CONFIG, SCRATCH, OK = (_abi.MOONEP_ERR_ARG, _abi.MOONEP_ERR_CONFIG, _abi.MOONEP_ERR_SCRATCH,
                             _abi.MOONEP_OK)
@@ -103,3 +106,26 @@ def test_binding_refuses():
         moonep.shared_ffn_workspace(4, 96, 64, device="cpu")
     with pytest.raises(moonep.MoonepError):
         moonep.shared_ffn_bwd_workspace(1 << 20, 7168, 64, device="cpu")
+
+
+def test_cases_take_every_tile():
+    """The sizes that the GPU test runs cover what any size takes."""
+    covered = set().union(*(taken(*c) for c in CASES))
+    rng = random.Random(7)
+    size = lambda top: 64 * int(round(math.exp(rng.uniform(0, math.log(top)))))
+    for _ in range(40000):
+        H, Hp = size(1024), size(1024)
+        T = int(round(math.exp(rng.uniform(0, math.log(1 << 17)))))
+        if H * Hp < 1 << 30:
+            assert taken(T, H, Hp) <= covered, (T, H, Hp)
+
+
+def test_tile_query_refuses():
+    lib, n = _abi.lib(), ctypes.c_int32()
+    f = lib.moonep_shared_ffn_tile
+    assert f(4, 64, 64, 0, ctypes.byref(n)) >= 0 and n.value == 1
+    for bad in ((0, 64, 64, 0), (4, 96, 64, 0), (4, 64, 0, 1), (4, 64, 64, 5), (4, 64, 64, -1),
+                (1 << 24, 64, 64, 2)):
+        assert f(*bad, ctypes.byref(n)) == -1
+    assert f(1 << 24, 64, 64, 0, ctypes.byref(n)) >= 0      # the forward takes more tokens
+    assert f(4, 64, 64, 0, None) == -1
