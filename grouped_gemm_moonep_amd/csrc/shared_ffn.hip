@@ -383,12 +383,13 @@ __global__ __launch_bounds__(kThreads, DEEP ? 1 : 2) void small_kernel(SmallArgs
 
 // dX and the weight gradients, which both need dG and dU and not each other, in
 // one launch: the first nx workgroups are dX's.
-template <int BM>
-__global__ __launch_bounds__(kThreads, 2) void small_last(SmallArgs x, SmallArgs w, unsigned nx) {
-  constexpr int kX = Small<BM, false>::kLds, kW = Small<128, false>::kLds;
+template <int BM, bool DEEP>
+__global__ __launch_bounds__(kThreads, DEEP ? 1 : 2) void small_last(SmallArgs x, SmallArgs w,
+                                                                     unsigned nx) {
+  constexpr int kX = Small<BM, DEEP>::kLds, kW = Small<128, DEEP>::kLds;
   __shared__ __attribute__((aligned(16))) char smem[kX > kW ? kX : kW];
-  if (blockIdx.x < nx) small_tile<OP_ROWS2, BM, false, false>(x, blockIdx.x, smem);
-  else small_tile<OP_WGRAD, 128, false, false>(w, blockIdx.x - nx, smem);
+  if (blockIdx.x < nx) small_tile<OP_ROWS2, BM, false, DEEP>(x, blockIdx.x, smem);
+  else small_tile<OP_WGRAD, 128, false, DEEP>(w, blockIdx.x - nx, smem);
 }
 
 // Z Wd^T (+ add) of up to 32 tokens without splits between workgroups: a
@@ -727,10 +728,11 @@ struct LargeTile {
 };
 // M-tiles of `height` rows in groups of eight, each group swept over the
 // N-tiles, as in gemm_core.h: what runs together on an XCD shares weight slabs.
-__device__ __forceinline__ bool large_tile(const LargeArgs& a, int height, LargeTile* t) {
+__device__ __forceinline__ bool large_tile(const LargeArgs& a, int height, LargeTile* t,
+                                           unsigned block) {
   const int64_t each = (int64_t)a.ntm * a.ntn, total = each * a.S, per = (total + kXcds - 1) / kXcds;
-  int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  if (blockIdx.x / kXcds >= per || l >= total) return false;
+  int64_t l = (int64_t)(block % kXcds) * per + block / kXcds;
+  if (block / kXcds >= per || l >= total) return false;
   t->sp = (int)(l / each);
   l -= t->sp * each;
   const int group = (int)(l / (8LL * a.ntn));
@@ -769,7 +771,7 @@ struct Waves {
                             amdgpu_waves_per_eu(1, 1))) void name##_256(LargeArgs a) {     \
     MOONEP_RING(smem);                                                                     \
     LargeTile t;                                                                           \
-    if (!large_tile(a, 256, &t)) return;                                                   \
+    if (!large_tile(a, 256, &t, blockIdx.x)) return;                                                \
     if (t.rows <= kHalfTileM) body<Four, 2, false>(a, smem, t);                            \
     else body<Four, 4, false>(a, smem, t);                                                 \
   }                                                                                        \
@@ -780,7 +782,7 @@ struct Waves {
                             amdgpu_waves_per_eu(2, 2))) void name(LargeArgs a) {           \
     MOONEP_RING(smem);                                                                     \
     LargeTile t;                                                                           \
-    if (!large_tile(a, 128, &t)) return;                                                   \
+    if (!large_tile(a, 128, &t, blockIdx.x)) return;                                                \
     body<Eight, 2, PART>(a, smem, t);                                                      \
   }
 
@@ -1191,12 +1193,12 @@ struct ColTileA8 {       // 128 columns loaded by eight waves, laid out as a reg
 };
 
 template <class G, int MI, bool PART>
-__device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem) {
+__device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem, unsigned block) {
   constexpr int kM = G::kWaves == 4 ? 256 : 128, NJ = G::NJ;
   const int64_t each = (int64_t)a.ntm * a.ntn, total = 3 * each * a.S;
   const int64_t per = (total + kXcds - 1) / kXcds;
-  int64_t l = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  if (blockIdx.x / kXcds >= per || l >= total) return;
+  int64_t l = (int64_t)(block % kXcds) * per + block / kXcds;
+  if (block / kXcds >= per || l >= total) return;
   LargeTile t;
   t.sp = (int)(l / (3 * each));
   l -= t.sp * 3 * each;
@@ -1270,17 +1272,43 @@ __device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem)
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
                           amdgpu_waves_per_eu(1, 1))) void large_wgrad_256(LargeArgs a) {
   MOONEP_RING(smem);
-  wgrad_tile<Four, 4, false>(a, smem);
+  wgrad_tile<Four, 4, false>(a, smem, blockIdx.x);
 }
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
                           amdgpu_waves_per_eu(2, 2))) void large_wgrad_128(LargeArgs a) {
   MOONEP_RING(smem);
-  wgrad_tile<Eight, 2, false>(a, smem);
+  wgrad_tile<Eight, 2, false>(a, smem, blockIdx.x);
 }
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
                           amdgpu_waves_per_eu(2, 2))) void large_wgrad_splits(LargeArgs a) {
   MOONEP_RING(smem);
-  wgrad_tile<Eight, 2, true>(a, smem);
+  wgrad_tile<Eight, 2, true>(a, smem, blockIdx.x);
+}
+
+// The weight gradients and dX, which both need dG and dU and not each other, in
+// one launch where their tiles are alike: dX's shorter tiles fill what the last
+// round of the others leaves idle (a multiple of the XCDs, nw workgroups, is the
+// weight gradients').
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
+                          amdgpu_waves_per_eu(1, 1))) void large_last_256(LargeArgs w, LargeArgs x,
+                                                                          unsigned nw) {
+  MOONEP_RING(smem);
+  if (blockIdx.x < nw) {
+    wgrad_tile<Four, 4, false>(w, smem, blockIdx.x);
+    return;
+  }
+  LargeTile t;
+  if (!large_tile(x, 256, &t, blockIdx.x - nw)) return;
+  if (t.rows <= kHalfTileM) large_dx_tile<Four, 2, false>(x, smem, t);
+  else large_dx_tile<Four, 4, false>(x, smem, t);
+}
+__global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
+                          amdgpu_waves_per_eu(2, 2))) void large_last_128(LargeArgs w, LargeArgs x,
+                                                                          unsigned nw) {
+  MOONEP_RING(smem);
+  LargeTile t;
+  if (blockIdx.x < nw) wgrad_tile<Eight, 2, false>(w, smem, blockIdx.x);
+  else if (large_tile(x, 128, &t, blockIdx.x - nw)) large_dx_tile<Eight, 2, false>(x, smem, t);
 }
 
 // ------------------------------------------------------------- choice
@@ -1458,6 +1486,12 @@ void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
   }
 }
 
+template <int BM>
+void run_last(unsigned n, const SmallArgs& x, const SmallArgs& w, unsigned nx, hipStream_t st) {
+  if (n <= 256) small_last<BM, true><<<n, kThreads, 0, st>>>(x, w, nx);
+  else small_last<BM, false><<<n, kThreads, 0, st>>>(x, w, nx);
+}
+
 LargeArgs with_shape(LargeArgs a, const Shape& s) {
   a.ntm = s.ntm;
   a.ntn = s.ntn;
@@ -1610,9 +1644,17 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
   if (dx && dw && !dxs.large && dxs.S == 1 && !ws_.large && ws_.S == 1) {
     const SmallArgs ax = with_shape(xa, dxs), aw = with_shape(wa, ws_);
     const unsigned nx = blocks_of(dxs), n = nx + blocks_of(ws_);
-    if (dxs.rows == 128) small_last<128><<<n, kThreads, 0, s>>>(ax, aw, nx);
-    else if (dxs.rows == 64) small_last<64><<<n, kThreads, 0, s>>>(ax, aw, nx);
-    else small_last<32><<<n, kThreads, 0, s>>>(ax, aw, nx);
+    if (dxs.rows == 128) run_last<128>(n, ax, aw, nx, s);
+    else if (dxs.rows == 64) run_last<64>(n, ax, aw, nx, s);
+    else run_last<32>(n, ax, aw, nx, s);
+    return hipGetLastError();
+  }
+  if (dx && dw && dxs.large && ws_.large && dxs.S == 1 && ws_.S == 1 && dxs.rows == ws_.rows) {
+    const LargeArgs ax = with_shape(big, dxs), aw = with_shape(big, ws_);
+    const unsigned nw = (unsigned)(ceil_div(3LL * ws_.ntm * ws_.ntn, kXcds) * kXcds);
+    const unsigned n = nw + blocks_of(dxs);
+    if (ws_.rows == 256) large_last_256<<<n, 256, 0, s>>>(aw, ax, nw);
+    else large_last_128<<<n, 512, 0, s>>>(aw, ax, nw);
     return hipGetLastError();
   }
   if (dx) {
