@@ -333,6 +333,54 @@ def time_backward(w, buf, plan, batches, x_nvs, z_ws, home, pool, steps, warmup,
                    "the bf16 operand rows once; steps cycle the same maxvio targets")
     out["weighted"] = time_weighted(w, buf, plan, x, dout, x_nvs, dy_nvs, dx_nvs, z_ws, home, pool,
                                     grads[0], flush)
+    out["block"] = time_block(w, x, dout, flush)
+    return out
+
+
+def time_block(w, x, dout, flush):
+    """The steps of a block around the experts, for all ranks' tokens: the norms
+    with residual (two outputs, norms on both sides, a gate per channel) and the
+    shared expert of one expert's size, forward and backward.  Medians of five,
+    the cache flushed before each."""
+    import torch
+    from grouped_gemm_moonep_amd import (block_norm, block_norm_bwd, block_norm_bwd_workspace,
+                                         shared_ffn, shared_ffn_bwd, shared_ffn_bwd_workspace,
+                                         shared_ffn_workspace)
+    dev, tokens = x.device, w.R * w.S
+    g = torch.Generator(device=dev).manual_seed(3)
+    weights = [(torch.randn((w.H, w.Hp), generator=g, device=dev) * 0.02).to(torch.bfloat16)
+               for _ in range(3)]
+    routed, h = torch.randn_like(x), torch.randn_like(x)
+    form = dict(gate=torch.rand((w.H,), generator=g, device=dev),
+                w_post=torch.ones((w.H,), device=dev), w_pre=torch.ones((w.H,), device=dev), scale=0.5)
+    ws = shared_ffn_workspace(tokens, w.H, w.Hp, device=dev)
+    wsb = shared_ffn_bwd_workspace(tokens, w.H, w.Hp, device=dev)
+    wsn = block_norm_bwd_workspace(tokens, w.H, device=dev)
+    shared, h_out, u = (torch.empty_like(x) for _ in range(3))
+    legs = {
+        "shared_ffn": lambda: shared_ffn(x, weights, add=routed, out=shared, ws=ws),
+        "block_norm": lambda: block_norm(h, routed, shared, h_out=h_out, u=u, **form),
+        "block_norm_bwd": lambda: block_norm_bwd(h_out, dout, u, routed, shared, ws=wsn, **form),
+        "shared_ffn_bwd": lambda: shared_ffn_bwd(x, dout, weights, ws=wsb),
+    }
+    out = {}
+    for name, f in legs.items():
+        ms = []
+        for _ in range(6):
+            flush()
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            f()
+            b.record()
+            torch.cuda.synchronize()
+            ms.append(a.elapsed_time(b))
+        out[name + "_ms"] = round(float(np.median(ms[1:])), 4)
+    flops = 1e-9 * tokens * w.H * w.Hp
+    out["shared_ffn_TFLOPs"] = round(6 * flops / out["shared_ffn_ms"], 1)
+    out["shared_ffn_bwd_TFLOPs"] = round(16 * flops / out["shared_ffn_bwd_ms"], 1)
+    row = 1e-6 * tokens * w.H
+    out["block_norm_GBps"] = round(10 * row / out["block_norm_ms"], 1)
+    out["block_norm_bwd_GBps"] = round(14 * row / out["block_norm_bwd_ms"], 1)
     return out
 
 
@@ -732,7 +780,8 @@ def main():
                     help="also time a training step's backward (combine bwd, FFN backward, "
                          "dispatch bwd, three weight gradients, reduce_grad) and the steps that "
                          "route weights and an orthogonalising optimiser add (router, weighted "
-                         "combine's gradient, directions) and report it under 'train'; needs ~90 GB more HBM for the fp32 gradient buffers")
+                         "combine's gradient, directions) and those of a block around the experts "
+                         "(norms, shared expert) and report it under 'train'; needs ~90 GB more HBM for the fp32 gradient buffers")
     ap.add_argument("--overlap", action="store_true",
                     help="also time two pipelined micro-batches with dispatch/combine on a "
                          "second stream at a 32-CU budget against running them back to back")
