@@ -874,26 +874,10 @@ __device__ __forceinline__ void large_gateup_tile(const LargeArgs& a, const Ring
   St::flush(reg, zs, at.m0, a.Hp, at.pair[0], nv);
 }
 
-// A tile of 256 bf16 columns from the accumulators, by way of LDS.
-template <class G, int MI>
-__device__ __forceinline__ void store_bf16(const Ring& smem, const f32x16 (&acc)[MI][G::NJ],
-                                           const Waves<G, MI>& at, uint16_t* out, int64_t ld,
-                                           int rows, int cols) {
-  typedef Stage<32 * MI, 32 * G::NJ> St;
-  lds_t* reg = smem.base + at.w * St::kBytes;
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < G::NJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        St::put(reg, i, j, q, pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
-  St::flush(reg, make_rsrc(out, (int64_t)rows * ld * 2), at.m0, ld, at.nrow[0], cols);
-}
-
 // What is added to 32 rows of a wave's 32 NJ columns, as it is stored: lane l has
-// eight columns of one of an access's 64 / kLanes rows.
+// eight columns of one of an access's 64 / kLanes rows.  Places past the tile's
+// rows or columns read one inside it, for loads under a condition would each
+// wait behind a branch; what they give is never stored.
 template <int NJ>
 struct Added {
   static constexpr int kLanes = 4 * NJ, kRows = 64 / kLanes, kPieces = 32 / kRows;
@@ -901,62 +885,44 @@ struct Added {
   __device__ __forceinline__ void load(const uint16_t* add, int64_t ld, int m0, int rows, int c0,
                                        int cols) {
     const int lane = threadIdx.x & 63, c = c0 + 8 * (lane % kLanes);
+    if (!add) {
+#pragma unroll
+      for (int t = 0; t < kPieces; ++t) v[t] = u32x4{0, 0, 0, 0};
+      return;
+    }
 #pragma unroll
     for (int t = 0; t < kPieces; ++t) {
       const int m = m0 + kRows * t + lane / kLanes;
-      v[t] = u32x4{0, 0, 0, 0};
-      if (m < rows && c < cols) v[t] = *(const u32x4*)(add + (int64_t)m * ld + c);
+      v[t] = *(const u32x4*)(add + (int64_t)(m < rows ? m : rows - 1) * ld + (c < cols ? c : 0));
     }
   }
 };
 
-// Y: 256 columns, K = H'.  What is added is read along whole rows, so the sums
-// go through LDS in fp32, 32 rows at a time, to meet it (read at the
-// accumulators' places, 8 bytes a lane and row, it cost 150 us of 32768 tokens'
-// 990); each 32 rows' loads are issued before the 32 rows in front are
-// finished.
-template <class G, int MI, bool PART>
-__device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& smem,
-                                                const LargeTile& t) {
-  typedef Waves<G, MI> Wv;
+// A tile of 256 bf16 columns from the accumulators (+ add).  What is added is
+// read along whole rows, so the sums go through LDS in fp32, 32 rows at a time,
+// to meet it and to be stored as whole rows; each 32 rows' loads are issued
+// before the 32 rows in front are finished.  (Read at the accumulators' places, 8
+// bytes a lane and row, it cost 150 us of 32768 tokens' 990.  Without anything
+// added too: all of a wave's rows staged in bf16 before the first is stored took
+// 2271 us for the whole forward there, this 2226 us.)
+template <class G, int MI>
+__device__ __forceinline__ void store_rows(const Ring& smem, const f32x16 (&acc)[MI][G::NJ],
+                                           const Waves<G, MI>& wv, const uint16_t* add,
+                                           uint16_t* out, int64_t ld, int rows, int cols) {
   constexpr int NJ = G::NJ;
-  const Wv wv;
-  const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
-  const Steps k = steps_of<PART>(a, t, a.Hp / BK);
-  const int64_t k0 = (int64_t)k.j0 * BK, at = (int64_t)t.m0 * a.H + n0;
-  typename G::template Tiles<MI>::A la;
-  typename G::template Tiles<MI>::B lb;
-  la.init(a.z + (int64_t)t.m0 * a.Hp + k0, a.Hp, t.rows);
-  lb.init(a.w[2] + (int64_t)n0 * a.Hp + k0, a.Hp, cols);
-  f32x16 acc[MI][NJ];
-  product<G, MI>(la, lb, smem, k.n, acc, wv.m0, wv.nrow);
-  if constexpr (PART) {
-    int64_t col[NJ];
-    int left[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      col[j] = n0 + wv.nrow[j];
-      left[j] = cols - wv.nrow[j];
-    }
-    store_f32<G, MI>(acc, wv, a.part + ((int64_t)t.sp * a.T + t.m0) * a.H, a.H, t.rows, col, left);
-    return;
-  }
-  if (!a.add) {
-    store_bf16<G, MI>(smem, acc, wv, a.y + at, a.H, t.rows, cols);
-    return;
-  }
   typedef __attribute__((address_space(3))) float lds_f;
   typedef Added<NJ> Ad;
   constexpr int kRow = 32 * NJ + 4;               // floats: 32 rows' pieces on distinct banks
   lds_f* reg = (lds_f*)(smem.base + wv.w * (32 * kRow * 4));
   const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5, c0 = wv.nrow[0];
-  const Rsrc ys = make_rsrc(a.y + at, (int64_t)t.rows * a.H * 2);
+  const Rsrc to = make_rsrc(out, (int64_t)rows * ld * 2);
   Ad next;
-  next.load(a.add + at, a.H, wv.m0, t.rows, c0, cols);
+  next.load(add, ld, wv.m0, rows, c0, cols);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
+    MOONEP_PIN();                 // else every block's loads move up here, and their registers spill
     const Ad now = next;
-    if (i + 1 < MI) next.load(a.add + at, a.H, wv.m0 + 32 * (i + 1), t.rows, c0, cols);
+    if (i + 1 < MI) next.load(add, ld, wv.m0 + 32 * (i + 1), rows, c0, cols);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -979,10 +945,39 @@ __device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& 
         o[e] = pack_bf16x2(lo + bf16_of(now.v[p][e], 0), hi + bf16_of(now.v[p][e], 1));
       }
       const int m = wv.m0 + 32 * i + r;
-      const uint32_t off = c0 + c < cols ? (uint32_t)(((int64_t)m * a.H + c0 + c) * 2) : kOob;
-      __builtin_amdgcn_raw_buffer_store_b128(o, ys, off, 0, 0);
+      const uint32_t off = c0 + c < cols ? (uint32_t)(((int64_t)m * ld + c0 + c) * 2) : kOob;
+      __builtin_amdgcn_raw_buffer_store_b128(o, to, off, 0, 0);
     }
   }
+}
+
+// Y: 256 columns, K = H'.
+template <class G, int MI, bool PART>
+__device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& smem,
+                                                const LargeTile& t) {
+  constexpr int NJ = G::NJ;
+  const Waves<G, MI> wv;
+  const int n0 = t.nt * BN, cols = a.H - n0 < BN ? a.H - n0 : BN;
+  const Steps k = steps_of<PART>(a, t, a.Hp / BK);
+  const int64_t k0 = (int64_t)k.j0 * BK, at = (int64_t)t.m0 * a.H + n0;
+  typename G::template Tiles<MI>::A la;
+  typename G::template Tiles<MI>::B lb;
+  la.init(a.z + (int64_t)t.m0 * a.Hp + k0, a.Hp, t.rows);
+  lb.init(a.w[2] + (int64_t)n0 * a.Hp + k0, a.Hp, cols);
+  f32x16 acc[MI][NJ];
+  product<G, MI>(la, lb, smem, k.n, acc, wv.m0, wv.nrow);
+  if constexpr (PART) {
+    int64_t col[NJ];
+    int left[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      col[j] = n0 + wv.nrow[j];
+      left[j] = cols - wv.nrow[j];
+    }
+    store_f32<G, MI>(acc, wv, a.part + ((int64_t)t.sp * a.T + t.m0) * a.H, a.H, t.rows, col, left);
+    return;
+  }
+  store_rows<G, MI>(smem, acc, wv, a.add ? a.add + at : nullptr, a.y + at, a.H, t.rows, cols);
 }
 
 // dZ in fp32: 256 columns of H', K = H.
@@ -1026,14 +1021,16 @@ __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& sm
   // Z is kept in the accumulators of U until dG and dU are stored
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
+    MOONEP_PIN();
     f32x4 dzv[kHalf][4];
 #pragma unroll
     for (int j = 0; j < kHalf; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        // places past the edge read one inside it, as in Added
         const int m = wv.m0 + i * 32 + lr, n = wv.pair[j] + acc_col(q, lh);
-        dzv[j][q] = f32x4{0, 0, 0, 0};
-        if (m < t.rows && n < nv) dzv[j][q] = *(const f32x4*)(a.dz + at + (int64_t)m * a.Hp + n);
+        dzv[j][q] = *(const f32x4*)(a.dz + at + (int64_t)(m < t.rows ? m : t.rows - 1) * a.Hp +
+                                    (n < nv ? n : 0));
       }
 #pragma unroll
     for (int j = 0; j < kHalf; ++j)
@@ -1117,7 +1114,7 @@ __device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& sm
   la.init(a.dg + ab, a.du + ab, a.Hp, t.rows, a.Hp);
   lb.init(a.w[0] + bb, a.w[1] + bb, a.Hp, cols, a.Hp);
   product<G, MI>(la, lb, smem, 2 * a.Hp / BK, acc, at.m0, at.nrow);
-  store_bf16<G, MI>(smem, acc, at, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
+  store_rows<G, MI>(smem, acc, at, nullptr, a.dx + (int64_t)t.m0 * a.H + n0, a.H, t.rows, cols);
 }
 
 // G, U and dZ of a middling number of tokens in one launch, in splits: tiles of
@@ -1192,7 +1189,8 @@ struct ColTileA8 {       // 128 columns loaded by eight waves, laid out as a reg
   }
 };
 
-template <class G, int MI, bool PART>
+// F32: added to fp32 (both ends in one kernel would keep the sums twice, and spill).
+template <class G, int MI, bool PART, bool F32>
 __device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem, unsigned block) {
   constexpr int kM = G::kWaves == 4 ? 256 : 128, NJ = G::NJ;
   const int64_t each = (int64_t)a.ntm * a.ntn, total = 3 * each * a.S;
@@ -1238,8 +1236,8 @@ __device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem,
     return;
   }
   void* out = p == 0 ? a.dw[0] : p == 1 ? a.dw[1] : a.dw[2];
-  if (!a.f32) {
-    store_bf16<G, MI>(smem, acc, wv, (uint16_t*)out + at, a.Hp, mv, nv);
+  if constexpr (!F32) {
+    store_rows<G, MI>(smem, acc, wv, nullptr, (uint16_t*)out + at, a.Hp, mv, nv);
     return;
   }
   // read-modify-write, the reads of a block row before its writes
@@ -1269,32 +1267,35 @@ __device__ __forceinline__ void wgrad_tile(const LargeArgs& a, const Ring& smem,
       }
   }
 }
+template <bool F32>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
                           amdgpu_waves_per_eu(1, 1))) void large_wgrad_256(LargeArgs a) {
   MOONEP_RING(smem);
-  wgrad_tile<Four, 4, false>(a, smem, blockIdx.x);
+  wgrad_tile<Four, 4, false, F32>(a, smem, blockIdx.x);
 }
+template <bool F32>
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
                           amdgpu_waves_per_eu(2, 2))) void large_wgrad_128(LargeArgs a) {
   MOONEP_RING(smem);
-  wgrad_tile<Eight, 2, false>(a, smem, blockIdx.x);
+  wgrad_tile<Eight, 2, false, F32>(a, smem, blockIdx.x);
 }
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
                           amdgpu_waves_per_eu(2, 2))) void large_wgrad_splits(LargeArgs a) {
   MOONEP_RING(smem);
-  wgrad_tile<Eight, 2, true>(a, smem, blockIdx.x);
+  wgrad_tile<Eight, 2, true, false>(a, smem, blockIdx.x);
 }
 
 // The weight gradients and dX, which both need dG and dU and not each other, in
 // one launch where their tiles are alike: dX's shorter tiles fill what the last
 // round of the others leaves idle (a multiple of the XCDs, nw workgroups, is the
 // weight gradients').
+template <bool F32>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
                           amdgpu_waves_per_eu(1, 1))) void large_last_256(LargeArgs w, LargeArgs x,
                                                                           unsigned nw) {
   MOONEP_RING(smem);
   if (blockIdx.x < nw) {
-    wgrad_tile<Four, 4, false>(w, smem, blockIdx.x);
+    wgrad_tile<Four, 4, false, F32>(w, smem, blockIdx.x);
     return;
   }
   LargeTile t;
@@ -1302,12 +1303,13 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
   if (t.rows <= kHalfTileM) large_dx_tile<Four, 2, false>(x, smem, t);
   else large_dx_tile<Four, 4, false>(x, smem, t);
 }
+template <bool F32>
 __global__ __attribute__((amdgpu_flat_work_group_size(512, 512),
                           amdgpu_waves_per_eu(2, 2))) void large_last_128(LargeArgs w, LargeArgs x,
                                                                           unsigned nw) {
   MOONEP_RING(smem);
   LargeTile t;
-  if (blockIdx.x < nw) wgrad_tile<Eight, 2, false>(w, smem, blockIdx.x);
+  if (blockIdx.x < nw) wgrad_tile<Eight, 2, false, F32>(w, smem, blockIdx.x);
   else if (large_tile(x, 128, &t, blockIdx.x - nw)) large_dx_tile<Eight, 2, false>(x, smem, t);
 }
 
@@ -1653,8 +1655,9 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
     const LargeArgs ax = with_shape(big, dxs), aw = with_shape(big, ws_);
     const unsigned nw = (unsigned)(ceil_div(3LL * ws_.ntm * ws_.ntn, kXcds) * kXcds);
     const unsigned n = nw + blocks_of(dxs);
-    if (ws_.rows == 256) large_last_256<<<n, 256, 0, s>>>(aw, ax, nw);
-    else large_last_128<<<n, 512, 0, s>>>(aw, ax, nw);
+    if (ws_.rows == 256) (big.f32 ? large_last_256<true> : large_last_256<false>)
+        <<<n, 256, 0, s>>>(aw, ax, nw);
+    else (big.f32 ? large_last_128<true> : large_last_128<false>)<<<n, 512, 0, s>>>(aw, ax, nw);
     return hipGetLastError();
   }
   if (dx) {
@@ -1669,8 +1672,10 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
     if (ws_.large) {
       const LargeArgs a = with_shape(big, ws_);
       const unsigned n = (unsigned)(ceil_div(3LL * a.ntm * a.ntn * a.S, kXcds) * kXcds);
-      if (ws_.rows == 256) large_wgrad_256<<<n, 256, 0, s>>>(a);
-      else if (ws_.S == 1) large_wgrad_128<<<n, 512, 0, s>>>(a);
+      if (ws_.rows == 256) (big.f32 ? large_wgrad_256<true> : large_wgrad_256<false>)
+          <<<n, 256, 0, s>>>(a);
+      else if (ws_.S == 1) (big.f32 ? large_wgrad_128<true> : large_wgrad_128<false>)
+          <<<n, 512, 0, s>>>(a);
       else large_wgrad_splits<<<n, 512, 0, s>>>(a);
     } else {
       run_small<OP_WGRAD>(ws_, ws_.S > 1, wa, s);
