@@ -856,10 +856,12 @@ __device__ __forceinline__ void large_gateup_tile(const LargeArgs& a, const Ring
                      col, left);
     return;
   }
-  typedef Stage<32 * MI, 32 * Wv::kHalf> St;
+  // 32 rows at a time through LDS, to be stored as whole rows
+  typedef Stage<32, 32 * Wv::kHalf> St;
   lds_t* reg = smem.base + at.w * St::kBytes;
+  const Rsrc zs = make_rsrc(a.z + (int64_t)t.m0 * a.Hp + n0, (int64_t)t.rows * a.Hp * 2);
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+  for (int i = 0; i < MI; ++i) {
 #pragma unroll
     for (int j = 0; j < Wv::kHalf; ++j)
 #pragma unroll
@@ -868,10 +870,10 @@ __device__ __forceinline__ void large_gateup_tile(const LargeArgs& a, const Ring
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           z[e] = activate(a.act, acc[i][j][4 * q + e]).f * acc[i][j + Wv::kHalf][4 * q + e];
-        St::put(reg, i, j, q, pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
+        St::put(reg, 0, j, q, pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
       }
-  const Rsrc zs = make_rsrc(a.z + (int64_t)t.m0 * a.Hp + n0, (int64_t)t.rows * a.Hp * 2);
-  St::flush(reg, zs, at.m0, a.Hp, at.pair[0], nv);
+    St::flush(reg, zs, at.m0 + 32 * i, a.Hp, at.pair[0], nv);
+  }
 }
 
 // What is added to 32 rows of a wave's 32 NJ columns, as it is stored: lane l has
@@ -1018,7 +1020,8 @@ __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& sm
   lds_t* reg_g = smem.base + wv.w * (2 * St::kBytes);
   lds_t* reg_u = reg_g + St::kBytes;
   const int64_t at = (int64_t)t.m0 * a.Hp + n0, range = (int64_t)t.rows * a.Hp * 2;
-  // Z is kept in the accumulators of U until dG and dU are stored
+  // Z is kept in the accumulators of U until dG and dU are stored (all three stored 32 rows at a
+  // time: 24948 tokens of 256 x 2368 457 -> 479 us)
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     MOONEP_PIN();
