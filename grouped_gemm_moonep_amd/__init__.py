@@ -23,6 +23,15 @@ gradient), `Buffer.combine_bwd` (the gradient of the weighted combine) and
     dlogits = buf.route_bwd(logits, topk, drw)      # moonep_route_bwd
     direction = orthogonalize(grad_home)            # moonep_orthogonalize
 
+and what a block has around its experts: `shared_ffn` (the expert that every
+token passes, added to combine's output), `block_norm` (the block's end and the
+next one's start) and their gradients `shared_ffn_bwd` and `block_norm_bwd`:
+
+    both = shared_ffn(u, (gate, up, down), add=out)          # moonep_shared_ffn
+    h, u = block_norm(h, both, w_post=p, w_pre=n)            # moonep_block_norm
+    dh, dy, dg, dp, dn = block_norm_bwd(h, dh, du, both, w_post=p, w_pre=n)
+    du, dw = shared_ffn_bwd(u, dy, (gate, up, down))         # moonep_shared_ffn_bwd
+
 `SymmetricBuffer` is the README's [E+B,H,H'] weight (or fp32 gradient) buffer
 of one projection on virtual memory (moonep_symbuf_*): per-rank views whose
 rows [0,E) map every rank's home chunk, with the *_views methods addressing

@@ -16,8 +16,11 @@
 //
 // Design for CDNA4: every operand is read once and every result written once,
 // so a row stays in registers between its sums.  A row of up to 1024 elements
-// belongs to a wave, whose sums need no barrier; a longer one to a workgroup
-// of up to 16 waves with two 8-element vectors a lane.
+// belongs to a wave, whose sums need no barrier; a longer one to a workgroup of
+// as few waves as hold it with one 8-element vector a lane (up to 4096) or two.
+// Bound by bytes: 32768 rows of 7168 in bf16 with two outputs and both norms take
+// 450 us (2.35 GB, 5.2 TB/s; a copy reaches 4.9 to 5.4), backward 705 us (3.29 GB
+// and the shares below; 664 us without its sums).
 #include "internal.h"
 
 namespace moonep {
