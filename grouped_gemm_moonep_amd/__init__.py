@@ -601,6 +601,11 @@ def _maybe(t, dtype, shape, dev, name):
     return None if t is None else _rows(t, dtype, shape, dev, name)
 
 
+def _int32(n):
+    """A size for a 32-bit argument; one that does not fit is refused as the library refuses -1."""
+    return n if n < 1 << 31 else -1
+
+
 def _workspace(name, nbytes, device):
     if nbytes < 0:
         raise MoonepError(_abi.MOONEP_ERR_CONFIG, name)
@@ -634,17 +639,19 @@ def _ffn_inputs(x, weights, act):
     w = _abi.PTR3(_rows(weights[0], torch.bfloat16, shape, dev, "gate"),
                   _rows(weights[1], torch.bfloat16, shape, dev, "up"),
                   _rows(weights[2], torch.bfloat16, shape, dev, "down"))
-    return x.numel() // H if H else 0, H, Hp, _abi.ACTS[act], w
+    return x.numel() // H if H else 0, _int32(H), _int32(Hp), _abi.ACTS[act], w
 
 
 def shared_ffn_workspace(T, H, Hp, device="cuda"):
     """Workspace tensor of `shared_ffn` for T tokens."""
-    return _workspace("moonep_shared_ffn_ws", lib().moonep_shared_ffn_ws(T, H, Hp), device)
+    return _workspace("moonep_shared_ffn_ws",
+                      lib().moonep_shared_ffn_ws(T, _int32(H), _int32(Hp)), device)
 
 
 def shared_ffn_bwd_workspace(T, H, Hp, device="cuda"):
     """Workspace tensor of `shared_ffn_bwd` for T tokens."""
-    return _workspace("moonep_shared_ffn_bwd_ws", lib().moonep_shared_ffn_bwd_ws(T, H, Hp), device)
+    return _workspace("moonep_shared_ffn_bwd_ws",
+                      lib().moonep_shared_ffn_bwd_ws(T, _int32(H), _int32(Hp)), device)
 
 
 def shared_ffn(x, weights, act="silu", add=None, out=None, ws=None):
@@ -753,7 +760,7 @@ def _norm_inputs(h, y, y2, gate, w_post, w_pre):
              _maybe(y2, torch.bfloat16, shape, dev, "y2"), p_gate, kind,
              _maybe(w_post, torch.float32, (W,), dev, "w_post"),
              _maybe(w_pre, torch.float32, (W,), dev, "w_pre")),
-            (math.prod(shape[:-1]), W))
+            (math.prod(shape[:-1]), _int32(W)))
 
 
 def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0, eps=1e-6,
@@ -801,7 +808,8 @@ def block_norm(h, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0
 
 def block_norm_bwd_workspace(T, W, device="cuda"):
     """Workspace tensor of `block_norm_bwd` for T rows of W elements."""
-    return _workspace("moonep_block_norm_bwd_ws", lib().moonep_block_norm_bwd_ws(T, W), device)
+    return _workspace("moonep_block_norm_bwd_ws", lib().moonep_block_norm_bwd_ws(T, _int32(W)),
+                      device)
 
 
 def block_norm_bwd(h, dh, du=None, y=None, y2=None, gate=None, w_post=None, w_pre=None, scale=1.0,

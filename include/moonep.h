@@ -51,7 +51,7 @@ enum {
   MOONEP_ERR_NOMEM = 5,   /* scratch allocation in moonep_create failed    */
   MOONEP_ERR_SCRATCH = 6  /* moonep_plan_noalloc: the configuration needs
                              more planning scratch than the library holds;
-                             moonep_orthogonalize: workspace too small      */
+                             calls with a workspace: it is too small        */
 };
 
 /* Problem sizes, in the README's notation ("Usage > Integration"):
