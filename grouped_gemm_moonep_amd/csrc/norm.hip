@@ -371,7 +371,8 @@ __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
         const int c = 8 * (at.lane + p * at.lanes);
         if (c < W) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[p][i] = ra * (d[p][i] - av[p][i] * ma);
+          for (int i = 0; i < 8; ++i)         // without a norm a is no part of it, infinite or not
+            d[p][i] = a.w_post ? ra * (d[p][i] - av[p][i] * ma) : d[p][i];
           store8(a.dy + base + c, d[p]);
         }
       }

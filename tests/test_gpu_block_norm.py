@@ -257,6 +257,18 @@ def test_bad_values_stay_in_their_row(bad, W):
     assert torch.equal(got[1][rest], clean_b[1][rest]) and got[1][4].isnan().any()
 
 
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+@pytest.mark.parametrize("W", [200, 1800])
+def test_gradient_of_y_without_a_norm_does_not_see_y(gate, W):
+    h, v, n = draw(10, W, torch.float32, gate, post=False)
+    dh, du = n(10, W), n(10, W).bfloat16()
+    clean = block_norm_bwd(h, dh, du, **v)
+    v["y"] = v["y"].clone()
+    v["y"][4, 7], v["y"][5, 8] = float("inf"), float("nan")
+    got = block_norm_bwd(h, dh, du, **v)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+
+
 def test_repeats_bit_for_bit():
     h, v, n = draw(3001, 1160, torch.bfloat16)
     dh, du = n(3001, 1160).bfloat16(), n(3001, 1160).bfloat16()
