@@ -54,7 +54,9 @@ __device__ __forceinline__ Act activate(float g) {
   // the hardware's reciprocal and exponential: about 1e-7, far below the
   // rounding to bf16 that follows
   const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-c));
-  return {g * s, s * (1.0f + g * (1.0f - s) * dc)};
+  // s first: where it is 0, g dc may be past fp32
+  const float f = g * s;
+  return {f, s + f * ((1.0f - s) * dc)};
 }
 __device__ __forceinline__ Act activate(int kind, float g) {
   return kind == MOONEP_ACT_SILU ? activate<MOONEP_ACT_SILU>(g)
@@ -775,7 +777,7 @@ struct Waves {
                             amdgpu_waves_per_eu(1, 1))) void name##_256(LargeArgs a) {     \
     MOONEP_RING(smem);                                                                     \
     LargeTile t;                                                                           \
-    if (!large_tile(a, 256, &t, blockIdx.x)) return;                                                \
+    if (!large_tile(a, 256, &t, blockIdx.x)) return;                                       \
     if (t.rows <= kHalfTileM) body<Four, 2, false>(a, smem, t);                            \
     else body<Four, 4, false>(a, smem, t);                                                 \
   }                                                                                        \
@@ -786,7 +788,7 @@ struct Waves {
                             amdgpu_waves_per_eu(2, 2))) void name(LargeArgs a) {           \
     MOONEP_RING(smem);                                                                     \
     LargeTile t;                                                                           \
-    if (!large_tile(a, 128, &t, blockIdx.x)) return;                                                \
+    if (!large_tile(a, 128, &t, blockIdx.x)) return;                                       \
     body<Eight, 2, PART>(a, smem, t);                                                      \
   }
 

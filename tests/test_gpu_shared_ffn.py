@@ -168,6 +168,20 @@ def test_one_activation_value():
         assert torch.equal(dx[:, 0], torch.tensor([1.0, 0, 1.0, 0], device="cuda").bfloat16())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("T", [5, 20000])
+def test_gradient_far_below_the_activation(act, T):
+    """A gate of -1e33 or below: f and f' are 0, whatever g times the inner derivative would be."""
+    x = torch.zeros(T, 128, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = -1e17, 1.0
+    w = [torch.zeros(128, 256, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    w[0][0], w[1][1], w[2][2] = 1e16, 1.0, 1.0
+    dy = torch.ones_like(x)
+    assert not shared_ffn(x, w, act=act).any()
+    dx, dw = shared_ffn_bwd(x, dy, w, act=act)
+    assert not dx.any() and not any(t.any() for t in dw)
+
+
 def test_bad_values_stay_in_their_token():
     x, w, add, dy = draw(70, 192, 128)
     clean, (cdx, _) = shared_ffn(x, w, add=add), shared_ffn_bwd(x, dy, w)
