@@ -96,7 +96,7 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name}: expected device {device}, got {t.device}")
 
 
-def _apart(name, out, **inputs):
+def _apart(name, out, /, **inputs):
     """`out`, a tensor of the caller's, must not share memory with any of `inputs`."""
     o0 = out.data_ptr()
     o1 = o0 + out.nbytes

@@ -432,8 +432,8 @@ moonep_status_t moonep_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
                                           stream));
 }
 
-// What the forward and the backward of a block's norms take alike.
-// (arrays of no rows may be NULL).
+// What the forward and the backward of a block's norms take alike (arrays of no rows may be
+// NULL).
 static bool norm_form_ok(int64_t T, int32_t dtype, const void* y, const void* y2, const void* gate,
                          int32_t gate_kind, const void* w_post, const void* w_pre, float scale,
                          float eps) {
