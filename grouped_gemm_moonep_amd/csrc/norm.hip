@@ -17,7 +17,8 @@
 // Design for CDNA4: every operand is read once and every result written once,
 // so a row stays in registers between its sums.  A row of up to 1024 elements
 // belongs to a wave, whose sums need no barrier; a longer one to a workgroup of
-// as few waves as hold it with one 8-element vector a lane (up to 4096) or two.
+// as few waves as hold it with one 8-element vector a lane (up to 4096) or two, in
+// the backward beyond 8192 four.
 // Bound by bytes: 32768 rows of 7168 in bf16 with two outputs and both norms take
 // 450 us (2.35 GB, 5.2 TB/s; a copy reaches 4.9 to 5.4), backward 705 us (3.29 GB
 // and the shares below; 664 us without its sums).
@@ -284,9 +285,80 @@ struct RowBwdIn {
   }
 };
 
-// Sums over tokens stay in a lane's registers, for its columns, over all rows
-// of its wave or workgroup; each workgroup then writes its share to part
-// [3][shares][W] and norm_bwd_sum adds the shares, in an order that T and W fix.
+// A lane's sums over tokens for its columns, in registers or, where these do not
+// hold all three, in LDS, whose places no other lane touches.
+template <int VPT, bool kLds>
+struct Sums {
+  float v[VPT][8];
+  __device__ __forceinline__ Sums(void*) {
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+  }
+  __device__ __forceinline__ void add(int p, const float (&t)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[p][i] += t[i];
+  }
+  __device__ __forceinline__ void store(int p, float* to) const { store8(to, v[p]); }
+};
+template <int VPT>
+struct Sums<VPT, true> {
+  typedef __attribute__((address_space(3))) f32x4 lds_f4;
+  static constexpr int kBytes = 512 * VPT * 32;
+  lds_f4* at;                          // the next four of a lane's sums lie 512 places on
+  __device__ __forceinline__ Sums(void* lds) : at((lds_f4*)lds + threadIdx.x) {
+#pragma unroll
+    for (int q = 0; q < 2 * VPT; ++q) at[512 * q] = f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void add(int p, const float (&t)[8]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x4 o = at[512 * (2 * p + q)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += t[4 * q + e];
+      at[512 * (2 * p + q)] = o;
+    }
+  }
+  __device__ __forceinline__ void store(int p, float* to) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) *((f32x4*)to + q) = at[512 * (2 * p + q)];
+  }
+};
+
+// A workgroup's share of one sum; the sums of four waves with rows of their own
+// leave as one.
+template <int VPT, bool kWave, class S>
+__device__ __forceinline__ void put_share(const S& s, const Place<kWave>& at, int W, float* q) {
+  if constexpr (kWave) {
+    __shared__ __attribute__((aligned(16))) float four[4][64 * 8 * VPT];
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) s.store(p, &four[threadIdx.x >> 6][8 * (at.lane + 64 * p)]);
+    __syncthreads();
+    for (int c = 4 * threadIdx.x; c < W; c += 1024) {
+      f32x4 t = *(const f32x4*)&four[0][c];
+#pragma unroll
+      for (int w = 1; w < 4; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] += four[w][c + e];
+      *(f32x4*)(q + c) = t;
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int c = 8 * (at.lane + p * at.lanes);
+      if (c < W) s.store(p, q + c);
+    }
+  }
+}
+
+// Sums over tokens stay with a lane, for its columns, over all rows of its
+// wave or workgroup; each workgroup then writes its share to part [3][shares][W]
+// and norm_bwd_sum adds the shares, in an order that T and W fix.  With four
+// vectors a lane two of the three sums lie in LDS (8192 rows of 16384 in bf16 447
+// us; two vectors in 1024 lanes, whose 128 registers spill, 1394 us).  Up to 8192
+// elements registers hold all (32768 rows of 7168 707 us, in LDS 742 us).
 template <class TS, int VPT, bool kWave, int kMost>
 __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][kVals][16];
@@ -294,33 +366,39 @@ __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
   const Place<kWave> at;
   const int W = a.W;
   const float inv_w = 1.0f / (float)W;
+  const bool channel = a.gate_kind == MOONEP_GATE_CHANNEL && a.dgate;
   const bool need_a = a.y && (a.w_post || a.gate_kind != MOONEP_GATE_NONE);
-  float s_pre[VPT][8], s_post[VPT][8], s_gate[VPT][8];
-#pragma unroll
-  for (int p = 0; p < VPT; ++p)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[p][i] = s_post[p][i] = s_gate[p][i] = 0.0f;
+  constexpr bool kLds = VPT == 4;
+  __shared__ __attribute__((aligned(16))) char held[2][kLds ? Sums<VPT, true>::kBytes : 16];
+  Sums<VPT, false> s_pre(nullptr);
+  Sums<VPT, kLds> s_post(held[0]), s_gate(held[1]);
   for (int64_t r = at.row; r < a.T; r += at.step) {
     const int64_t base = r * W;
+    Place<kWave> in = at;
+    // the addresses are taken anew for each row: kept, they would make the widest rows spill
+    if constexpr (kLds) asm volatile("" : "+v"(in.lane));
     RowBwdIn<TS, VPT> cur;
-    cur.load(a, at, r, need_a);
+    cur.load(a, in, r, need_a);
     float d[VPT][8], av[VPT][8];
-    float s3[3] = {0.0f, 0.0f, 0.0f};       // h'^2, v h', a^2
+    float s3[3] = {0.0f, 0.0f, 0.0f};       // h'^2, v h', a^2: each vector's, then theirs
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      const int c = 8 * (at.lane + p * at.lanes);
+      const int c = 8 * (in.lane + p * in.lanes);
       Raw<float> w;
       w.zero();
       if (a.w_pre && c < W) w.load(a.w_pre + c);
+      float t[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float h = cur.h[p].get(i);
         av[p][i] = cur.y[p].get(i) + cur.y2[p].get(i);
         d[p][i] = cur.du[p].get(i) * w.get(i);
-        s3[0] += h * h;
-        s3[1] += d[p][i] * h;
-        s3[2] += av[p][i] * av[p][i];
+        t[0] += h * h;
+        t[1] += d[p][i] * h;
+        t[2] += av[p][i] * av[p][i];
       }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) s3[k] += t[k];
     }
     if (a.w_pre || a.w_post) sum(s3);
     const float rh = a.w_pre ? rstd(s3[0], inv_w, a.eps) : 0.0f;
@@ -329,46 +407,49 @@ __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
     float s2[2] = {0.0f, 0.0f};             // D n, w_post dn a
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      const int c = 8 * (at.lane + p * at.lanes);
+      const int c = 8 * (in.lane + p * in.lanes);
       if (c < W) {
         Raw<float> w, g;
         if (a.w_post) w.load(a.w_post + c);
         if (a.gate_kind == MOONEP_GATE_CHANNEL) g.load((const float*)a.gate + c);
-        float dg[8];
+        float dg[8], dw[8], t[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float h = cur.h[p].get(i);
-          s_pre[p][i] += cur.du[p].get(i) * (h * rh);
+          dw[i] = cur.du[p].get(i) * (h * rh);
           d[p][i] = cur.dh[p].get(i) + rh * (d[p][i] - h * mh);
         }
+        s_pre.add(p, dw);
         store8((TS*)a.dres + base + c, d[p]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float hat = av[p][i] * ra;
           const float n = a.w_post ? hat * w.get(i) : hat;
           const float sd = a.scale * d[p][i];
-          const float t = sd * n;
-          dg[i] = t;
-          s_gate[p][i] += t;
-          s2[0] += t;
+          dg[i] = sd * n;
+          t[0] += dg[i];
           float dn = sd * cur.gt;
           if (a.gate_kind == MOONEP_GATE_CHANNEL) dn *= g.get(i);
           if (a.gate_kind == MOONEP_GATE_FULL) dn *= cur.g[p].get(i);
-          s_post[p][i] += dn * hat;
+          dw[i] = dn * hat;
           d[p][i] = a.w_post ? dn * w.get(i) : dn;
-          s2[1] += d[p][i] * av[p][i];
+          t[1] += d[p][i] * av[p][i];
         }
+        s2[0] += t[0];
+        s2[1] += t[1];
+        if (!kLds || a.dw_post) s_post.add(p, dw);
+        if (!kLds || channel) s_gate.add(p, dg);
         if (a.gate_kind == MOONEP_GATE_FULL && a.dgate) store8((uint16_t*)a.dgate + base + c, dg);
       }
     }
     const bool token = a.gate_kind == MOONEP_GATE_TOKEN && a.dgate;
     if (token || (a.dy && a.w_post)) sum(s2);
-    if (token && at.lane == 0) ((float*)a.dgate)[r] = s2[0];
+    if (token && in.lane == 0) ((float*)a.dgate)[r] = s2[0];
     if (a.dy) {
       const float ma = a.w_post ? s2[1] * inv_w * ra * ra : 0.0f;
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
-        const int c = 8 * (at.lane + p * at.lanes);
+        const int c = 8 * (in.lane + p * in.lanes);
         if (c < W) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)         // without a norm a is no part of it, infinite or not
@@ -379,36 +460,11 @@ __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
     }
   }
   if (!a.part) return;
-  const bool want[3] = {a.dw_pre != nullptr, a.dw_post != nullptr,
-                        a.gate_kind == MOONEP_GATE_CHANNEL && a.dgate};
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (!want[k]) continue;
-    float (*v)[8] = k == 0 ? s_pre : k == 1 ? s_post : s_gate;
-    float* q = a.part + ((int64_t)k * a.shares + blockIdx.x) * W;
-    if constexpr (kWave) {
-      // the four waves' sums leave as one share
-      __shared__ __attribute__((aligned(16))) float four[4][64 * 8 * VPT];
-#pragma unroll
-      for (int p = 0; p < VPT; ++p) store8(&four[threadIdx.x >> 6][8 * (at.lane + 64 * p)], v[p]);
-      __syncthreads();
-      for (int c = 4 * threadIdx.x; c < W; c += 1024) {
-        f32x4 t = *(const f32x4*)&four[0][c];
-#pragma unroll
-        for (int w = 1; w < 4; ++w)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] += four[w][c + e];
-        *(f32x4*)(q + c) = t;
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int p = 0; p < VPT; ++p) {
-        const int c = 8 * (at.lane + p * at.lanes);
-        if (c < W) store8(q + c, v[p]);
-      }
-    }
-  }
+  float* q = a.part + (int64_t)blockIdx.x * W;
+  const int64_t each = (int64_t)a.shares * W;
+  if (a.dw_pre) put_share<VPT, kWave>(s_pre, at, W, q);
+  if (a.dw_post) put_share<VPT, kWave>(s_post, at, W, q + each);
+  if (channel) put_share<VPT, kWave>(s_gate, at, W, q + 2 * each);
 }
 
 // out_k [W] = the sum of the shares of part[k]: a workgroup takes 64 columns,
@@ -437,7 +493,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum(const float* part, int shar
 }
 
 // Workgroups of a launch and the lanes of each: up to 1024 elements a wave, up to 4096 a workgroup
-// with a vector a lane, beyond two.  Workgroups per CU: as many as have `waves` waves, one at least.
+// with a vector a lane, beyond two, in the backward past 8192 four.  Workgroups per CU: as many as
+// have `waves` waves, one at least.
 // Forward: a row a workgroup nearly always (32768 rows of 7168 in bf16: 448 us, with nine workgroups
 // per CU 485 us; the next row's loads ahead of a row's sums 480 to 490 us).  Backward: as few
 // workgroups as keep the CUs busy, for each leaves a share of the sums over tokens (702 us with one
@@ -451,10 +508,10 @@ NormGrid norm_grid(int64_t T, int W, bool bwd) {
   NormGrid g;
   const int vecs = W / 8;
   g.wave = vecs <= 128;
-  g.vpt = vecs <= 64 || (vecs > 128 && vecs <= 512) ? 1 : 2;
+  g.vpt = vecs <= 64 || (vecs > 128 && vecs <= 512) ? 1 : bwd && vecs > 1024 ? 4 : 2;
   g.threads = g.wave ? 256 : (vecs + 64 * g.vpt - 1) / (64 * g.vpt) * 64;
   const int64_t need = g.wave ? (T + 3) / 4 : T;
-  const int waves = !bwd ? 512 : g.vpt == 1 ? 16 : 12;
+  const int waves = !bwd ? 512 : g.vpt == 1 ? 16 : g.vpt == 2 ? 12 : 8;
   const int per_cu = waves * 64 / g.threads;
   const int64_t most = 256LL * (per_cu > 1 ? per_cu : 1);
   g.blocks = need < most ? need : most;
@@ -494,8 +551,8 @@ static hipError_t norm_bwd_as(const NormBwdArgs& a, hipStream_t s) {
   else if (g.wave && g.vpt == 1) norm_bwd_kernel<TS, 1, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   else if (g.wave) norm_bwd_kernel<TS, 2, true, 256><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   else if (g.vpt == 1) norm_bwd_kernel<TS, 1, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else if (g.threads <= 512) norm_bwd_kernel<TS, 2, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
-  else norm_bwd_kernel<TS, 2, false, 1024><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else if (g.vpt == 2) norm_bwd_kernel<TS, 2, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
+  else norm_bwd_kernel<TS, 4, false, 512><<<(unsigned)g.blocks, g.threads, 0, s>>>(a);
   float* dgate = a.gate_kind == MOONEP_GATE_CHANNEL ? (float*)a.dgate : nullptr;
   if (a.dw_pre || a.dw_post || dgate) {
     norm_bwd_sum<<<dim3((unsigned)((a.W + 63) / 64), 3), 1024, 0, s>>>(a.part, a.shares, a.W,

@@ -173,6 +173,15 @@ def test_forms(gate, post, pre, two, W):
     check_backward(37, W, torch.bfloat16, **form)
 
 
+@pytest.mark.parametrize("gate,post,pre", [("channel", True, True), ("channel", False, True),
+                                           ("token", True, False), ("full", True, True),
+                                           (None, False, False)])
+@pytest.mark.parametrize("W,dtype", [(8264, torch.float32), (12288, torch.bfloat16)])
+def test_backward_of_wide_rows(gate, post, pre, W, dtype):
+    """More rows than CUs: some workgroups sum two rows."""
+    check_backward(300, W, dtype, gate=gate, post=post, pre=pre)
+
+
 def test_no_gradient_from_behind():
     check_backward(9, 264, torch.float32, with_dh=False)
 
