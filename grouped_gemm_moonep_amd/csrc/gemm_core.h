@@ -45,6 +45,7 @@
 // or activation slabs in that XCD's L2.
 #pragma once
 
+#include "col_geom.h"
 #include "internal.h"
 #include "tile_schedule.h"
 
@@ -78,7 +79,6 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 // wave-uniform (readfirstlane) so the compiler never wraps a load in a
 // per-lane loop over descriptors.
 typedef __amdgpu_buffer_rsrc_t Rsrc;
-constexpr uint32_t kOob = 0x80000000u;   // any offset >= num_records reads 0
 
 __device__ __forceinline__ Rsrc make_rsrc(const void* base, int64_t bytes) {
   const uint32_t n = bytes > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)bytes;
@@ -232,47 +232,52 @@ struct RowTile2 {
   }
 };
 
-struct ColTile {
+// COLS columns of a region, loaded by WAVES waves (col_geom.h).
+template <int COLS, int WAVES>
+struct ColTileT {
+  typedef ColGeom<COLS, WAVES> G;
   static constexpr bool kRows = false;
-  static constexpr int kLoads = 8;
-  DmaRsrc rs;           // this wave's region (waves 0,1: region 0; waves 2,3: region 1)
+  static constexpr int kLoads = G::kLoads;
+  static constexpr int kBytes = 2 * G::kRegion;    // of two regions
+  DmaRsrc rs;           // this wave's region: the first WAVES waves have the first one
   uint32_t voff;        // this lane's offset for load 0 of k-block 0 (out of range past nv)
   uint32_t ld2;
   uint32_t wlds;        // this wave's first 1 KiB block inside a slot
-  // src0/src1: k 0, n 0 of the two 128-column regions; ld: k stride
-  // (elements); k_total: valid k rows from k 0; nv0/nv1: valid columns
+  // src: k 0, n 0 of the wave's region; ld: k stride (elements); k_total: valid k rows from k 0;
+  // nv: valid columns
+  __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t k_total, int nv) {
+    const int w = wave_id();
+    ld2 = (uint32_t)(ld * 2);
+    rs = make_dma_rsrc(src, G::bytes(ld2, (int)k_total, nv));
+    voff = G::lane(w, threadIdx.x & 63, ld2, nv);
+    wlds = (uint32_t)(w * kLoads * 1024);
+  }
+  // two regions
   __device__ __forceinline__ void init(const uint16_t* src0, const uint16_t* src1, int64_t ld,
                                        int64_t k_total, int nv0, int nv1) {
-    const int w = wave_id(), lane = threadIdx.x & 63;
-    const int region = w >> 1;
-    rs = make_dma_rsrc(region ? src1 : src0, k_total * ld * 2);
-    ld2 = (uint32_t)(ld * 2);
-    const int k = 32 * (w & 1) + (lane >> 4);        // load i adds 4 i rows
-    const int col = 8 * ((lane & 15) ^ (4 * (k & 3)));
-    voff = col < (region ? nv1 : nv0) ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
-    wlds = (uint32_t)(w * 8 * 1024);
+    const bool second = wave_id() >= WAVES;
+    init(second ? src1 : src0, ld, k_total, second ? nv1 : nv0);
   }
   __device__ __forceinline__ uint32_t koff(int64_t k0) const { return (uint32_t)(k0 * ld2); }
   // ko: the step's byte offset, or kOob past the end
   __device__ __forceinline__ void issue1(lds_t* tile, int i, uint32_t ko) const {
-    const uint32_t s = ko + (uint32_t)(4 * i) * ld2;
-    load_lds(rs, tile + wlds + i * 1024, voff + s);
+    load_lds(rs, tile + wlds + i * 1024, G::load(voff, ko, i, ld2));
   }
   __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
     const uint32_t ko = valid ? koff(k0) : kOob;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) issue1(tile, i, ko);
+    for (int i = 0; i < kLoads; ++i) issue1(tile, i, ko);
   }
   // 8 consecutive k (sub-step kk of 4, lane half lh) of tile column n (the lane's)
   __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
     const int lane = threadIdx.x & 63, q = lane & 15, g = (lane >> 4) & 1;
-    const lds_t* region = tile + (nb >> 7) * 16384;
-    const int col = (nb & 127) + 16 * g + 4 * (q & 3);
+    const lds_t* region = tile + (unsigned)nb / COLS * G::kRegion;
+    const int col = (nb & (COLS - 1)) + 16 * g + 4 * (q & 3);
     i16x4 h[2];
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const int k = 16 * kk + 8 * lh + 4 * hh + (q >> 2);
-      const int off = k * 256 + (((col >> 3) ^ (4 * (k & 3))) << 4) + (col & 7) * 2;
+      const int off = k * COLS * 2 + (((col >> 3) ^ G::swz(k)) << 4) + (col & 7) * 2;
       h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (__attribute__((address_space(3))) i16x4*)(region + off));
     }
@@ -280,6 +285,7 @@ struct ColTile {
     return __builtin_bit_cast(bf16x8, v);
   }
 };
+typedef ColTileT<128, 2> ColTile;      // two regions of 128 columns, four waves
 
 // MFMA fragments of one 16-deep sub-step for a wave: A rows arow0 + 32 i
 // (i < MI), B columns nrow[j] (+ lane%32).

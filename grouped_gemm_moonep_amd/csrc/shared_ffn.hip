@@ -69,46 +69,8 @@ __device__ __forceinline__ float bf16_of(unsigned pair, int hi) {
 
 // ------------------------------------------------------------- small tiles
 // Column tile of 128 columns as two regions of 64 (gate and up, or two halves
-// of one matrix): 64 k rows of 128 B each, whole cache lines.  16-byte chunk c
-// of row k sits at c ^ (4 (k / 2 % 2)): a transposing read of 32 lanes takes 64
-// bytes of four rows, two of which share each 256-byte window of the LDS.
-struct ColTile64 {
-  static constexpr bool kRows = false;
-  static constexpr int kLoads = 4;
-  static constexpr int kBytes = 2 * 64 * 128;
-  DmaRsrc rs;           // waves 0, 1: region 0; waves 2, 3: region 1
-  uint32_t voff, ld2, wlds;
-  __device__ __forceinline__ void init(const uint16_t* src0, const uint16_t* src1, int64_t ld,
-                                       int64_t k_total, int nv0, int nv1) {
-    const int w = wave_id(), lane = threadIdx.x & 63, region = w >> 1;
-    rs = make_dma_rsrc(region ? src1 : src0, k_total * ld * 2);
-    ld2 = (uint32_t)(ld * 2);
-    const int k = 32 * (w & 1) + (lane >> 3);          // load i adds 8 i rows
-    const int col = 8 * ((lane & 7) ^ (4 * ((k >> 1) & 1)));
-    voff = col < (region ? nv1 : nv0) ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
-    wlds = (uint32_t)(w * 4 * 1024);
-  }
-  __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
-    const uint32_t ko = valid ? (uint32_t)(k0 * ld2) : kOob;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_lds(rs, tile + wlds + i * 1024, voff + (ko + (uint32_t)(8 * i) * ld2));
-  }
-  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
-    const int lane = threadIdx.x & 63, q = lane & 15, g = (lane >> 4) & 1;
-    const lds_t* region = tile + (nb >> 6) * 8192;
-    const int col = (nb & 63) + 16 * g + 4 * (q & 3);
-    i16x4 h[2];
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int k = 16 * kk + 8 * lh + 4 * hh + (q >> 2);
-      const int off = k * 128 + (((col >> 3) ^ (4 * ((k >> 1) & 1))) << 4) + (col & 7) * 2;
-      h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) i16x4*)(region + off));
-    }
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-  }
-};
+// of one matrix): 64 k rows of 128 B each, whole cache lines.
+typedef ColTileT<64, 2> ColTile64;
 template <class T> struct TileBytes;
 template <int NL> struct TileBytes<RowTileT<NL>> { static constexpr int value = NL * 4096; };
 template <int NL> struct TileBytes<RowTile2<NL>> { static constexpr int value = NL * 4096; };
@@ -589,35 +551,7 @@ struct Four {
   };
 };
 
-// gemm_core.h's column tile loaded by eight waves.
-struct ColTile8 {
-  static constexpr bool kRows = false;
-  static constexpr int kLoads = 4;
-  DmaRsrc rs;           // waves 0..3: region 0; waves 4..7: region 1
-  uint32_t voff, ld2, wlds;
-  __device__ __forceinline__ void init(const uint16_t* src0, const uint16_t* src1, int64_t ld,
-                                       int64_t k_total, int nv0, int nv1) {
-    const int w = wave_id(), lane = threadIdx.x & 63, region = w >> 2;
-    rs = make_dma_rsrc(region ? src1 : src0, k_total * ld * 2);
-    ld2 = (uint32_t)(ld * 2);
-    const int k = 16 * (w & 3) + (lane >> 4);        // load i adds 4 i rows
-    const int col = 8 * ((lane & 15) ^ (4 * (k & 3)));
-    voff = col < (region ? nv1 : nv0) ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
-    wlds = (uint32_t)(w * 4 * 1024);
-  }
-  __device__ __forceinline__ uint32_t koff(int64_t k0) const { return (uint32_t)(k0 * ld2); }
-  __device__ __forceinline__ void issue1(lds_t* tile, int i, uint32_t ko) const {
-    load_lds(rs, tile + wlds + i * 1024, voff + (ko + (uint32_t)(4 * i) * ld2));
-  }
-  __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
-    const uint32_t ko = valid ? koff(k0) : kOob;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) issue1(tile, i, ko);
-  }
-  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
-    return ColTile::frag(tile, nb, kk, lh);
-  }
-};
+typedef ColTileT<128, 4> ColTile8;     // gemm_core.h's column tile loaded by eight waves
 struct Eight {
   static constexpr int kWaves = 8, NJ = 2;
   template <int MI> struct Tiles {
@@ -1170,33 +1104,7 @@ MOONEP_LARGE_128(large_grad_splits, large_grad_tile, true)
 
 // dW of the three projections, the sum over the tokens: tiles of 256 columns of
 // H' and 256 rows of H by four waves, or 128 by eight.
-struct ColTileA8 {       // 128 columns loaded by eight waves, laid out as a region of ColTile
-  static constexpr bool kRows = false;
-  static constexpr int kLoads = 2;
-  DmaRsrc rs;
-  uint32_t voff, ld2, wlds;
-  __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t k_total, int nv) {
-    const int w = wave_id(), lane = threadIdx.x & 63;
-    rs = make_dma_rsrc(src, k_total * ld * 2);
-    ld2 = (uint32_t)(ld * 2);
-    const int k = 8 * w + (lane >> 4);               // load i adds 4 i rows
-    const int col = 8 * ((lane & 15) ^ (4 * (k & 3)));
-    voff = col < nv ? (uint32_t)(k * ld * 2 + col * 2) : kOob;
-    wlds = (uint32_t)(w * 2 * 1024);
-  }
-  __device__ __forceinline__ uint32_t koff(int64_t k0) const { return (uint32_t)(k0 * ld2); }
-  __device__ __forceinline__ void issue1(lds_t* tile, int i, uint32_t ko) const {
-    load_lds(rs, tile + wlds + i * 1024, voff + (ko + (uint32_t)(4 * i) * ld2));
-  }
-  __device__ __forceinline__ void issue(lds_t* tile, int64_t k0, bool valid) const {
-    const uint32_t ko = valid ? koff(k0) : kOob;
-    issue1(tile, 0, ko);
-    issue1(tile, 1, ko);
-  }
-  __device__ __forceinline__ static bf16x8 frag(const lds_t* tile, int nb, int kk, int lh) {
-    return ColTile::frag(tile, nb, kk, lh);
-  }
-};
+typedef ColTileT<128, 8> ColTileA8;    // one region loaded by eight waves
 
 // F32: added to fp32 (both ends in one kernel would keep the sums twice, and spill).
 template <class G, int MI, bool PART, bool F32>
