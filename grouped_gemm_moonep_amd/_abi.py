@@ -82,6 +82,7 @@ def lib():
         "moonep_shared_ffn_ws": (i64, [i64, i32, i32]),
         "moonep_shared_ffn": (i32, [vp, P3, i32, vp, i64, i32, i32, vp, vp, i64, vp]),
         "moonep_shared_ffn_tile": (i32, [i64, i32, i32, i32, ctypes.POINTER(i32)]),
+        "moonep_shared_ffn_last_tile": (i32, [i64, i32, i32]),
         "moonep_shared_ffn_bwd_ws": (i64, [i64, i32, i32]),
         "moonep_shared_ffn_bwd": (i32, [vp, vp, P3, i32, i64, i32, i32, vp, ctypes.POINTER(vp), i32,
                                         vp, i64, vp]),
@@ -169,6 +170,11 @@ def shared_ffn_tile(T: int, H: int, Hp: int, product: int):
     """(tile, splits) of a product of the shared expert (host only)."""
     splits = ctypes.c_int32()
     return int(lib().moonep_shared_ffn_tile(T, H, Hp, product, ctypes.byref(splits))), splits.value
+
+
+def shared_ffn_last_tile(T: int, H: int, Hp: int):
+    """Tile of dX and the weight gradients of the shared expert in one launch, or -1 (host only)."""
+    return int(lib().moonep_shared_ffn_last_tile(T, H, Hp))
 
 
 def ptr3(ts):

@@ -402,6 +402,10 @@ int32_t moonep_shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product
   return shared_ffn_tile(T, H, Hp, product, splits);
 }
 
+int32_t moonep_shared_ffn_last_tile(int64_t T, int32_t H, int32_t Hp) {
+  return T >= 1 && shared_ffn_bwd_shape_ok(T, H, Hp) ? shared_ffn_last_tile(T, H, Hp) : -1;
+}
+
 int64_t moonep_shared_ffn_bwd_ws(int64_t T, int32_t H, int32_t Hp) {
   return shared_ffn_bwd_shape_ok(T, H, Hp) ? shared_ffn_bwd_ws_bytes(T, H, Hp) : -1;
 }

@@ -190,6 +190,7 @@ bool shared_ffn_bwd_shape_ok(int64_t T, int32_t H, int32_t Hp);
 int64_t shared_ffn_ws_bytes(int64_t T, int32_t H, int32_t Hp);
 int64_t shared_ffn_bwd_ws_bytes(int64_t T, int32_t H, int32_t Hp);
 int32_t shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product, int32_t* splits);
+int32_t shared_ffn_last_tile(int64_t T, int32_t H, int32_t Hp);
 hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,
                              const uint16_t* add, int64_t T, int32_t H, int32_t Hp, uint16_t* y,
                              char* ws, hipStream_t s);

@@ -1379,6 +1379,20 @@ SmallArgs with_shape(SmallArgs a, const Shape& s) {
 // One workgroup per CU at most: deep rings.
 bool deep(const Shape& s) { return (int64_t)s.ntm * s.ntn * s.S <= 256; }
 
+// Whether dX and the weight gradients, asked for together, are one launch, and whether its small
+// tiles' rings are deep: by the workgroups of both.
+bool joined(const Shape& x, const Shape& w) {
+  return x.S == 1 && w.S == 1 && x.large == w.large && (!x.large || x.rows == w.rows);
+}
+bool joined_deep(const Shape& x, const Shape& w) { return blocks_of(x) + blocks_of(w) <= 256; }
+
+int32_t tile_of(const Shape& s, bool deep_rings) {
+  if (s.large) return s.rows == 256 ? MOONEP_FFN_TILE_256X256 : MOONEP_FFN_TILE_128X256;
+  const int32_t t = s.rows == 32 ? MOONEP_FFN_TILE_32 : s.rows == 64 ? MOONEP_FFN_TILE_64
+                                                                     : MOONEP_FFN_TILE_128;
+  return t + (deep_rings ? MOONEP_FFN_TILE_DEEP : 0);
+}
+
 template <int OP, int BM, bool PART>
 void run_small_as(const Shape& s, const SmallArgs& a, hipStream_t st) {
   if (deep(s)) small_kernel<OP, BM, PART, true><<<blocks_of(s), kThreads, 0, st>>>(a);
@@ -1406,8 +1420,10 @@ void run_small(const Shape& s, bool part, const SmallArgs& in, hipStream_t st) {
 }
 
 template <int BM>
-void run_last(unsigned n, const SmallArgs& x, const SmallArgs& w, unsigned nx, hipStream_t st) {
-  if (n <= 256) small_last<BM, true><<<n, kThreads, 0, st>>>(x, w, nx);
+void run_last(const Shape& xs, const Shape& ws, const SmallArgs& x, const SmallArgs& w,
+              hipStream_t st) {
+  const unsigned nx = blocks_of(xs), n = nx + blocks_of(ws);
+  if (joined_deep(xs, ws)) small_last<BM, true><<<n, kThreads, 0, st>>>(x, w, nx);
   else small_last<BM, false><<<n, kThreads, 0, st>>>(x, w, nx);
 }
 
@@ -1461,10 +1477,12 @@ int32_t shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product, int32
     *splits = 1;
     return MOONEP_FFN_TILE_FEW;
   }
-  if (s.large) return s.rows == 256 ? MOONEP_FFN_TILE_256X256 : MOONEP_FFN_TILE_128X256;
-  const int32_t t = s.rows == 32 ? MOONEP_FFN_TILE_32 : s.rows == 64 ? MOONEP_FFN_TILE_64
-                                                                     : MOONEP_FFN_TILE_128;
-  return t + (deep(s) ? MOONEP_FFN_TILE_DEEP : 0);
+  return tile_of(s, deep(s));
+}
+
+int32_t shared_ffn_last_tile(int64_t T, int32_t H, int32_t Hp) {
+  const Shape x = dx_shape(T, H, Hp), w = wgrad_shape(T, H, Hp);
+  return joined(x, w) ? tile_of(x, joined_deep(x, w)) : -1;
 }
 
 hipError_t launch_shared_ffn(const uint16_t* x, const uint16_t* const w[3], int32_t act,
@@ -1560,15 +1578,15 @@ hipError_t launch_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
   wa.part = part; wa.M = H; wa.N = Hp; wa.K = (int)T; wa.f32 = big.f32;
   JoinW j;
   for (int i = 0; i < 3; ++i) wa.out[i] = j.out[i] = big.dw[i];
-  if (dx && dw && !dxs.large && dxs.S == 1 && !ws_.large && ws_.S == 1) {
+  const bool one = dx && dw && joined(dxs, ws_);
+  if (one && !dxs.large) {
     const SmallArgs ax = with_shape(xa, dxs), aw = with_shape(wa, ws_);
-    const unsigned nx = blocks_of(dxs), n = nx + blocks_of(ws_);
-    if (dxs.rows == 128) run_last<128>(n, ax, aw, nx, s);
-    else if (dxs.rows == 64) run_last<64>(n, ax, aw, nx, s);
-    else run_last<32>(n, ax, aw, nx, s);
+    if (dxs.rows == 128) run_last<128>(dxs, ws_, ax, aw, s);
+    else if (dxs.rows == 64) run_last<64>(dxs, ws_, ax, aw, s);
+    else run_last<32>(dxs, ws_, ax, aw, s);
     return hipGetLastError();
   }
-  if (dx && dw && dxs.large && ws_.large && dxs.S == 1 && ws_.S == 1 && dxs.rows == ws_.rows) {
+  if (one) {
     const LargeArgs ax = with_shape(big, dxs), aw = with_shape(big, ws_);
     const unsigned nw = (unsigned)(ceil_div(3LL * ws_.ntm * ws_.ntn, kXcds) * kXcds);
     const unsigned n = nw + blocks_of(dxs);

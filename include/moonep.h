@@ -457,10 +457,10 @@ moonep_status_t moonep_shared_ffn_bwd(const uint16_t* x, const uint16_t* dy,
 
 /* Tile (MOONEP_FFN_TILE_*) that a product (MOONEP_FFN_*) of T >= 1 tokens is
  * computed in, and into how many splits its sums are cut (host only): GATEUP and
- * DOWN of the forward; of the backward GRAD (G, U and dZ), DX and WGRAD.  The
- * small tiles are 32, 64 or 128 rows by 128 columns, plus MOONEP_FFN_TILE_DEEP
- * where their loads run further ahead.  -1 for sizes or a product that there is
- * not, or a NULL splits. */
+ * DOWN of the forward; of the backward GRAD (G, U and dZ), DX and WGRAD, each
+ * launched by itself.  The small tiles are 32, 64 or 128 rows by 128 columns, plus
+ * MOONEP_FFN_TILE_DEEP where their loads run further ahead.  -1 for sizes or a
+ * product that there is not, or a NULL splits. */
 enum {
   MOONEP_FFN_GATEUP = 0, MOONEP_FFN_DOWN, MOONEP_FFN_GRAD, MOONEP_FFN_DX, MOONEP_FFN_WGRAD
 };
@@ -471,6 +471,13 @@ enum {
   MOONEP_FFN_TILE_DEEP = 8
 };
 int32_t moonep_shared_ffn_tile(int64_t T, int32_t H, int32_t Hp, int32_t product, int32_t* splits);
+
+/* Tile that dX is computed in where the backward, asked for dx and dw, takes dX and
+ * the weight gradients in one launch without splits (host only); the weight
+ * gradients' is then MOONEP_FFN_TILE_128 with the same depth beside a small tile,
+ * the same one beside a large.  -1 where they are launched one after the other, in
+ * the tiles of DX and WGRAD, and for sizes that there are not. */
+int32_t moonep_shared_ffn_last_tile(int64_t T, int32_t H, int32_t Hp);
 
 /* A block's end and the next one's start in one pass (the framework-side steps
  * between combine and the next block): for T rows of W elements, with

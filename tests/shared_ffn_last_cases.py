@@ -1,0 +1,11 @@
+"""Sizes that between them take every tile and ring depth of the launch that computes dX and the weight
+gradients of the shared expert together; the host test checks that they do, the GPU test runs them."""
+from grouped_gemm_moonep_amd import _abi
+
+DEEP = _abi.FFN_TILE_DEEP
+# (T, H, H'): tile of dX
+LAST = {
+    (1, 64, 64): _abi.FFN_TILE_32 + DEEP, (36, 64, 64): _abi.FFN_TILE_64 + DEEP,
+    (79, 64, 64): _abi.FFN_TILE_128 + DEEP, (1, 5312, 192): _abi.FFN_TILE_32,
+    (35, 3200, 320): _abi.FFN_TILE_64, (148, 6464, 64): _abi.FFN_TILE_128,
+}
