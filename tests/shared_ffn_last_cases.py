@@ -8,4 +8,7 @@ LAST = {
     (1, 64, 64): _abi.FFN_TILE_32 + DEEP, (36, 64, 64): _abi.FFN_TILE_64 + DEEP,
     (79, 64, 64): _abi.FFN_TILE_128 + DEEP, (1, 5312, 192): _abi.FFN_TILE_32,
     (35, 3200, 320): _abi.FFN_TILE_64, (148, 6464, 64): _abi.FFN_TILE_128,
+    (132, 25088, 64): _abi.FFN_TILE_128X256,
+    (407, 16448, 320): _abi.FFN_TILE_256X256,          # last rows of dX: 151 in a whole tile,
+    (778, 9408, 320): _abi.FFN_TILE_256X256,           # 10 in a half one
 }

@@ -55,10 +55,11 @@ def test_agrees_with_the_products():
                 assert (last >= DEEP) == (blocks(*size, last) <= 256), size
 
 
-def test_cases_take_every_small_tile():
-    for size in sizes(40000):
-        last = _abi.shared_ffn_last_tile(*size)
-        assert last % DEEP > _abi.FFN_TILE_128 or last in LAST.values() or last < 0, size
+def test_cases_take_every_form():
+    """The sizes that the GPU test runs cover what any size takes, the training microbatch among them."""
+    seen = {_abi.shared_ffn_last_tile(*size) for size in sizes(40000)}
+    seen.add(_abi.shared_ffn_last_tile(32768, 7168, 2048))
+    assert seen - {-1} == set(LAST.values())
 
 
 def test_sizes_that_there_are_not():
