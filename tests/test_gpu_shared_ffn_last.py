@@ -1,11 +1,12 @@
 """shared_ffn_bwd at sizes that take every form of the launch that computes dX
 and the weight gradients together, against the oracle (the checks and bounds of
-test_gpu_shared_ffn), the weight gradients written and added to."""
+test_gpu_shared_ffn), the weight gradients written and added to; and of the
+weight gradients' own launch, added to gradients that are not zero."""
 import pytest
 import torch
 
 from grouped_gemm_moonep_amd import shared_ffn_bwd
-from shared_ffn_last_cases import LAST
+from shared_ffn_last_cases import ALONE, LAST
 from test_gpu_shared_ffn import check, draw
 
 pytestmark = pytest.mark.gpu
@@ -15,6 +16,11 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("T,H,Hp", list(LAST))
 def test_one_launch(T, H, Hp, f32):
     check(T, H, Hp, act="gelu_tanh" if T % 2 else "silu", f32=f32, forward=False, seed=T)
+
+
+@pytest.mark.parametrize("T,H,Hp", list(ALONE))
+def test_adding_in_every_tile(T, H, Hp):
+    check(T, H, Hp, f32=True, forward=False, seed=T)
 
 
 @pytest.mark.parametrize("T,H,Hp", list(LAST))

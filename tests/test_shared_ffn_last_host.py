@@ -6,7 +6,7 @@ import random
 import pytest
 
 from grouped_gemm_moonep_amd import _abi
-from shared_ffn_last_cases import DEEP, LAST
+from shared_ffn_last_cases import ALONE, DEEP, LAST
 
 
 def blocks(T, H, Hp, tile):
@@ -60,6 +60,15 @@ def test_cases_take_every_form():
     seen = {_abi.shared_ffn_last_tile(*size) for size in sizes(40000)}
     seen.add(_abi.shared_ffn_last_tile(32768, 7168, 2048))
     assert seen - {-1} == set(LAST.values())
+
+
+def test_cases_take_every_launch_of_the_weight_gradients():
+    def alone(*size):
+        tile, splits = _abi.shared_ffn_tile(*size, _abi.FFN_WGRAD)
+        return (tile, splits > 1) if _abi.shared_ffn_last_tile(*size) < 0 else None
+
+    assert {size: alone(*size) for size in ALONE} == ALONE
+    assert {alone(*size) for size in sizes(40000)} - {None} == set(ALONE.values())
 
 
 def test_sizes_that_there_are_not():
