@@ -356,8 +356,9 @@ __device__ __forceinline__ void put_share(const S& s, const Place<kWave>& at, in
 // Sums over tokens stay with a lane, for its columns, over all rows of its
 // wave or workgroup; each workgroup then writes its share to part [3][shares][W]
 // and norm_bwd_sum adds the shares, in an order that T and W fix.  With four
-// vectors a lane two of the three sums lie in LDS (8192 rows of 16384 in bf16 447
-// us; two vectors in 1024 lanes, whose 128 registers spill, 1394 us).  Up to 8192
+// vectors a lane two of the three sums lie in LDS (8192 rows of 16384 in bf16 with
+// two outputs 443 us, 4.2 TB/s; two vectors in 1024 lanes, whose 128 registers
+// spill, 1394 us).  Up to 8192
 // elements registers hold all (32768 rows of 7168 707 us, in LDS 742 us).
 template <class TS, int VPT, bool kWave, int kMost>
 __global__ __launch_bounds__(kMost) void norm_bwd_kernel(NormBwdArgs a) {
@@ -495,8 +496,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum(const float* part, int shar
 // Workgroups of a launch and the lanes of each: up to 1024 elements a wave, up to 4096 a workgroup
 // with a vector a lane, beyond two, in the backward past 8192 four.  Workgroups per CU: as many as
 // have `waves` waves, one at least.
-// Forward: a row a workgroup nearly always (32768 rows of 7168 in bf16: 448 us, with nine workgroups
-// per CU 485 us; the next row's loads ahead of a row's sums 480 to 490 us).  Backward: as few
+// Forward: many more than run at once, so that a workgroup has few rows: of 7168 elements up to 18688
+// workgroups, of 16384 up to 8192 (32768 rows of 7168 in bf16, one or two each: 448 us, with nine
+// workgroups per CU 485 us; the next row's loads ahead of a row's sums 480 to 490 us).  Backward: as few
 // workgroups as keep the CUs busy, for each leaves a share of the sums over tokens (702 us with one
 // per CU, 728 us with three; 16384 rows of 4096 208 us with two per CU, 235 us with one).
 struct NormGrid {

@@ -22,7 +22,8 @@
 // still stream the weights through every CU; the splits' sums go to the workspace
 // in fp32 and an elementwise kernel adds them in order (no atomics: results
 // repeat) and finishes.  Bound by the matrix units at the power limit with many
-// tokens (32768 of 7168 x 2048: 2.27 ms, 1270 TFLOP/s; backward 5.95 ms, 1290), by
+// tokens (32768 of 7168 x 2048: 2.25 to 2.31 ms from card to card, 1250 to 1280
+// TFLOP/s; backward 5.95 to 6.09 ms, 1260 to 1290), by
 // the delivery of tiles to the CUs with a few hundred (1024: 108 us), by the
 // weights' bytes with few (8: 24 us, of which the two products 20 us at 4.4 TB/s).
 #include "gemm_core.h"
@@ -51,8 +52,8 @@ __device__ __forceinline__ Act activate(float g) {
     c = k * t * (1.0f + 0.044715f * t * t);
     dc = k * (1.0f + 3 * 0.044715f * t * t);
   }
-  // the hardware's reciprocal and exponential: about 1e-7, far below the
-  // rounding to bf16 that follows
+  // the hardware's reciprocal and exponential: off by about (1 + |c|) 1e-7, far
+  // below the rounding to bf16 that follows; 0 below c of -87, where f(g) is below 1e-35
   const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-c));
   // s first: where it is 0, g dc may be past fp32
   const float f = g * s;
@@ -926,6 +927,7 @@ __device__ __forceinline__ void large_down_tile(const LargeArgs& a, const Ring& 
 template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
+  static_assert(!PART, "K is not cut");
   const Waves<G, MI> at;
   const int n0 = t.nt * BN, cols = a.Hp - n0 < BN ? a.Hp - n0 : BN;
   const int nv0 = cols < 128 ? cols : 128;
@@ -949,6 +951,7 @@ __device__ __forceinline__ void large_dz_tile(const LargeArgs& a, const Ring& sm
 template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_gu_tile(const LargeArgs& a, const Ring& smem,
                                               const LargeTile& t) {
+  static_assert(!PART, "K is not cut");
   typedef Waves<G, MI> Wv;
   constexpr int kHalf = Wv::kHalf;
   const Wv wv;
@@ -1066,6 +1069,7 @@ __device__ __forceinline__ void large_dx_tile(const LargeArgs& a, const Ring& sm
 template <class G, int MI, bool PART>
 __device__ __forceinline__ void large_grad_tile(const LargeArgs& a, const Ring& smem,
                                                 const LargeTile& t) {
+  static_assert(PART, "K is always cut");
   const Waves<G, MI> wv;
   const int gu = (a.Hp + 127) / 128;
   const bool dz = t.nt >= gu;
